@@ -14,8 +14,10 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libcachegen.so")
-SOURCES = ["cg_api.cu", "cg_fit.cu", "cg_encode.cu", "cg_decode.cu", "cg_noalloc.cu", "cg_plan.cu", "cg_assemble.cu"]
-HEADERS = ["cg_layout.cuh", "cg_kernels.cuh", "cg_args.h"]
+SOURCES = ["cg_api.cu", "cg_fit.cu", "cg_encode.cu", "cg_decode.cu", "cg_noalloc.cu", "cg_plan.cu", "cg_assemble.cu",
+           "cg_cache_write.cu", "cg_cache_attend.cu", "cg_prompt.cu", "cg_pages.cu"]
+HEADERS = ["cg_layout.cuh", "cg_kernels.cuh", "cg_args.h", "cg_cache.cuh"]
+ABI = ["cachegen.h", "cachegen_cache.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -30,7 +32,7 @@ def _stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(ROOT, "include", "cachegen.h")]
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(ROOT, "include", f) for f in ABI]
     return any(os.path.getmtime(p) > t for p in deps)
 
 

@@ -1,4 +1,4 @@
-"""ctypes binding of libcachegen.so (include/cachegen.h), same names as the C ABI.
+"""ctypes binding of libcachegen.so (include/cachegen.h and cachegen_cache.h), same names as the C ABI.
 
 Argument marshalling only: every step of fit, encode and decode runs in the
 library's CUDA kernels.  Device buffers are torch tensors (their data_ptr()
@@ -27,6 +27,34 @@ class cg_dims(ctypes.Structure):
 class cg_params(ctypes.Structure):
     _fields_ = [("n_levels", ctypes.c_int32), ("level_base", ctypes.c_float * 8),
                 ("layer_mult", ctypes.c_void_p), ("alphabet_radius", ctypes.c_int32)]
+
+
+CG_CACHE_F16, CG_CACHE_E4M3, CG_CACHE_INT8 = 0, 1, 2
+CG_F16, CG_BF16 = 0, 1
+
+
+class cg_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("L", "H", "d", "block_tokens", "n_blocks", "format")]
+
+
+class cg_rows(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_seq", "n_rows", "max_new", "dtype", "table_stride", "reserved")] + \
+        [("stride_token", ctypes.c_int64), ("stride_head", ctypes.c_int64)]
+
+
+class cg_attend(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_seq", "q_tokens", "Hq", "dtype", "table_stride")] + \
+        [("scale", ctypes.c_float), ("q_stride", ctypes.c_int64 * 3)]
+
+
+class cg_prompt(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_seq", "Hq", "H", "d", "dtype", "max_q", "max_k", "n_q", "n_k")] + \
+        [("scale", ctypes.c_float)] + [(n, ctypes.c_int64 * 2) for n in ("q_stride", "k_stride", "v_stride")]
+
+
+class cg_pages(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("table_stride", ctypes.c_int32), ("refs_dev", ctypes.c_void_p),
+                ("table_dev", ctypes.c_void_p), ("len_dev", ctypes.c_void_p)]
 
 
 class CacheGenError(RuntimeError):
@@ -72,6 +100,17 @@ def lib() -> ctypes.CDLL:
                                                 ctypes.c_int32, ctypes.c_int32, P, P, S, P]),
             "cg_decode_paged": (ctypes.c_int, [D, Pr, P, P, ctypes.c_uint64, ctypes.c_int32, ctypes.c_int32,
                                                P, P, ctypes.c_int32, ctypes.c_int32, P, S, P]),
+            "cg_cache_write": (ctypes.c_int, [P] * 12 + [S, P]),
+            "cg_cache_workspace_bytes": (S, [P, P]),
+            "cg_cache_attend": (ctypes.c_int, [P] * 12 + [S, P]),
+            "cg_prompt_workspace_bytes": (S, [P]),
+            "cg_prompt_attend": (ctypes.c_int, [P] * 9 + [S, P]),
+            "cg_pages_workspace_bytes": (S, [P, P, ctypes.c_int32]),
+            "cg_pages_extend": (ctypes.c_int, [P, P, ctypes.c_int32, P, P, P, S, P]),
+            "cg_pages_fork": (ctypes.c_int, [P, P, P, P, ctypes.c_int32, P, P, P, S, P]),
+            "cg_pages_free": (ctypes.c_int, [P, P, ctypes.c_int32, P, P, S, P]),
+            "cg_pages_copy": (ctypes.c_int, [P, P, P, ctypes.c_int32, P, P, P, S, P]),
+            "cg_pages_compact": (ctypes.c_int, [P, P, P, P, P, P, P, P, S, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -114,6 +153,59 @@ class Config:
                   layer_mult=w.layer_mult_array())
         kw.update(over)
         return cls(**kw)
+
+
+class Cache:
+    """A paged cache: 2*L pools of n_blocks pages [H][block_tokens][d], fp16 or 8-bit codes (CG_CACHE_*)."""
+
+    def __init__(self, L, H, d, block_tokens, n_blocks, format=CG_CACHE_E4M3):
+        self.c = cg_cache(L, H, d, block_tokens, n_blocks, format)
+        self.ref = ctypes.addressof(self.c)
+
+
+class Rows:
+    """New keys and values of cg_cache_write: n_rows rows, at most max_new of a sequence; strides in elements."""
+
+    def __init__(self, n_seq, n_rows, max_new, dtype, table_stride, stride_token, stride_head):
+        self.c = cg_rows(n_seq, n_rows, max_new, dtype, table_stride, 0, stride_token, stride_head)
+        self.ref = ctypes.addressof(self.c)
+
+
+class Attend:
+    """A cg_cache_attend call's shape; q_stride (sequence, token, head) in elements, None where q is contiguous and
+    heads have head_dim elements (filled in from the cache by the call)."""
+
+    def __init__(self, n_seq, q_tokens, Hq, dtype, table_stride, scale, q_stride=None):
+        self.contiguous = q_stride is None
+        self.c = cg_attend(n_seq, q_tokens, Hq, dtype, table_stride, scale,
+                           (ctypes.c_int64 * 3)(*([0, 0, 0] if q_stride is None else q_stride)))
+        self.ref = ctypes.addressof(self.c)
+
+    def for_cache(self, cache):
+        if self.contiguous:
+            d, hq = cache.c.d, self.c.Hq
+            self.c.q_stride[:] = [self.c.q_tokens * hq * d, hq * d, d]
+        return self.ref
+
+
+class Prompt:
+    """A cg_prompt_attend call's shape; strides (row, head) in elements."""
+
+    def __init__(self, n_seq, Hq, H, d, dtype, n_q, n_k, max_q, max_k, scale, q_stride, k_stride, v_stride):
+        two = ctypes.c_int64 * 2
+        self.c = cg_prompt(n_seq, Hq, H, d, dtype, max_q, max_k, n_q, n_k, scale, two(*q_stride), two(*k_stride),
+                           two(*v_stride))
+        self.ref = ctypes.addressof(self.c)
+
+
+class Pages:
+    """The bookkeeping of a paged cache: device int32 tensors refs [n_blocks], table [n_seqs, table_stride] and
+    lens [n_seqs], kept for as long as this object."""
+
+    def __init__(self, refs, table, lens):
+        self.tensors = (refs, table, lens)
+        self.c = cg_pages(table.shape[0], table.shape[1], _ptr(refs), _ptr(table), _ptr(lens))
+        self.ref = ctypes.addressof(self.c)
 
 
 # ---- the C ABI, one function each -----------------------------------------
@@ -256,6 +348,73 @@ def cg_entropy_bound(cfg: Config, ws_fit, level: int = 0) -> float:
     check(lib().cg_entropy_bound(ctypes.byref(cfg.dims), ctypes.byref(cfg.params), _ptr(ws_fit), int(level),
                                  ctypes.byref(out)), "cg_entropy_bound")
     return out.value
+
+
+# ---- serving a decoded context (include/cachegen_cache.h) -------------------
+def _bytes(ws) -> int:
+    return ws.numel() * ws.element_size()
+
+
+def cg_cache_write(cache: Cache, rows: Rows, k, v, cu_new, start, table, k_pool, v_pool, k_scale, v_scale, ws,
+                   stream=None) -> int:
+    return lib().cg_cache_write(cache.ref, rows.ref, _ptr(k), _ptr(v), _ptr(cu_new), _ptr(start), _ptr(table),
+                                _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(ws), _bytes(ws),
+                                _stream(stream))
+
+
+def cg_cache_workspace_bytes(cache: Cache, attend: Attend) -> int:
+    return lib().cg_cache_workspace_bytes(cache.ref, attend.for_cache(cache))
+
+
+def cg_cache_attend(cache: Cache, attend: Attend, q, k_pool, v_pool, k_scale, v_scale, table, lens, out, lse, ws,
+                    stream=None) -> int:
+    """lse may be None."""
+    return lib().cg_cache_attend(cache.ref, attend.for_cache(cache), _ptr(q), _ptr(k_pool), _ptr(v_pool),
+                                 _ptr(k_scale), _ptr(v_scale), _ptr(table), _ptr(lens), _ptr(out), _ptr(lse),
+                                 _ptr(ws), _bytes(ws), _stream(stream))
+
+
+def cg_prompt_workspace_bytes(prompt: Prompt) -> int:
+    return lib().cg_prompt_workspace_bytes(prompt.ref)
+
+
+def cg_prompt_attend(prompt: Prompt, q, k, v, cu_q, cu_k, out, lse, ws, stream=None) -> int:
+    """lse may be None."""
+    return lib().cg_prompt_attend(prompt.ref, _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), _ptr(out), _ptr(lse),
+                                  _ptr(ws), _bytes(ws), _stream(stream))
+
+
+def cg_pages_workspace_bytes(cache: Cache, pages: Pages | None, n: int) -> int:
+    return lib().cg_pages_workspace_bytes(cache.ref, None if pages is None else pages.ref, int(n))
+
+
+def cg_pages_extend(cache: Cache, pages: Pages, seqs, new_len, ws, stream=None) -> int:
+    return lib().cg_pages_extend(cache.ref, pages.ref, seqs.numel(), _ptr(seqs), _ptr(new_len), _ptr(ws), _bytes(ws),
+                                 _stream(stream))
+
+
+def cg_pages_fork(cache: Cache, pages: Pages, pools, scales, parents, children, ws, stream=None) -> int:
+    """pools and scales: device int64 tensors of the 2*L addresses (scales None for fp16 pages)."""
+    if parents.numel() != children.numel():
+        return CG_ERR_INVALID_ARG
+    return lib().cg_pages_fork(cache.ref, pages.ref, _ptr(pools), _ptr(scales), parents.numel(), _ptr(parents),
+                               _ptr(children), _ptr(ws), _bytes(ws), _stream(stream))
+
+
+def cg_pages_free(cache: Cache, pages: Pages, seqs, ws, stream=None) -> int:
+    return lib().cg_pages_free(cache.ref, pages.ref, seqs.numel(), _ptr(seqs), _ptr(ws), _bytes(ws), _stream(stream))
+
+
+def cg_pages_copy(cache: Cache, pools, scales, src, dst, ws, stream=None) -> int:
+    if src.numel() != dst.numel():
+        return CG_ERR_INVALID_ARG
+    return lib().cg_pages_copy(cache.ref, _ptr(pools), _ptr(scales), src.numel(), _ptr(src), _ptr(dst), _ptr(ws),
+                               _bytes(ws), _stream(stream))
+
+
+def cg_pages_compact(cache: Cache, pages: Pages, pools, scales, refs_out, table_out, n_live, ws, stream=None) -> int:
+    return lib().cg_pages_compact(cache.ref, pages.ref, _ptr(pools), _ptr(scales), _ptr(refs_out), _ptr(table_out),
+                                  _ptr(n_live), _ptr(ws), _bytes(ws), _stream(stream))
 
 
 def cg_read_status(ws) -> int:
