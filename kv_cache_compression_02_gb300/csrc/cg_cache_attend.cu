@@ -1,10 +1,47 @@
 // cg_cache_attend.cu -- cg_cache_attend: new tokens attend over 8-bit pages.
+//
+// For one KV head of one sequence the G = Hq / H query heads of the T new
+// tokens are T * G rows that read the same keys and values, so they are rows
+// of one matrix product.  Sixteen rows are a tile of mma.sync m16n8k16 (f16
+// operands, fp32 sums): codes of either format are exact in f16, page scales
+// are applied outside the products, on the scores (K) and on the
+// probabilities (V).
+//
+// What bounds it is the read of the codes: 2 d bytes per token and head
+// against 4 T G d operations, so the tensor cores of tcgen05, which take their
+// operands from shared memory in one format, would only add a pass that
+// converts codes there.  The codes go from shared memory to registers once,
+// each thread 16 bytes of a row at a time, and become the operands of
+// mma.sync as they are: both products leave the order of their summed index
+// free, so a thread takes 16 consecutive channels of a token (K) or of two
+// tokens (V) for the fragments of four or sixteen products.
+//
+// Work is cut into units of 64 positions of one (sequence, head, row tile),
+// and the units of the whole call are dealt in equal runs to as many CTAs as
+// fit on the GPU: a long context is shared by all SMs, short ones are packed.
+// A CTA that covers only a part of an item leaves its running maximum, sum
+// and output in the workspace; the last one of an item to finish joins the
+// parts in their order, so the result does not depend on timing.
 #include "cg_cache.cuh"
 
 namespace cg {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTok = 16;               // positions of a warp's tile
+constexpr int kUnit = kTok * kWarps;   // positions of a unit
+constexpr int kRows = 16;              // query rows of an item
+constexpr int kStages = 3;             // tiles in flight per warp
+constexpr int kPerSM = 3;              // CTAs
+constexpr int kGrid = kSMs * kPerSM;
+
+// A probability is held as p = 2^(s - m + kLift), and m may lag behind the
+// true maximum by kLag, so that p < 2^15.  For the second product it is
+// multiplied by its page's V scale over the largest so far and rounded to f16:
+// 11 bits from kNormal up.  Smaller ones, rare but for sharp distributions,
+// go through products of their own, raised by 2^28 each time.
+constexpr float kLift = 12.0f, kLag = 3.0f, kNormal = 0x1p-14f;
 
 struct AttendArgs {
   const uint16_t *q;
@@ -14,68 +51,656 @@ struct AttendArgs {
   uint16_t *out;
   float *lse;
   uint32_t *status;
+  int32_t *count;   // [items]: parts of an item that are in the workspace
+  float *parts;     // [2 * kGrid][kRows][D + 2]
   int64_t q_seq, q_tok, q_head;
-  int B, T, Hq, H, d, bt, n_blocks, stride;
+  int B, T, Hq, H, G, HR, d, bt, n_blocks, stride;  // HR: heads x row tiles
   float scale_log2;  // scale * log2(e)
 };
 
-// One CTA per output row; each warp takes every fourth position and keeps its
-// own running maximum, sum and output.
-template <int FMT, bool BF16>
-__global__ void __launch_bounds__(kThreads) k_attend(const AttendArgs a) {
-  const int b = blockIdx.x / a.T, t = blockIdx.x % a.T, hq = blockIdx.y, h = hq / (a.Hq / a.H);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int64_t len = a.len[b];
-  const int64_t most = int64_t(a.stride) * a.bt;
-  if (len < 0 || len > most) {
-    if (threadIdx.x == 0) atomicOr(a.status, kStBadArg);
-    len = len < 0 ? 0 : most;
+template <int D>
+struct Stage {
+  uint8_t k[kTok * D], v[kTok * D];
+  float ks[kTok], vs[kTok];
+};
+
+template <int D>
+struct Smem {
+  Stage<D> ring[kWarps][kStages];
+  float o[2][kRows * D];  // where warps hand their outputs over
+  float m[kWarps][kRows], l[kWarps][kRows];
+  uint32_t valid[kWarps][kStages];
+  int64_t sum[kThreads / 32], start, prefix;
+  int b, last;
+};
+
+// Where 16-byte chunk c of row r lies in a tile.  The reads are: K, chunks
+// 0-3 (or 4-7) of rows 2i, 2i+1 by eight lanes; V, the chunks 2i, 2i+1 of
+// four rows of one parity.  With this swizzle neither has a bank conflict.
+template <int D>
+__device__ inline int chunk_at(int r, int c) {
+  if (D == 128) return r * 128 + ((c ^ ((r & 6) ^ ((r & 1) << 2))) << 4);
+  return (r >> 1) * 128 + (((((r & 1) << 2) | c) ^ (r & 6)) << 4);
+}
+
+__device__ inline uint32_t smem_of(const void *p) { return uint32_t(__cvta_generic_to_shared(p)); }
+
+template <int N>
+__device__ inline void copy_async(uint32_t dst, const void *src, bool ok) {
+  const int n = ok ? N : 0;  // the rest is filled with zeros
+  if (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(n) : "memory");
+}
+
+__device__ inline void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ inline float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Codes in the low (H = 0) or high half of w -> two f16.
+template <int FMT, int H>
+__device__ inline uint32_t halves_of(uint32_t w) {
+  uint32_t r;
+  if (FMT == CG_CACHE_E4M3) {
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(uint16_t(H ? w >> 16 : w)));
+  } else {  // 0x64uu is 1024 + u; w holds code + 128
+    const __half2 x = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    uint32_t p = __byte_perm(w, 0x64646464u, H ? 0x4342 : 0x4140);
+    const __half2 y = __hsub2(*reinterpret_cast<__half2 *>(&p), x);
+    r = *reinterpret_cast<const uint32_t *>(&y);
   }
-  const int64_t seen = len - a.T + t + 1;
-  const uint16_t *q = a.q + b * a.q_seq + t * a.q_tok + hq * a.q_head;
-  float qf[4], o[4] = {0.0f, 0.0f, 0.0f, 0.0f}, m = -INFINITY, l = 0.0f;
+  return r;
+}
+
+template <int FMT>
+__device__ inline uint32_t biased(uint32_t w) {
+  return FMT == CG_CACHE_INT8 ? w ^ 0x80808080u : w;
+}
+
+__device__ inline uint32_t pack(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// A walk over the units of a call, from one item to the next.
+struct Walk {
+  int b, hr, tile, tiles;
+  int64_t len;
+};
+
+__device__ inline int64_t length(const AttendArgs &a, int b) {
+  const int64_t n = a.len[b], most = int64_t(a.stride) * a.bt;
+  return n < 0 ? 0 : n > most ? most : n;
+}
+
+__device__ inline void set_seq(const AttendArgs &a, Walk &w) {
+  w.len = length(a, w.b);
+  w.tiles = int((w.len + kUnit - 1) / kUnit);
+}
+
+// The next unit; the caller knows that there is one.
+__device__ inline void step(const AttendArgs &a, Walk &w) {
+  if (++w.tile < w.tiles) return;
+  w.tile = 0;
+  if (++w.hr < a.HR) return;
+  w.hr = 0;
+  do {
+    w.b++;
+    set_seq(a, w);
+  } while (w.tiles == 0);
+}
+
+// One row's outputs: lane t of a quad holds channels D/4 t .. D/4 t + D/4 - 1
+// of row g in o[j][0], o[j][1] and of row g + 8 in o[j][2], o[j][3].
+template <int D>
+__device__ inline float out_at(const float (&o)[D / 8][4], int half, int i) {
+  return o[i % (D / 8)][2 * half + i / (D / 8)];
+}
+
+// Channels c0 .. c0 + N - 1 of a finished row.
+template <bool BF16, int N>
+__device__ inline void write_row(const AttendArgs &a, int b, int h, int r, const float (&x)[N], int c0, float m,
+                                 float l, bool lead) {
+  const int t = r / a.G;
+  const int64_t row = (int64_t(b) * a.T + t) * a.Hq + h * a.G + r % a.G;
+  const float f = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-  for (int i = 0; i < 4; i++) qf[i] = 4 * lane + i < a.d ? elem<BF16>(q[4 * lane + i]) : 0.0f;
-  for (int64_t j = warp; j < seen; j += kThreads / 32) {
-    const int page = a.table[int64_t(b) * a.stride + j / a.bt];
-    if (uint32_t(page) >= uint32_t(a.n_blocks)) {
-      if (lane == 0) atomicOr(a.status, kStBadArg);
-      continue;
-    }
-    const int64_t row = page_row(page, a.H, h, a.bt, int(j % a.bt), a.d);
-    uint32_t kc = 0, vc = 0;
-    if (4 * lane < a.d) {
-      kc = *reinterpret_cast<const uint32_t *>(a.kp + row + 4 * lane);
-      vc = *reinterpret_cast<const uint32_t *>(a.vp + row + 4 * lane);
-    }
-    float s = 0.0f;
+  for (int i = 0; i < N; i += 8) {
+    if (c0 + i >= a.d) continue;
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; i++) s += qf[i] * value_of<FMT>((kc >> (8 * i)) & 0xffu);
-#pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= a.scale_log2 * a.ks[int64_t(page) * a.H + h];
-    const float top = fmaxf(m, s), keep = exp2f(m - top), p = exp2f(s - top), w = p * a.vs[int64_t(page) * a.H + h];
-    l = l * keep + p;
-#pragma unroll
-    for (int i = 0; i < 4; i++) o[i] = o[i] * keep + w * value_of<FMT>((vc >> (8 * i)) & 0xffu);
-    m = top;
+    for (int k = 0; k < 4; k++)
+      w[k] = uint32_t(elem_of<BF16>(x[i + 2 * k] * f)) | uint32_t(elem_of<BF16>(x[i + 2 * k + 1] * f)) << 16;
+    *reinterpret_cast<uint4 *>(a.out + row * a.d + c0 + i) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  __shared__ float s_m[4], s_l[4], s_o[4][128];
-  if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+  if (lead && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (m - kLift + log2f(l)) * 0.6931471805599453f;
+}
+
+template <int FMT, int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, kPerSM) k_attend(const AttendArgs a) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  Smem<D> &sm = *reinterpret_cast<Smem<D> *>(smem_raw);
+  constexpr int kNT = D / 8;       // output column tiles
+  constexpr int kChunks = D / 16;  // 16-byte chunks of a row
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+
+  // Sequences with nothing in them, and the units of the call.
+  const int per = (a.B + kThreads - 1) / kThreads, b0 = threadIdx.x * per, b1 = min(a.B, b0 + per);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; b++) {
+    const int n = a.len[b];
+    if (blockIdx.x == 0 && (n < 0 || int64_t(n) > int64_t(a.stride) * a.bt)) atomicOr(a.status, kStBadArg);
+    mine += (length(a, b) + kUnit - 1) / kUnit;
+  }
+  mine *= a.HR;
+  int64_t before = mine;
 #pragma unroll
-  for (int i = 0; i < 4; i++) s_o[warp][4 * lane + i] = o[i];
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += y;
+  }
+  if (lane == 31) sm.sum[warp] = before;
   __syncthreads();
-  float top = -INFINITY, sum = 0.0f, x = 0.0f;
-  for (int w = 0; w < 4; w++) top = fmaxf(top, s_m[w]);
-  if (seen > 0)
-    for (int w = 0; w < 4; w++) {
-      const float f = s_m[w] == -INFINITY ? 0.0f : exp2f(s_m[w] - top);
-      sum += f * s_l[w];
-      x += f * s_o[w][threadIdx.x];
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; w++) {
+    if (w < warp) before += sm.sum[w];
+    total += sm.sum[w];
+  }
+  before -= mine;
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+    if (length(a, b) == 0) {
+      const int64_t rows = int64_t(a.T) * a.Hq, at = b * rows;
+      for (int64_t i = threadIdx.x; i < rows * a.d / 8; i += kThreads)
+        reinterpret_cast<uint4 *>(a.out + at * a.d)[i] = make_uint4(0, 0, 0, 0);
+      if (a.lse)
+        for (int64_t i = threadIdx.x; i < rows; i += kThreads) a.lse[at + i] = -INFINITY;
     }
-  const int64_t r = (int64_t(b) * a.T + t) * a.Hq + hq;
-  if (int(threadIdx.x) < a.d) a.out[r * a.d + threadIdx.x] = elem_of<BF16>(sum == 0.0f ? 0.0f : x / sum);
-  if (threadIdx.x == 0 && a.lse) a.lse[r] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  const int64_t ctas = min(int64_t(gridDim.x), total);
+  if (blockIdx.x >= ctas) return;
+  const int64_t lo = total * blockIdx.x / ctas, hi = total * (blockIdx.x + 1) / ctas;
+  if (lo >= before && lo < before + mine) {  // one thread's sequences hold the first unit
+    int64_t at = before;
+    int b = b0;
+    for (;; b++) {
+      const int64_t n = (length(a, b) + kUnit - 1) / kUnit * a.HR;
+      if (lo < at + n) break;
+      at += n;
+    }
+    sm.b = b;
+    sm.prefix = at;
+  }
+  if (a.d < D) {  // channels that no copy fills
+    uint4 *z = reinterpret_cast<uint4 *>(sm.ring[warp]);
+    for (int i = lane; i < int(sizeof(sm.ring[warp]) / 16); i += 32) z[i] = make_uint4(0, 0, 0, 0);
+  }
+  __syncthreads();
+
+  Walk cur;
+  cur.b = sm.b;
+  set_seq(a, cur);
+  cur.hr = int((lo - sm.prefix) / cur.tiles);
+  cur.tile = int((lo - sm.prefix) % cur.tiles);
+  int64_t item_u0 = sm.prefix + int64_t(cur.hr) * cur.tiles;  // the item's first unit
+  Walk ahead = cur;
+  const int64_t units = hi - lo;
+
+  // Page of this lane's row (lane & 15) of the unit that `ahead` stands at.
+  int page = -1, slot = 0, page_h = 0;
+  auto find_page = [&]() {
+    const int64_t tok = int64_t(ahead.tile) * kUnit + warp * kTok + (lane & 15);
+    page = -1;
+    page_h = ahead.hr;
+    if (tok < ahead.len) {
+      const int64_t blk = tok / a.bt;
+      slot = int(tok - blk * a.bt);
+      page = a.table[int64_t(ahead.b) * a.stride + blk];
+      if (uint32_t(page) >= uint32_t(a.n_blocks)) {
+        atomicOr(a.status, kStBadArg);
+        page = -1;
+      }
+    }
+  };
+  const int n_row_tiles = a.HR / a.H;
+  auto issue = [&](int s) {
+    Stage<D> &st = sm.ring[warp][s];
+    const int h = page_h / n_row_tiles;
+    const bool ok = page >= 0;
+    const uint32_t valid = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+    if (lane == 0) sm.valid[warp][s] = valid;
+    const int64_t off = ok ? page_row(page, a.H, h, a.bt, slot, a.d) : 0;
+    copy_async<4>(smem_of(&st.ks[lane]), (lane < 16 ? a.ks : a.vs) + (ok ? int64_t(page) * a.H + h : 0), ok);  // ks, vs
+#pragma unroll
+    for (int i = 0; i < kChunks / 2; i++) {
+      const int r = i * (32 / kChunks) + lane / kChunks, c = lane % kChunks;
+      const int64_t at = __shfl_sync(0xffffffffu, off, r) + c * 16;
+      const bool have = valid >> r & 1;
+      const int to = chunk_at<D>(r, c);
+      if (c * 16 < a.d) {
+        if ((a.d & 15) == 0) {
+          copy_async<16>(smem_of(st.k + to), a.kp + (have ? at : 0), have);
+          copy_async<16>(smem_of(st.v + to), a.vp + (have ? at : 0), have);
+        } else {
+          copy_async<8>(smem_of(st.k + to), a.kp + (have ? at : 0), have);
+          copy_async<8>(smem_of(st.v + to), a.vp + (have ? at : 0), have);
+          if (c * 16 + 8 < a.d) {
+            copy_async<8>(smem_of(st.k + to + 8), a.kp + (have ? at + 8 : 0), have);
+            copy_async<8>(smem_of(st.v + to + 8), a.vp + (have ? at + 8 : 0), have);
+          }
+        }
+      }
+    }
+  };
+  int64_t issued = 0;
+  find_page();
+#pragma unroll
+  for (int s = 0; s < kStages - 1; s++) {
+    if (issued < units) {
+      issue(s);
+      issued++;
+      if (issued < units) {
+        step(a, ahead);
+        find_page();
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+
+  uint32_t q[D / 16][4];
+  float o[kNT][4], m[2], l[2], sc[2];
+  int last[2], v_exp = 1;  // O is in units of 2^(v_exp - 127), the largest V scale so far
+  bool first = true;
+  for (int64_t u = 0; u < units; u++) {
+    const int h = cur.hr / n_row_tiles, r0 = (cur.hr % n_row_tiles) * kRows;
+    if (first) {  // a new item: its query rows
+      first = false;
+#pragma unroll
+      for (int half = 0; half < 2; half++) {
+        const int r = r0 + g + 8 * half, tt = r / a.G;
+        const bool ok = r < a.T * a.G;
+        const uint16_t *src = a.q + cur.b * a.q_seq + tt * a.q_tok + int64_t(h * a.G + r % a.G) * a.q_head;
+        last[half] = ok ? int(cur.len - a.T + tt) : 0x7fffffff;  // a row of padding may see anything
+        uint4 w[D / 32];
+#pragma unroll
+        for (int c = 0; c < D / 32; c++) {  // channels 64 (c / 2) + 16 t + 8 (c % 2) ...
+          const int ch = 64 * (c >> 1) + 16 * t + 8 * (c & 1);
+          w[c] = ok && ch < a.d ? *reinterpret_cast<const uint4 *>(src + ch) : make_uint4(0, 0, 0, 0);
+        }
+        sc[half] = a.scale_log2;
+        if (BF16) {  // to f16, exactly but for what is under 2^-38 of the row's largest
+          uint32_t top = 0;
+#pragma unroll
+          for (int c = 0; c < D / 32; c++) {
+            const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+            for (int k = 0; k < 4; k++) top = max(top, max(x[k] << 16 & 0x7fff0000u, x[k] & 0x7fff0000u));
+          }
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int f = min(253, max(1, 268 - int(top >> 23)));
+          const float up = __int_as_float(f << 23);
+          sc[half] *= __int_as_float((254 - f) << 23);
+#pragma unroll
+          for (int c = 0; c < D / 32; c++) {
+            uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+              x[k] = pack(__uint_as_float(x[k] << 16) * up, __uint_as_float(x[k] & 0xffff0000u) * up);
+            w[c] = make_uint4(x[0], x[1], x[2], x[3]);
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < D / 64; c++) {
+          q[4 * c][half] = w[2 * c].x, q[4 * c][half + 2] = w[2 * c].y;
+          q[4 * c + 1][half] = w[2 * c].z, q[4 * c + 1][half + 2] = w[2 * c].w;
+          q[4 * c + 2][half] = w[2 * c + 1].x, q[4 * c + 2][half + 2] = w[2 * c + 1].y;
+          q[4 * c + 3][half] = w[2 * c + 1].z, q[4 * c + 3][half + 2] = w[2 * c + 1].w;
+        }
+        m[half] = -INFINITY;
+        l[half] = 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < kNT; j++) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+      v_exp = 1;
+    }
+
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncwarp();
+    const int s = int(u % kStages);
+    if (issued < units) {
+      issue(int((u + kStages - 1) % kStages));
+      issued++;
+      if (issued < units) {
+        step(a, ahead);
+        find_page();
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+
+    const Stage<D> &st = sm.ring[warp][s];
+    const uint32_t valid = sm.valid[warp][s];
+    const int64_t tok0 = int64_t(cur.tile) * kUnit + warp * kTok;
+    if (valid) {
+      // S = Q K^T: positions 8 n + 2 t, 8 n + 2 t + 1 of rows g and g + 8
+      float x[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; n++) {
+        x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < D / 64; c++) {
+          const uint4 w = *reinterpret_cast<const uint4 *>(st.k + chunk_at<D>(8 * n + g, 4 * c + t));
+          const uint32_t y[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int k = 0; k < 4; k++) {
+            const uint32_t z = biased<FMT>(y[k]);
+            mma(x[n], q[4 * c + k], halves_of<FMT, 0>(z), halves_of<FMT, 1>(z));
+          }
+        }
+      }
+      float vs[2][2];
+#pragma unroll
+      for (int n = 0; n < 2; n++) {
+        const float2 ks = *reinterpret_cast<const float2 *>(&st.ks[8 * n + 2 * t]);
+        const float2 v2 = *reinterpret_cast<const float2 *>(&st.vs[8 * n + 2 * t]);
+        vs[n][0] = v2.x, vs[n][1] = v2.y;
+        x[n][0] *= ks.x * sc[0], x[n][1] *= ks.y * sc[0];
+        x[n][2] *= ks.x * sc[1], x[n][3] *= ks.y * sc[1];
+      }
+      // whether every position is there and every row sees it
+      const bool whole = valid == 0xffffu && tok0 + kTok - 1 <= cur.len - a.T;
+      uint32_t seen = 0xffu;  // bit 4 n + 2 half + i
+      if (!whole) {
+        seen = 0;
+#pragma unroll
+        for (int n = 0; n < 2; n++)
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const int p = 8 * n + 2 * t + (i & 1);
+            if ((valid >> p & 1) && tok0 + p <= last[i >> 1])
+              seen |= 1u << (4 * n + i);
+            else
+              x[n][i] = -INFINITY;
+          }
+      }
+      float keep[2];
+      bool moved = false;
+#pragma unroll
+      for (int half = 0; half < 2; half++) {
+        float top = fmaxf(fmaxf(x[0][2 * half], x[0][2 * half + 1]), fmaxf(x[1][2 * half], x[1][2 * half + 1]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        keep[half] = 1.0f;
+        if (top > m[half] + kLag) {
+          keep[half] = ex2(m[half] - top);
+          m[half] = top;
+          moved = true;
+        }
+      }
+      float vmax = fmaxf(fmaxf(fabsf(vs[0][0]), fabsf(vs[0][1])), fmaxf(fabsf(vs[1][0]), fabsf(vs[1][1])));
+      vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
+      vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
+      const int e = min(254, int(__float_as_uint(vmax) >> 23) + 1);
+      float down = 1.0f;
+      if (e > v_exp) {  // the same in every lane
+        down = e - v_exp > 126 ? 0.0f : __int_as_float((127 + v_exp - e) << 23);
+        v_exp = e;
+        moved = true;
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+        l[0] *= keep[0], l[1] *= keep[1];
+        const float f0 = keep[0] * down, f1 = keep[1] * down;
+#pragma unroll
+        for (int j = 0; j < kNT; j++) o[j][0] *= f0, o[j][1] *= f0, o[j][2] *= f1, o[j][3] *= f1;
+      }
+      const float unit = __int_as_float((254 - v_exp) << 23);
+      bool small = false;
+      float base[2];
+#pragma unroll
+      for (int half = 0; half < 2; half++) base[half] = kLift - (m[half] == -INFINITY ? 0.0f : m[half]);
+#pragma unroll
+      for (int n = 0; n < 2; n++) {
+        vs[n][0] *= unit, vs[n][1] *= unit;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const float p = ex2(x[n][i] + base[i >> 1]);
+          l[i >> 1] += p;
+          x[n][i] = seen >> (4 * n + i) & 1 ? p * vs[n][i & 1] : 0.0f;
+          small |= fabsf(x[n][i]) < kNormal && x[n][i] != 0.0f;
+        }
+      }
+      uint32_t pf[4];
+      auto to_half = [&](float below) {  // without what is smaller than `below`
+#pragma unroll
+        for (int n = 0; n < 2; n++)
+#pragma unroll
+          for (int half = 0; half < 2; half++) {
+            const float p0 = x[n][2 * half], p1 = x[n][2 * half + 1];
+            pf[2 * n + half] = pack(fabsf(p0) < below ? 0.0f : p0, fabsf(p1) < below ? 0.0f : p1);
+          }
+      };
+      small = __any_sync(0xffffffffu, small);
+      if (small)
+        to_half(kNormal);
+      else
+        to_half(0.0f);
+
+      // O += P V: column tile j is channel (D / 8) g + j; positions 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+      constexpr int kWords = D / 32;  // words of a token that a lane takes
+      uint32_t w[4][kWords];
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const int r = 2 * t + (i & 1) + 8 * (i >> 1);
+        if (D == 128) {
+          const uint4 y = *reinterpret_cast<const uint4 *>(st.v + chunk_at<D>(r, g));
+          w[i][0] = y.x, w[i][1] = y.y, w[i][kWords - 2] = y.z, w[i][kWords - 1] = y.w;
+        } else {
+          const uint2 y = *reinterpret_cast<const uint2 *>(st.v + chunk_at<D>(r, g >> 1) + 8 * (g & 1));
+          w[i][0] = y.x, w[i][1] = y.y;
+        }
+      }
+      bool odd = false;
+      if (FMT == CG_CACHE_E4M3 && !whole && a.T > 1) {
+        // A NaN code behind a row's last position must not reach that row
+        // through 0 * NaN: such codes are taken out of the product, and a
+        // product of "sees" and "is NaN" says which outputs are NaN.
+        uint32_t any = 0;
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+          for (int k = 0; k < kWords; k++) any |= __vcmpeq4(w[i][k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+        odd = __any_sync(0xffffffffu, any != 0);
+      }
+      if (odd) {
+        const uint32_t one = 0x3c00u;
+        uint32_t sees[4];
+#pragma unroll
+        for (int n = 0; n < 2; n++)
+#pragma unroll
+          for (int half = 0; half < 2; half++)
+            sees[2 * n + half] = (seen >> (4 * n + 2 * half) & 1 ? one : 0) | (seen >> (4 * n + 2 * half + 1) & 1 ? one << 16 : 0);
+#pragma unroll
+        for (int k = 0; k < kWords; k++) {
+          uint32_t z[4];
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            z[i] = __vcmpeq4(w[i][k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+            w[i][k] &= ~z[i];
+          }
+#pragma unroll
+          for (int c = 0; c < 4; c++) {
+            const uint32_t n0 = (z[0] >> (8 * c) & 1 ? one : 0) | (z[1] >> (8 * c) & 1 ? one << 16 : 0);
+            const uint32_t n1 = (z[2] >> (8 * c) & 1 ? one : 0) | (z[3] >> (8 * c) & 1 ? one << 16 : 0);
+            float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            mma(hit, sees, n0, n1);
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+              if (hit[i] > 0.0f) o[4 * k + c][i] = __int_as_float(0x7fffffff);
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kWords; k++) {
+        uint32_t z[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) z[i] = biased<FMT>(w[i][k]);
+        const uint32_t a01 = __byte_perm(z[0], z[1], 0x5140), a23 = __byte_perm(z[0], z[1], 0x7362);
+        const uint32_t b01 = __byte_perm(z[2], z[3], 0x5140), b23 = __byte_perm(z[2], z[3], 0x7362);
+        mma(o[4 * k], pf, halves_of<FMT, 0>(a01), halves_of<FMT, 0>(b01));
+        mma(o[4 * k + 1], pf, halves_of<FMT, 1>(a01), halves_of<FMT, 1>(b01));
+        mma(o[4 * k + 2], pf, halves_of<FMT, 0>(a23), halves_of<FMT, 0>(b23));
+        mma(o[4 * k + 3], pf, halves_of<FMT, 1>(a23), halves_of<FMT, 1>(b23));
+      }
+      if (small) {
+        float fall = 1.0f;
+#pragma unroll 1
+        for (int pass = 0; pass < 4; pass++) {  // to 2^-126
+          fall *= 0x1p-28f;
+          bool have = false;
+#pragma unroll
+          for (int n = 0; n < 2; n++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {  // what the last product had goes, the rest is raised
+              x[n][i] = fabsf(x[n][i]) < kNormal ? x[n][i] * 0x1p28f : 0.0f;
+              have |= x[n][i] != 0.0f;
+            }
+          if (!__any_sync(0xffffffffu, have)) break;
+          to_half(kNormal);
+#pragma unroll
+          for (int k = 0; k < kWords; k++) {
+            uint32_t z[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) z[i] = biased<FMT>(w[i][k]);
+            const uint32_t a01 = __byte_perm(z[0], z[1], 0x5140), a23 = __byte_perm(z[0], z[1], 0x7362);
+            const uint32_t b01 = __byte_perm(z[2], z[3], 0x5140), b23 = __byte_perm(z[2], z[3], 0x7362);
+            float y[4][4] = {};
+            mma(y[0], pf, halves_of<FMT, 0>(a01), halves_of<FMT, 0>(b01));
+            mma(y[1], pf, halves_of<FMT, 1>(a01), halves_of<FMT, 1>(b01));
+            mma(y[2], pf, halves_of<FMT, 0>(a23), halves_of<FMT, 0>(b23));
+            mma(y[3], pf, halves_of<FMT, 1>(a23), halves_of<FMT, 1>(b23));
+#pragma unroll
+            for (int c = 0; c < 4; c++)
+#pragma unroll
+              for (int i = 0; i < 4; i++) o[4 * k + c][i] += y[c][i] * fall;
+          }
+        }
+      }
+    }
+
+    const bool end = cur.tile + 1 == cur.tiles || u + 1 == units;
+    if (end) {
+      // The four warps' parts of the item, joined in a fixed order.
+#pragma unroll
+      for (int half = 0; half < 2; half++) {
+        l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
+        l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
+        if (t == 0) sm.m[warp][g + 8 * half] = m[half], sm.l[warp][g + 8 * half] = l[half];
+      }
+      __syncthreads();
+      float top[2], sum[2];
+#pragma unroll
+      for (int half = 0; half < 2; half++) {
+        const int r = g + 8 * half;
+        top[half] = -INFINITY;
+        for (int w = 0; w < kWarps; w++) top[half] = fmaxf(top[half], sm.m[w][r]);
+        sum[half] = 0.0f;
+        for (int w = 0; w < kWarps; w++)
+          sum[half] += sm.l[w][r] * (sm.m[w][r] == -INFINITY ? 0.0f : ex2(sm.m[w][r] - top[half]));
+        const float f = (m[half] == -INFINITY ? 0.0f : ex2(m[half] - top[half])) * __int_as_float(v_exp << 23);
+#pragma unroll
+        for (int j = 0; j < kNT; j++) o[j][2 * half] *= f, o[j][2 * half + 1] *= f;
+      }
+#pragma unroll
+      for (int w = kWarps / 2; w; w >>= 1) {  // warps w .. 2w-1 hand theirs to 0 .. w-1
+        if (warp >= w && warp < 2 * w)
+#pragma unroll
+          for (int j = 0; j < kNT; j++)
+            *reinterpret_cast<float4 *>(&sm.o[warp - w][(j * 32 + lane) * 4]) = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
+        __syncthreads();
+        if (warp < w)
+#pragma unroll
+          for (int j = 0; j < kNT; j++) {
+            const float4 y = *reinterpret_cast<const float4 *>(&sm.o[warp][(j * 32 + lane) * 4]);
+            o[j][0] += y.x, o[j][1] += y.y, o[j][2] += y.z, o[j][3] += y.w;
+          }
+        __syncthreads();
+      }
+      // who has units of this item
+      const int64_t u1 = item_u0 + cur.tiles - 1;
+      const int64_t c0 = ((item_u0 + 1) * ctas - 1) / total, c1 = ((u1 + 1) * ctas - 1) / total;
+      if (c0 == c1) {
+        if (warp == 0)
+#pragma unroll
+          for (int half = 0; half < 2; half++) {
+            const int r = r0 + g + 8 * half;
+            float y[D / 4];
+#pragma unroll
+            for (int i = 0; i < D / 4; i++) y[i] = out_at<D>(o, half, i);
+            if (r < a.T * a.G) write_row<BF16>(a, cur.b, h, r, y, D / 4 * t, top[half], sum[half], t == 0);
+          }
+      } else {
+        // slot 1: the CTA's last part, where another came before it
+        const int64_t begin = max(lo, item_u0);
+        float *part = a.parts + (2 * int64_t(blockIdx.x) + (begin > lo)) * kRows * (D + 2);
+        if (warp == 0)
+#pragma unroll
+          for (int half = 0; half < 2; half++) {
+            const int r = g + 8 * half;
+#pragma unroll
+            for (int i = 0; i < D / 4; i += 4)
+              *reinterpret_cast<float4 *>(part + r * D + D / 4 * t + i) =
+                  make_float4(out_at<D>(o, half, i), out_at<D>(o, half, i + 1), out_at<D>(o, half, i + 2), out_at<D>(o, half, i + 3));
+            if (t == 0) part[kRows * D + r] = top[half], part[kRows * D + kRows + r] = sum[half];
+          }
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0)
+          sm.last = atomicAdd(&a.count[int64_t(cur.b) * a.HR + cur.hr], 1) == int(c1 - c0);
+        __syncthreads();
+        if (sm.last) {
+          __threadfence();
+          auto slot_of = [&](int64_t c) {  // every part but the first is the first of its CTA
+            return a.parts + (2 * c + (c == c0 && total * c / ctas < item_u0)) * kRows * (D + 2);
+          };
+          constexpr int kLanes = D / 8;  // threads of a row, eight channels each
+          const int rows = min(kRows, a.T * a.G - r0);
+          for (int r = threadIdx.x / kLanes; r < rows; r += kThreads / kLanes) {
+            const int ch = threadIdx.x % kLanes * 8;
+            float tp = -INFINITY, sum_l = 0.0f, y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            for (int64_t c = c0; c <= c1; c++) tp = fmaxf(tp, __ldcg(slot_of(c) + kRows * D + r));
+#pragma unroll 4
+            for (int64_t c = c0; c <= c1; c++) {
+              const float *p = slot_of(c);
+              const float mm = __ldcg(p + kRows * D + r), f = mm == -INFINITY ? 0.0f : ex2(mm - tp);
+              sum_l += f * __ldcg(p + kRows * D + kRows + r);
+              const float4 y0 = __ldcg(reinterpret_cast<const float4 *>(p + r * D + ch));
+              const float4 y1 = __ldcg(reinterpret_cast<const float4 *>(p + r * D + ch + 4));
+              y[0] += f * y0.x, y[1] += f * y0.y, y[2] += f * y0.z, y[3] += f * y0.w;
+              y[4] += f * y1.x, y[5] += f * y1.y, y[6] += f * y1.z, y[7] += f * y1.w;
+            }
+            write_row<BF16>(a, cur.b, h, r0 + r, y, ch, tp, sum_l, ch == 0);
+          }
+        }
+      }
+      first = true;
+      item_u0 += cur.tiles;
+    }
+    if (u + 1 < units) step(a, cur);
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+int row_tiles(const cg_cache *c, const cg_attend *t) {
+  return int((int64_t(t->q_tokens) * (t->Hq / c->H) + kRows - 1) / kRows);
 }
 
 bool attend_ok(const cg_cache *c, const cg_attend *t) {
@@ -85,14 +710,36 @@ bool attend_ok(const cg_cache *c, const cg_attend *t) {
   for (int64_t s : t->q_stride)
     if (s % 8) return false;
   return t->n_seq <= (1 << 20) && t->q_tokens <= (1 << 16) && t->Hq <= 65535 &&
-         int64_t(t->n_seq) * t->q_tokens <= 0x7fffffff;
+         int64_t(t->n_seq) * c->H * row_tiles(c, t) <= (1 << 28);
+}
+
+uint64_t counts_bytes(const cg_cache *c, const cg_attend *t) {
+  return pad256(256 + 4 * uint64_t(t->n_seq) * c->H * row_tiles(c, t));
+}
+
+int padded(int d) { return d <= 64 ? 64 : 128; }
+
+template <int FMT, int D, bool BF16>
+cudaError_t launch(const AttendArgs &a, unsigned grid, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(k_attend<FMT, D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(Smem<D>)));
+  if (e != cudaSuccess) return e;
+  k_attend<FMT, D, BF16><<<grid, kThreads, sizeof(Smem<D>), st>>>(a);
+  return cudaGetLastError();
+}
+
+template <int FMT>
+cudaError_t launch_format(const AttendArgs &a, bool bf16, unsigned grid, cudaStream_t st) {
+  if (a.d <= 64) return bf16 ? launch<FMT, 64, true>(a, grid, st) : launch<FMT, 64, false>(a, grid, st);
+  return bf16 ? launch<FMT, 128, true>(a, grid, st) : launch<FMT, 128, false>(a, grid, st);
 }
 
 }  // namespace
 }  // namespace cg
 
 extern "C" size_t cg_cache_workspace_bytes(const cg_cache *cache, const cg_attend *attend) {
-  return cg::attend_ok(cache, attend) ? 256 : 0;
+  using namespace cg;
+  if (!attend_ok(cache, attend)) return 0;
+  return size_t(counts_bytes(cache, attend) + 4 * uint64_t(2 * kGrid) * kRows * (padded(cache->d) + 2));
 }
 
 extern "C" cg_status cg_cache_attend(const cg_cache *cache, const cg_attend *attend, const void *q_dev,
@@ -109,22 +756,27 @@ extern "C" cg_status cg_cache_attend(const cg_cache *cache, const cg_attend *att
       ws_bytes < cg_cache_workspace_bytes(cache, attend))
     return CG_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(ws_dev, 0, 256, st) != cudaSuccess) return CG_ERR_CUDA;
+  uint8_t *ws = static_cast<uint8_t *>(ws_dev);
+  const uint64_t counts = counts_bytes(cache, attend);
+  if (cudaMemsetAsync(ws, 0, counts, st) != cudaSuccess) return CG_ERR_CUDA;
   AttendArgs a{};
   a.q = static_cast<const uint16_t *>(q_dev);
   a.kp = static_cast<const uint8_t *>(k_pool), a.vp = static_cast<const uint8_t *>(v_pool);
   a.ks = k_scale, a.vs = v_scale, a.table = table_dev, a.len = len_dev;
   a.out = static_cast<uint16_t *>(out_dev), a.lse = lse_dev;
-  a.status = static_cast<uint32_t *>(ws_dev);
+  a.status = reinterpret_cast<uint32_t *>(ws);
+  a.count = reinterpret_cast<int32_t *>(ws + 256);
+  a.parts = reinterpret_cast<float *>(ws + counts);
   a.q_seq = attend->q_stride[0], a.q_tok = attend->q_stride[1], a.q_head = attend->q_stride[2];
   a.B = attend->n_seq, a.T = attend->q_tokens, a.Hq = attend->Hq, a.H = cache->H, a.d = cache->d;
+  a.G = a.Hq / a.H, a.HR = a.H * row_tiles(cache, attend);
   a.bt = cache->block_tokens, a.n_blocks = cache->n_blocks, a.stride = attend->table_stride;
   a.scale_log2 = attend->scale * 1.4426950408889634f;
-  const dim3 grid(unsigned(a.B * a.T), unsigned(a.Hq));
-  const bool e4m3 = cache->format == CG_CACHE_E4M3, bf16 = attend->dtype == CG_BF16;
-  if (e4m3 && bf16) k_attend<CG_CACHE_E4M3, true><<<grid, kThreads, 0, st>>>(a);
-  if (e4m3 && !bf16) k_attend<CG_CACHE_E4M3, false><<<grid, kThreads, 0, st>>>(a);
-  if (!e4m3 && bf16) k_attend<CG_CACHE_INT8, true><<<grid, kThreads, 0, st>>>(a);
-  if (!e4m3 && !bf16) k_attend<CG_CACHE_INT8, false><<<grid, kThreads, 0, st>>>(a);
-  return launched();
+  const int64_t most = (int64_t(a.stride) * a.bt + kUnit - 1) / kUnit;  // units of an item
+  const int64_t items = int64_t(a.B) * a.HR;
+  const unsigned grid = unsigned(most >= kGrid || items * most >= kGrid ? kGrid : items * most);
+  const bool bf16 = attend->dtype == CG_BF16;
+  const cudaError_t e = cache->format == CG_CACHE_E4M3 ? launch_format<CG_CACHE_E4M3>(a, bf16, grid, st)
+                                                       : launch_format<CG_CACHE_INT8>(a, bf16, grid, st);
+  return e == cudaSuccess ? CG_OK : CG_ERR_CUDA;
 }
