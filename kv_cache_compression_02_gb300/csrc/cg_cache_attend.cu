@@ -16,12 +16,15 @@
 // free, so a thread takes 16 consecutive channels of a token (K) or of two
 // tokens (V) for the fragments of four or sixteen products.
 //
-// Work is cut into units of 64 positions of one (sequence, head, row tile),
-// and the units of the whole call are dealt in equal runs to as many CTAs as
-// fit on the GPU: a long context is shared by all SMs, short ones are packed.
-// A CTA that covers only a part of an item leaves its running maximum, sum
-// and output in the workspace; the last one of an item to finish joins the
-// parts in their order, so the result does not depend on timing.
+// Work is cut into units of 128 positions of one item (sequence, head, row
+// tile), and the units of the whole call are dealt in equal runs to as many
+// CTAs as fit on the GPU: a long context is shared by all SMs, short ones are
+// packed.  A CTA that covers only a part of an item leaves its running
+// maximum, sum and output in the workspace, and a second kernel, already
+// waiting when the first one ends, joins the parts in their order: the result
+// does not depend on timing.
+#include <type_traits>
+
 #include "cg_cache.cuh"
 
 namespace cg {
@@ -29,12 +32,13 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTok = 16;               // positions of a warp's tile
+constexpr int kTok = 32;               // positions of a warp's tile
 constexpr int kUnit = kTok * kWarps;   // positions of a unit
 constexpr int kRows = 16;              // query rows of an item
-constexpr int kStages = 3;             // tiles in flight per warp
-constexpr int kPerSM = 3;              // CTAs
+constexpr int kStages = 2;             // tiles in flight per warp
+constexpr int kPerSM = 2;              // CTAs
 constexpr int kGrid = kSMs * kPerSM;
+constexpr int kShort = 8;               // units of an item that one CTA takes where items are few
 
 // A probability is held as p = 2^(s - m + kLift), and m may lag behind the
 // true maximum by kLag, so that p < 2^15.  For the second product it is
@@ -42,6 +46,26 @@ constexpr int kGrid = kSMs * kPerSM;
 // 11 bits from kNormal up.  Smaller ones, rare but for sharp distributions,
 // go through products of their own, raised by 2^28 each time.
 constexpr float kLift = 12.0f, kLag = 3.0f, kNormal = 0x1p-14f;
+
+// n / d for n < 2^31 (a multiplication by the reciprocal, rounded up).
+struct Divisor {
+  uint32_t mul, shift;
+  Divisor(uint32_t d = 1) {
+    shift = 0;
+    while ((uint64_t(1) << shift) < d) shift++;
+    mul = uint32_t(((uint64_t(1) << 32) * ((uint64_t(1) << shift) - d)) / d + 1);
+  }
+  __device__ uint32_t operator()(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
+// What a CTA leaves behind: its error bits, and the item that it has the first
+// but not the last part of (parts = 0: none).
+struct Note {
+  uint32_t errors;
+  int32_t parts;   // of the item, in this CTA and the next ones
+  int32_t second;  // the first part is in this CTA's second slot
+  int32_t b, h, rt;
+};
 
 struct AttendArgs {
   const uint16_t *q;
@@ -51,11 +75,12 @@ struct AttendArgs {
   uint16_t *out;
   float *lse;
   uint32_t *status;
-  int32_t *count;   // [items]: parts of an item that are in the workspace
+  Note *notes;      // [kGrid]: what each CTA of k_attend leaves for k_join
   float *parts;     // [2 * kGrid][kRows][D + 2]
   int64_t q_seq, q_tok, q_head;
-  int B, T, Hq, H, G, HR, d, bt, n_blocks, stride;  // HR: heads x row tiles
+  int B, T, Hq, H, G, RT, HR, d, bt, n_blocks, stride;  // RT: row tiles; HR: heads x row tiles
   float scale_log2;  // scale * log2(e)
+  Divisor by_bt;
 };
 
 template <int D>
@@ -70,8 +95,9 @@ struct Smem {
   float o[2][kRows * D];  // where warps hand their outputs over
   float m[kWarps][kRows], l[kWarps][kRows];
   uint32_t valid[kWarps][kStages];
-  int64_t sum[kThreads / 32], start, prefix;
-  int b, last;
+  int64_t sum[kWarps][2], start, prefix;
+  int most[kWarps], b;
+  uint32_t errors;
 };
 
 // Where 16-byte chunk c of row r lies in a tile.  The reads are: K, chunks
@@ -94,10 +120,47 @@ __device__ inline void copy_async(uint32_t dst, const void *src, bool ok) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(n) : "memory");
 }
 
+__device__ inline void copy_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 __device__ inline void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ inline float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+__device__ inline float min3(float a, float b, float c) {
+  float y;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+// Two fp32 operations in one instruction.
+__device__ inline float2 fma2(float2 a, float2 b, float2 c) {
+  float2 y;
+  asm("{.reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7};"
+      " fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d;}"
+      : "=f"(y.x), "=f"(y.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return y;
+}
+__device__ inline float2 add2(float2 a, float2 b) {
+  float2 y;
+  asm("{.reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d;}"
+      : "=f"(y.x), "=f"(y.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
+}
+__device__ inline float2 mul2(float2 a, float2 b) {
+  float2 y;
+  asm("{.reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mul.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d;}"
+      : "=f"(y.x), "=f"(y.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
 }
 
 __device__ inline float ex2(float x) {
@@ -132,32 +195,37 @@ __device__ inline uint32_t pack(float lo, float hi) {
   return r;
 }
 
-// A walk over the units of a call, from one item to the next.
+// A walk over the units of a call, from one item (sequence, head, row tile) to the next.
 struct Walk {
-  int b, hr, tile, tiles;
-  int64_t len;
+  int b, h, rt, tile, tiles, len;
 };
 
-__device__ inline int64_t length(const AttendArgs &a, int b) {
-  const int64_t n = a.len[b], most = int64_t(a.stride) * a.bt;
-  return n < 0 ? 0 : n > most ? most : n;
+__device__ inline int length(const AttendArgs &a, int b) {
+  return int(max(int64_t(0), min(int64_t(a.len[b]), int64_t(a.stride) * a.bt)));
 }
+
+__device__ inline int tiles_of(int len) { return int((uint32_t(len) + kUnit - 1) / kUnit); }
 
 __device__ inline void set_seq(const AttendArgs &a, Walk &w) {
   w.len = length(a, w.b);
-  w.tiles = int((w.len + kUnit - 1) / kUnit);
+  w.tiles = tiles_of(w.len);
 }
 
-// The next unit; the caller knows that there is one.
-__device__ inline void step(const AttendArgs &a, Walk &w) {
-  if (++w.tile < w.tiles) return;
+// The next item; the caller knows that there is one.
+__device__ inline void next_item(const AttendArgs &a, Walk &w) {
   w.tile = 0;
-  if (++w.hr < a.HR) return;
-  w.hr = 0;
+  if (++w.rt < a.RT) return;
+  w.rt = 0;
+  if (++w.h < a.H) return;
+  w.h = 0;
   do {
     w.b++;
     set_seq(a, w);
   } while (w.tiles == 0);
+}
+
+__device__ inline void step(const AttendArgs &a, Walk &w) {
+  if (++w.tile == w.tiles) next_item(a, w);
 }
 
 // One row's outputs: lane t of a quad holds channels D/4 t .. D/4 t + D/4 - 1
@@ -186,7 +254,10 @@ __device__ inline void write_row(const AttendArgs &a, int b, int h, int r, const
   if (lead && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (m - kLift + log2f(l)) * 0.6931471805599453f;
 }
 
-template <int FMT, int D, bool BF16>
+// PLAIN: pages are a multiple of 16 tokens and a row has D channels, so that
+// half a warp's tile lies in one page (one table entry, one scale and one
+// address for sixteen rows) and no chunk of it is ragged.  MEASURE
+template <int FMT, int D, bool BF16, bool PLAIN>
 __global__ void __launch_bounds__(kThreads, kPerSM) k_attend(const AttendArgs a) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Smem<D> &sm = *reinterpret_cast<Smem<D> *>(smem_raw);
@@ -194,31 +265,48 @@ __global__ void __launch_bounds__(kThreads, kPerSM) k_attend(const AttendArgs a)
   constexpr int kChunks = D / 16;  // 16-byte chunks of a row
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
-  // Sequences with nothing in them, and the units of the call.
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (threadIdx.x == 0) {
+    sm.errors = 0;
+    a.notes[blockIdx.x].parts = 0;
+  }
+  // The items of the call and what they cost.  An item costs its units and
+  // one more (its queries' way in, the warps' join and the way out take about
+  // as long).  Where items are few and short each has a CTA of its own.
   const int per = (a.B + kThreads - 1) / kThreads, b0 = threadIdx.x * per, b1 = min(a.B, b0 + per);
-  int64_t mine = 0;
+  int64_t cost = 0, items = 0;
+  int most = 0;
+  bool bad_len = false;
   for (int b = b0; b < b1; b++) {
     const int n = a.len[b];
-    if (blockIdx.x == 0 && (n < 0 || int64_t(n) > int64_t(a.stride) * a.bt)) atomicOr(a.status, kStBadArg);
-    mine += (length(a, b) + kUnit - 1) / kUnit;
+    bad_len |= n < 0 || int64_t(n) > int64_t(a.stride) * a.bt;
+    const int tiles = tiles_of(length(a, b));
+    cost += tiles ? tiles + 1 : 0;
+    items += tiles > 0;
+    most = max(most, tiles);
   }
-  mine *= a.HR;
-  int64_t before = mine;
+  cost *= a.HR, items *= a.HR;
+  int64_t cost_to = cost, items_to = items;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += y;
+    const int64_t y = __shfl_up_sync(0xffffffffu, cost_to, o), z = __shfl_up_sync(0xffffffffu, items_to, o);
+    if (lane >= o) cost_to += y, items_to += z;
   }
-  if (lane == 31) sm.sum[warp] = before;
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) sm.sum[warp][0] = cost_to, sm.sum[warp][1] = items_to, sm.most[warp] = most;
   __syncthreads();
-  int64_t total = 0;
+  int64_t total = 0, n_items = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; w++) {
-    if (w < warp) before += sm.sum[w];
-    total += sm.sum[w];
+    if (w < warp) cost_to += sm.sum[w][0], items_to += sm.sum[w][1];
+    total += sm.sum[w][0], n_items += sm.sum[w][1];
+    most = max(most, sm.most[w]);
   }
-  before -= mine;
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+  const bool single = most <= kShort && n_items <= gridDim.x;  // a CTA per item
+  if (single) total = n_items, cost = items, cost_to = items_to;
+  const int64_t before = cost_to - cost;
+  if (blockIdx.x == 0 && bad_len) atomicOr(&sm.errors, kStBadArg);
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x)  // sequences with nothing in them
     if (length(a, b) == 0) {
       const int64_t rows = int64_t(a.T) * a.Hq, at = b * rows;
       for (int64_t i = threadIdx.x; i < rows * a.d / 8; i += kThreads)
@@ -227,20 +315,25 @@ __global__ void __launch_bounds__(kThreads, kPerSM) k_attend(const AttendArgs a)
         for (int64_t i = threadIdx.x; i < rows; i += kThreads) a.lse[at + i] = -INFINITY;
     }
   const int64_t ctas = min(int64_t(gridDim.x), total);
-  if (blockIdx.x >= ctas) return;
+  if (blockIdx.x >= ctas) {
+    __syncthreads();
+    if (threadIdx.x == 0) a.notes[blockIdx.x].errors = sm.errors;
+    return;
+  }
   const int64_t lo = total * blockIdx.x / ctas, hi = total * (blockIdx.x + 1) / ctas;
-  if (lo >= before && lo < before + mine) {  // one thread's sequences hold the first unit
+  auto cost_of = [&](int tiles) { return single ? (tiles > 0) : tiles ? tiles + 1 : 0; };
+  if (lo >= before && lo < before + cost) {  // one thread's sequences hold the first unit
     int64_t at = before;
     int b = b0;
     for (;; b++) {
-      const int64_t n = (length(a, b) + kUnit - 1) / kUnit * a.HR;
+      const int64_t n = int64_t(cost_of(tiles_of(length(a, b)))) * a.HR;
       if (lo < at + n) break;
       at += n;
     }
     sm.b = b;
     sm.prefix = at;
   }
-  if (a.d < D) {  // channels that no copy fills
+  if (!PLAIN && a.d < D) {  // channels that no copy fills
     uint4 *z = reinterpret_cast<uint4 *>(sm.ring[warp]);
     for (int i = lane; i < int(sizeof(sm.ring[warp]) / 16); i += 32) z[i] = make_uint4(0, 0, 0, 0);
   }
@@ -249,59 +342,114 @@ __global__ void __launch_bounds__(kThreads, kPerSM) k_attend(const AttendArgs a)
   Walk cur;
   cur.b = sm.b;
   set_seq(a, cur);
-  cur.hr = int((lo - sm.prefix) / cur.tiles);
-  cur.tile = int((lo - sm.prefix) % cur.tiles);
-  int64_t item_u0 = sm.prefix + int64_t(cur.hr) * cur.tiles;  // the item's first unit
+  int item_cost = cost_of(cur.tiles);
+  const int item0 = int((lo - sm.prefix) / item_cost);
+  cur.h = item0 / a.RT, cur.rt = item0 % a.RT;
+  int64_t item_lo = sm.prefix + int64_t(item0) * item_cost;  // where the item's cost begins
+  // A run [lo, hi) of costs has the tiles whose costs lie in it; an item's
+  // first cost is no tile.
+  const int skip = single ? 0 : 1;
+  cur.tile = max(0, int(lo - item_lo) - skip);
+  int units = 0;  // tiles of the run
+  if (single) {
+    units = cur.tiles;
+  } else {
+    int64_t at = lo;
+    Walk w = cur;
+    int64_t w_lo = item_lo;
+    int w_cost = item_cost;
+    while (at < hi) {  // item by item
+      const int64_t end = min(hi, w_lo + w_cost);
+      units += int(max(int64_t(0), end - w_lo - 1) - max(int64_t(0), at - w_lo - 1));
+      at = end;
+      if (at < hi) {
+        w_lo += w_cost;
+        next_item(a, w);
+        w_cost = w.tiles + 1;
+      }
+    }
+  }
   Walk ahead = cur;
-  const int64_t units = hi - lo;
 
-  // Page of this lane's row (lane & 15) of the unit that `ahead` stands at.
-  int page = -1, slot = 0, page_h = 0;
+  // The page of row `lane` of the warp's tile in the unit that `ahead` stands
+  // at; PLAIN: that of the lane's half of the tile.
+  const int d = PLAIN ? D : a.d;
+  const int64_t page_elems = int64_t(a.H) * a.bt * d;
+  int page = -1, slot = 0, page_h = 0, have_rows = 0;
   auto find_page = [&]() {
-    const int64_t tok = int64_t(ahead.tile) * kUnit + warp * kTok + (lane & 15);
+    const uint32_t tok0 = uint32_t(ahead.tile) * kUnit + warp * kTok, tok = tok0 + (PLAIN ? lane & 16 : lane);
     page = -1;
-    page_h = ahead.hr;
-    if (tok < ahead.len) {
-      const int64_t blk = tok / a.bt;
+    page_h = ahead.h;
+    have_rows = ahead.len - int(tok0);
+    if (tok < uint32_t(ahead.len)) {
+      const uint32_t blk = a.by_bt(tok);
       slot = int(tok - blk * a.bt);
       page = a.table[int64_t(ahead.b) * a.stride + blk];
       if (uint32_t(page) >= uint32_t(a.n_blocks)) {
-        atomicOr(a.status, kStBadArg);
+        atomicOr(&sm.errors, kStBadArg);
         page = -1;
       }
     }
   };
-  const int n_row_tiles = a.HR / a.H;
   auto issue = [&](int s) {
     Stage<D> &st = sm.ring[warp][s];
-    const int h = page_h / n_row_tiles;
     const bool ok = page >= 0;
-    const uint32_t valid = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+    const int64_t off = ok ? page * page_elems + (int64_t(page_h) * a.bt + slot) * d : 0;
+    const int64_t sc_at = ok ? int64_t(page) * a.H + page_h : 0;
+    const int c = lane % kChunks, r0 = lane / kChunks;
+    const uint32_t pages = __ballot_sync(0xffffffffu, ok);
+    uint32_t valid = pages;
+    if (PLAIN) {  // the rows that are there, of the pages that are right
+      valid &= have_rows >= kTok ? 0xffffffffu : have_rows <= 0 ? 0u : (1u << have_rows) - 1;
+      if ((lane & 15) < 2) copy_async<4>(smem_of((lane & 1 ? st.vs : st.ks) + (lane >> 4)), (lane & 1 ? a.vs : a.ks) + sc_at, ok);
+    } else {
+      copy_async<4>(smem_of(&st.ks[lane]), a.ks + sc_at, ok);
+      copy_async<4>(smem_of(&st.vs[lane]), a.vs + sc_at, ok);
+    }
     if (lane == 0) sm.valid[warp][s] = valid;
-    const int64_t off = ok ? page_row(page, a.H, h, a.bt, slot, a.d) : 0;
-    copy_async<4>(smem_of(&st.ks[lane]), (lane < 16 ? a.ks : a.vs) + (ok ? int64_t(page) * a.H + h : 0), ok);  // ks, vs
+    constexpr int kStep = 32 / kChunks;  // rows of one copy
+    if (PLAIN && valid == 0xffffffffu) {  // all there: addresses that differ by constants
+      const int64_t h0 = __shfl_sync(0xffffffffu, off, 0) + r0 * D + c * 16, h1 = __shfl_sync(0xffffffffu, off, 16) + r0 * D + c * 16;
+      const uint8_t *k0 = a.kp + h0, *k1 = a.kp + h1, *v0 = a.vp + h0, *v1 = a.vp + h1;
 #pragma unroll
-    for (int i = 0; i < kChunks / 2; i++) {
-      const int r = i * (32 / kChunks) + lane / kChunks, c = lane % kChunks;
-      const int64_t at = __shfl_sync(0xffffffffu, off, r) + c * 16;
+      for (int i = 0; i < kTok / kStep; i++) {
+        const int to = chunk_at<D>(i * kStep + r0, c), at = i * kStep % 16 * D;
+        copy_async16(smem_of(st.k + to), (i * kStep < 16 ? k0 : k1) + at);
+        copy_async16(smem_of(st.v + to), (i * kStep < 16 ? v0 : v1) + at);
+      }
+      return;
+    }
+    const int64_t half0 = __shfl_sync(0xffffffffu, off, 0) + r0 * d + c * 16;
+    const int64_t half1 = __shfl_sync(0xffffffffu, off, 16) + r0 * d + c * 16;
+#pragma unroll
+    for (int i = 0; i < kTok / kStep; i++) {
+      const int r = i * kStep + r0, to = chunk_at<D>(r, c);
       const bool have = valid >> r & 1;
-      const int to = chunk_at<D>(r, c);
-      if (c * 16 < a.d) {
-        if ((a.d & 15) == 0) {
-          copy_async<16>(smem_of(st.k + to), a.kp + (have ? at : 0), have);
-          copy_async<16>(smem_of(st.v + to), a.vp + (have ? at : 0), have);
-        } else {
-          copy_async<8>(smem_of(st.k + to), a.kp + (have ? at : 0), have);
-          copy_async<8>(smem_of(st.v + to), a.vp + (have ? at : 0), have);
-          if (c * 16 + 8 < a.d) {
-            copy_async<8>(smem_of(st.k + to + 8), a.kp + (have ? at + 8 : 0), have);
-            copy_async<8>(smem_of(st.v + to + 8), a.vp + (have ? at + 8 : 0), have);
+      if (PLAIN) {
+        int64_t at = (i * kStep < 16 ? half0 : half1) + i * kStep % 16 * D;
+        if (!have) at = 0;
+        copy_async<16>(smem_of(st.k + to), a.kp + at, have);
+        copy_async<16>(smem_of(st.v + to), a.vp + at, have);
+      } else {
+        int64_t at = __shfl_sync(0xffffffffu, off, r) + c * 16;
+        if (!have) at = 0;
+        if (c * 16 < d) {
+          if ((d & 15) == 0) {
+            copy_async<16>(smem_of(st.k + to), a.kp + at, have);
+            copy_async<16>(smem_of(st.v + to), a.vp + at, have);
+          } else {
+            copy_async<8>(smem_of(st.k + to), a.kp + at, have);
+            copy_async<8>(smem_of(st.v + to), a.vp + at, have);
+            if (c * 16 + 8 < d) {
+              copy_async<8>(smem_of(st.k + to + 8), a.kp + (have ? at + 8 : 0), have);
+              copy_async<8>(smem_of(st.v + to + 8), a.vp + (have ? at + 8 : 0), have);
+            }
           }
         }
       }
     }
   };
-  int64_t issued = 0;
+  int issued = 0;
   find_page();
 #pragma unroll
   for (int s = 0; s < kStages - 1; s++) {
@@ -317,11 +465,14 @@ __global__ void __launch_bounds__(kThreads, kPerSM) k_attend(const AttendArgs a)
   }
 
   uint32_t q[D / 16][4];
-  float o[kNT][4], m[2], l[2], sc[2];
+  float o[kNT][4], m[2], sc[2];
+  float2 l[2];  // sums of the even and the odd positions
   int last[2], v_exp = 1;  // O is in units of 2^(v_exp - 127), the largest V scale so far
   bool first = true;
-  for (int64_t u = 0; u < units; u++) {
-    const int h = cur.hr / n_row_tiles, r0 = (cur.hr % n_row_tiles) * kRows;
+  int seg = 0;  // items begun before
+  int slot_now = 0, slot_next = kStages - 1;  // of the ring
+  for (int u = 0; u < units; u++) {
+    const int h = cur.h, r0 = cur.rt * kRows;
     if (first) {  // a new item: its query rows
       first = false;
 #pragma unroll
@@ -329,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, kPerSM) k_attend(const AttendArgs a)
         const int r = r0 + g + 8 * half, tt = r / a.G;
         const bool ok = r < a.T * a.G;
         const uint16_t *src = a.q + cur.b * a.q_seq + tt * a.q_tok + int64_t(h * a.G + r % a.G) * a.q_head;
-        last[half] = ok ? int(cur.len - a.T + tt) : 0x7fffffff;  // a row of padding may see anything
+        last[half] = ok ? cur.len - a.T + tt : 0x7fffffff;  // a row of padding may see anything
         uint4 w[D / 32];
 #pragma unroll
         for (int c = 0; c < D / 32; c++) {  // channels 64 (c / 2) + 16 t + 8 (c % 2) ...
@@ -367,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, kPerSM) k_attend(const AttendArgs a)
           q[4 * c + 3][half] = w[2 * c + 1].z, q[4 * c + 3][half + 2] = w[2 * c + 1].w;
         }
         m[half] = -INFINITY;
-        l[half] = 0.0f;
+        l[half] = make_float2(0.0f, 0.0f);
       }
 #pragma unroll
       for (int j = 0; j < kNT; j++) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
@@ -376,25 +527,28 @@ __global__ void __launch_bounds__(kThreads, kPerSM) k_attend(const AttendArgs a)
 
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
     __syncwarp();
-    const int s = int(u % kStages);
+    const int s = slot_now;
+    slot_now = slot_now + 1 == kStages ? 0 : slot_now + 1;
     if (issued < units) {
-      issue(int((u + kStages - 1) % kStages));
+      issue(slot_next);
       issued++;
       if (issued < units) {
         step(a, ahead);
         find_page();
       }
     }
+    slot_next = slot_next + 1 == kStages ? 0 : slot_next + 1;
     asm volatile("cp.async.commit_group;" ::: "memory");
 
     const Stage<D> &st = sm.ring[warp][s];
     const uint32_t valid = sm.valid[warp][s];
-    const int64_t tok0 = int64_t(cur.tile) * kUnit + warp * kTok;
+    const uint32_t tok0 = uint32_t(cur.tile) * kUnit + warp * kTok;
     if (valid) {
       // S = Q K^T: positions 8 n + 2 t, 8 n + 2 t + 1 of rows g and g + 8
-      float x[2][4];
+      constexpr int kN = kTok / 8;
+      float x[kN][4], vs[kN][2];
 #pragma unroll
-      for (int n = 0; n < 2; n++) {
+      for (int n = 0; n < kN; n++) {
         x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.0f;
 #pragma unroll
         for (int c = 0; c < D / 64; c++) {
@@ -407,36 +561,49 @@ __global__ void __launch_bounds__(kThreads, kPerSM) k_attend(const AttendArgs a)
           }
         }
       }
-      float vs[2][2];
+      float f[kN / 2][2];  // PLAIN: what turns a product into a score, for each half of the tile and of the rows
 #pragma unroll
-      for (int n = 0; n < 2; n++) {
-        const float2 ks = *reinterpret_cast<const float2 *>(&st.ks[8 * n + 2 * t]);
-        const float2 v2 = *reinterpret_cast<const float2 *>(&st.vs[8 * n + 2 * t]);
-        vs[n][0] = v2.x, vs[n][1] = v2.y;
-        x[n][0] *= ks.x * sc[0], x[n][1] *= ks.y * sc[0];
-        x[n][2] *= ks.x * sc[1], x[n][3] *= ks.y * sc[1];
+      for (int n = 0; n < kN; n++) {
+        if (PLAIN) {
+          const float ks = st.ks[n >> 1];
+          f[n >> 1][0] = ks * sc[0], f[n >> 1][1] = ks * sc[1];
+          vs[n][0] = vs[n][1] = st.vs[n >> 1];
+        } else {
+          const float2 ks = *reinterpret_cast<const float2 *>(&st.ks[8 * n + 2 * t]);
+          const float2 v2 = *reinterpret_cast<const float2 *>(&st.vs[8 * n + 2 * t]);
+          vs[n][0] = v2.x, vs[n][1] = v2.y;
+          x[n][0] *= ks.x * sc[0], x[n][1] *= ks.y * sc[0];
+          x[n][2] *= ks.x * sc[1], x[n][3] *= ks.y * sc[1];
+          f[n >> 1][0] = f[n >> 1][1] = 1.0f;
+        }
       }
       // whether every position is there and every row sees it
-      const bool whole = valid == 0xffffu && tok0 + kTok - 1 <= cur.len - a.T;
-      uint32_t seen = 0xffu;  // bit 4 n + 2 half + i
+      const bool whole = valid == 0xffffffffu && int(tok0) + kTok - 1 <= cur.len - a.T;
+      uint32_t seen = 0xffffu;  // bit 4 n + 2 half + i
       if (!whole) {
         seen = 0;
 #pragma unroll
-        for (int n = 0; n < 2; n++)
+        for (int n = 0; n < kN; n++)
 #pragma unroll
           for (int i = 0; i < 4; i++) {
             const int p = 8 * n + 2 * t + (i & 1);
-            if ((valid >> p & 1) && tok0 + p <= last[i >> 1])
-              seen |= 1u << (4 * n + i);
-            else
-              x[n][i] = -INFINITY;
+            const bool sees = (valid >> p & 1) && int(tok0) + p <= last[i >> 1];
+            seen |= uint32_t(sees) << (4 * n + i);
+            x[n][i] = sees ? x[n][i] * f[n >> 1][i >> 1] : -INFINITY;
           }
+#pragma unroll
+        for (int n = 0; n < kN / 2; n++) f[n][0] = f[n][1] = 1.0f;
       }
       float keep[2];
       bool moved = false;
 #pragma unroll
       for (int half = 0; half < 2; half++) {
-        float top = fmaxf(fmaxf(x[0][2 * half], x[0][2 * half + 1]), fmaxf(x[1][2 * half], x[1][2 * half + 1]));
+        float top = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < kN; n += 2) {
+          const float y = max3(x[n][2 * half], x[n][2 * half + 1], fmaxf(x[n + 1][2 * half], x[n + 1][2 * half + 1]));
+          top = fmaxf(top, y * f[n >> 1][half]);
+        }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         keep[half] = 1.0f;
@@ -446,9 +613,13 @@ __global__ void __launch_bounds__(kThreads, kPerSM) k_attend(const AttendArgs a)
           moved = true;
         }
       }
-      float vmax = fmaxf(fmaxf(fabsf(vs[0][0]), fabsf(vs[0][1])), fmaxf(fabsf(vs[1][0]), fabsf(vs[1][1])));
-      vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
-      vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
+      float vmax = fabsf(vs[0][0]);
+#pragma unroll
+      for (int n = PLAIN ? 2 : 0; n < kN; n += PLAIN ? 2 : 1) vmax = fmaxf(vmax, fmaxf(fabsf(vs[n][0]), fabsf(vs[n][1])));
+      if (!PLAIN) {
+        vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
+        vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
+      }
       const int e = min(254, int(__float_as_uint(vmax) >> 23) + 1);
       float down = 1.0f;
       if (e > v_exp) {  // the same in every lane
@@ -457,108 +628,127 @@ __global__ void __launch_bounds__(kThreads, kPerSM) k_attend(const AttendArgs a)
         moved = true;
       }
       if (__any_sync(0xffffffffu, moved)) {
-        l[0] *= keep[0], l[1] *= keep[1];
+        l[0].x *= keep[0], l[0].y *= keep[0], l[1].x *= keep[1], l[1].y *= keep[1];
         const float f0 = keep[0] * down, f1 = keep[1] * down;
 #pragma unroll
         for (int j = 0; j < kNT; j++) o[j][0] *= f0, o[j][1] *= f0, o[j][2] *= f1, o[j][3] *= f1;
       }
       const float unit = __int_as_float((254 - v_exp) << 23);
-      bool small = false;
-      float base[2];
+      float least = INFINITY;  // of the probabilities
 #pragma unroll
-      for (int half = 0; half < 2; half++) base[half] = kLift - (m[half] == -INFINITY ? 0.0f : m[half]);
+      for (int half = 0; half < 2; half++) {
+        const float base = kLift - (m[half] == -INFINITY ? 0.0f : m[half]);
 #pragma unroll
-      for (int n = 0; n < 2; n++) {
-        vs[n][0] *= unit, vs[n][1] *= unit;
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const float p = ex2(x[n][i] + base[i >> 1]);
-          l[i >> 1] += p;
-          x[n][i] = seen >> (4 * n + i) & 1 ? p * vs[n][i & 1] : 0.0f;
-          small |= fabsf(x[n][i]) < kNormal && x[n][i] != 0.0f;
+        for (int n = 0; n < kN; n++) {
+          float2 y = make_float2(x[n][2 * half], x[n][2 * half + 1]);
+          const float g1 = f[n >> 1][half];
+          y = fma2(y, make_float2(g1, g1), make_float2(base, base));
+          y = make_float2(ex2(y.x), ex2(y.y));
+          l[half] = add2(l[half], y);
+          y = mul2(y, make_float2(vs[n][0] * unit, vs[n][1] * unit));
+          x[n][2 * half] = y.x, x[n][2 * half + 1] = y.y;
+          least = min3(least, fabsf(y.x), fabsf(y.y));
         }
       }
-      uint32_t pf[4];
-      auto to_half = [&](float below) {  // without what is smaller than `below`
+      if (!whole) {  // 0 * NaN
 #pragma unroll
-        for (int n = 0; n < 2; n++)
+        for (int n = 0; n < kN; n++)
+#pragma unroll
+          for (int i = 0; i < 4; i++)
+            if (!(seen >> (4 * n + i) & 1)) x[n][i] = 0.0f;
+      }
+      uint32_t pf[kN / 2][4];
+      auto to_half = [&](auto keep_small) {
+#pragma unroll
+        for (int n = 0; n < kN; n++)
 #pragma unroll
           for (int half = 0; half < 2; half++) {
-            const float p0 = x[n][2 * half], p1 = x[n][2 * half + 1];
-            pf[2 * n + half] = pack(fabsf(p0) < below ? 0.0f : p0, fabsf(p1) < below ? 0.0f : p1);
+            float p0 = x[n][2 * half], p1 = x[n][2 * half + 1];
+            if (!keep_small.value) p0 = fabsf(p0) < kNormal ? 0.0f : p0, p1 = fabsf(p1) < kNormal ? 0.0f : p1;
+            pf[n >> 1][2 * (n & 1) + half] = pack(p0, p1);
           }
       };
-      small = __any_sync(0xffffffffu, small);
+      const bool small = __any_sync(0xffffffffu, least < kNormal);
       if (small)
-        to_half(kNormal);
+        to_half(std::false_type());
       else
-        to_half(0.0f);
+        to_half(std::true_type());
 
-      // O += P V: column tile j is channel (D / 8) g + j; positions 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+      // O += P V, sixteen positions at a time: column tile j is channel (D / 8) g + j
       constexpr int kWords = D / 32;  // words of a token that a lane takes
-      uint32_t w[4][kWords];
+      auto load_v = [&](int s16, uint32_t (&w)[4][kWords]) {  // positions 2 t, 2 t + 1, 2 t + 8, 2 t + 9
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const int r = 2 * t + (i & 1) + 8 * (i >> 1);
-        if (D == 128) {
-          const uint4 y = *reinterpret_cast<const uint4 *>(st.v + chunk_at<D>(r, g));
-          w[i][0] = y.x, w[i][1] = y.y, w[i][kWords - 2] = y.z, w[i][kWords - 1] = y.w;
-        } else {
-          const uint2 y = *reinterpret_cast<const uint2 *>(st.v + chunk_at<D>(r, g >> 1) + 8 * (g & 1));
-          w[i][0] = y.x, w[i][1] = y.y;
-        }
-      }
-      bool odd = false;
-      if (FMT == CG_CACHE_E4M3 && !whole && a.T > 1) {
-        // A NaN code behind a row's last position must not reach that row
-        // through 0 * NaN: such codes are taken out of the product, and a
-        // product of "sees" and "is NaN" says which outputs are NaN.
-        uint32_t any = 0;
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-#pragma unroll
-          for (int k = 0; k < kWords; k++) any |= __vcmpeq4(w[i][k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-        odd = __any_sync(0xffffffffu, any != 0);
-      }
-      if (odd) {
-        const uint32_t one = 0x3c00u;
-        uint32_t sees[4];
-#pragma unroll
-        for (int n = 0; n < 2; n++)
-#pragma unroll
-          for (int half = 0; half < 2; half++)
-            sees[2 * n + half] = (seen >> (4 * n + 2 * half) & 1 ? one : 0) | (seen >> (4 * n + 2 * half + 1) & 1 ? one << 16 : 0);
-#pragma unroll
-        for (int k = 0; k < kWords; k++) {
-          uint32_t z[4];
-#pragma unroll
-          for (int i = 0; i < 4; i++) {
-            z[i] = __vcmpeq4(w[i][k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-            w[i][k] &= ~z[i];
-          }
-#pragma unroll
-          for (int c = 0; c < 4; c++) {
-            const uint32_t n0 = (z[0] >> (8 * c) & 1 ? one : 0) | (z[1] >> (8 * c) & 1 ? one << 16 : 0);
-            const uint32_t n1 = (z[2] >> (8 * c) & 1 ? one : 0) | (z[3] >> (8 * c) & 1 ? one << 16 : 0);
-            float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma(hit, sees, n0, n1);
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-              if (hit[i] > 0.0f) o[4 * k + c][i] = __int_as_float(0x7fffffff);
+        for (int i = 0; i < 4; i++) {
+          const int r = 16 * s16 + 2 * t + (i & 1) + 8 * (i >> 1);
+          if (D == 128) {
+            const uint4 y = *reinterpret_cast<const uint4 *>(st.v + chunk_at<D>(r, g));
+            w[i][0] = y.x, w[i][1] = y.y, w[i][kWords - 2] = y.z, w[i][kWords - 1] = y.w;
+          } else {
+            const uint2 y = *reinterpret_cast<const uint2 *>(st.v + chunk_at<D>(r, g >> 1) + 8 * (g & 1));
+            w[i][0] = y.x, w[i][1] = y.y;
           }
         }
-      }
-#pragma unroll
-      for (int k = 0; k < kWords; k++) {
+      };
+      // the products of four column tiles with P
+      auto product = [&](const uint32_t (&w)[4][kWords], int k, const uint32_t (&p)[4], float (&c)[4][4]) {
         uint32_t z[4];
 #pragma unroll
         for (int i = 0; i < 4; i++) z[i] = biased<FMT>(w[i][k]);
         const uint32_t a01 = __byte_perm(z[0], z[1], 0x5140), a23 = __byte_perm(z[0], z[1], 0x7362);
         const uint32_t b01 = __byte_perm(z[2], z[3], 0x5140), b23 = __byte_perm(z[2], z[3], 0x7362);
-        mma(o[4 * k], pf, halves_of<FMT, 0>(a01), halves_of<FMT, 0>(b01));
-        mma(o[4 * k + 1], pf, halves_of<FMT, 1>(a01), halves_of<FMT, 1>(b01));
-        mma(o[4 * k + 2], pf, halves_of<FMT, 0>(a23), halves_of<FMT, 0>(b23));
-        mma(o[4 * k + 3], pf, halves_of<FMT, 1>(a23), halves_of<FMT, 1>(b23));
+        mma(c[0], p, halves_of<FMT, 0>(a01), halves_of<FMT, 0>(b01));
+        mma(c[1], p, halves_of<FMT, 1>(a01), halves_of<FMT, 1>(b01));
+        mma(c[2], p, halves_of<FMT, 0>(a23), halves_of<FMT, 0>(b23));
+        mma(c[3], p, halves_of<FMT, 1>(a23), halves_of<FMT, 1>(b23));
+      };
+      bool odd = false;
+#pragma unroll
+      for (int s16 = 0; s16 < kN / 2; s16++) {
+        uint32_t w[4][kWords];
+        load_v(s16, w);
+        if (FMT == CG_CACHE_E4M3 && !whole && a.T > 1) {
+          // A NaN code behind a row's last position must not reach that row
+          // through 0 * NaN: such codes are taken out of the product, and a
+          // product of "sees" and "is NaN" says which outputs are NaN.
+          uint32_t any = 0;
+#pragma unroll
+          for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int k = 0; k < kWords; k++) any |= __vcmpeq4(w[i][k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+          odd |= __any_sync(0xffffffffu, any != 0);
+        }
+        if (odd) {
+          const uint32_t one = 0x3c00u;
+          uint32_t sees[4];
+#pragma unroll
+          for (int n = 0; n < 2; n++)
+#pragma unroll
+            for (int half = 0; half < 2; half++) {
+              const uint32_t b = seen >> (4 * (2 * s16 + n) + 2 * half);
+              sees[2 * n + half] = (b & 1 ? one : 0) | (b & 2 ? one << 16 : 0);
+            }
+#pragma unroll
+          for (int k = 0; k < kWords; k++) {
+            uint32_t z[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+              z[i] = __vcmpeq4(w[i][k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              w[i][k] &= ~z[i];
+            }
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+              const uint32_t n0 = (z[0] >> (8 * c) & 1 ? one : 0) | (z[1] >> (8 * c) & 1 ? one << 16 : 0);
+              const uint32_t n1 = (z[2] >> (8 * c) & 1 ? one : 0) | (z[3] >> (8 * c) & 1 ? one << 16 : 0);
+              float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+              mma(hit, sees, n0, n1);
+#pragma unroll
+              for (int i = 0; i < 4; i++)
+                if (hit[i] > 0.0f) o[4 * k + c][i] = __int_as_float(0x7fffffff);
+            }
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kWords; k++) product(w, k, pf[s16], reinterpret_cast<float(&)[4][4]>(o[4 * k]));
       }
       if (small) {
         float fall = 1.0f;
@@ -567,30 +757,30 @@ __global__ void __launch_bounds__(kThreads, kPerSM) k_attend(const AttendArgs a)
           fall *= 0x1p-28f;
           bool have = false;
 #pragma unroll
-          for (int n = 0; n < 2; n++)
+          for (int n = 0; n < kN; n++)
 #pragma unroll
             for (int i = 0; i < 4; i++) {  // what the last product had goes, the rest is raised
               x[n][i] = fabsf(x[n][i]) < kNormal ? x[n][i] * 0x1p28f : 0.0f;
               have |= x[n][i] != 0.0f;
             }
           if (!__any_sync(0xffffffffu, have)) break;
-          to_half(kNormal);
+          to_half(std::false_type());
 #pragma unroll
-          for (int k = 0; k < kWords; k++) {
-            uint32_t z[4];
+          for (int s16 = 0; s16 < kN / 2; s16++) {
+            uint32_t w[4][kWords];
+            load_v(s16, w);
 #pragma unroll
-            for (int i = 0; i < 4; i++) z[i] = biased<FMT>(w[i][k]);
-            const uint32_t a01 = __byte_perm(z[0], z[1], 0x5140), a23 = __byte_perm(z[0], z[1], 0x7362);
-            const uint32_t b01 = __byte_perm(z[2], z[3], 0x5140), b23 = __byte_perm(z[2], z[3], 0x7362);
-            float y[4][4] = {};
-            mma(y[0], pf, halves_of<FMT, 0>(a01), halves_of<FMT, 0>(b01));
-            mma(y[1], pf, halves_of<FMT, 1>(a01), halves_of<FMT, 1>(b01));
-            mma(y[2], pf, halves_of<FMT, 0>(a23), halves_of<FMT, 0>(b23));
-            mma(y[3], pf, halves_of<FMT, 1>(a23), halves_of<FMT, 1>(b23));
+            for (int k = 0; k < kWords; k++) {
+              if (odd)
 #pragma unroll
-            for (int c = 0; c < 4; c++)
+                for (int i = 0; i < 4; i++) w[i][k] &= ~__vcmpeq4(w[i][k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              float y[4][4] = {};
+              product(w, k, pf[s16], y);
 #pragma unroll
-              for (int i = 0; i < 4; i++) o[4 * k + c][i] += y[c][i] * fall;
+              for (int c = 0; c < 4; c++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) o[4 * k + c][i] += y[c][i] * fall;
+            }
           }
         }
       }
@@ -601,9 +791,10 @@ __global__ void __launch_bounds__(kThreads, kPerSM) k_attend(const AttendArgs a)
       // The four warps' parts of the item, joined in a fixed order.
 #pragma unroll
       for (int half = 0; half < 2; half++) {
-        l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
-        l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
-        if (t == 0) sm.m[warp][g + 8 * half] = m[half], sm.l[warp][g + 8 * half] = l[half];
+        float y = l[half].x + l[half].y;
+        y += __shfl_xor_sync(0xffffffffu, y, 1);
+        y += __shfl_xor_sync(0xffffffffu, y, 2);
+        if (t == 0) sm.m[warp][g + 8 * half] = m[half], sm.l[warp][g + 8 * half] = y;
       }
       __syncthreads();
       float top[2], sum[2];
@@ -634,9 +825,9 @@ __global__ void __launch_bounds__(kThreads, kPerSM) k_attend(const AttendArgs a)
           }
         __syncthreads();
       }
-      // who has units of this item
-      const int64_t u1 = item_u0 + cur.tiles - 1;
-      const int64_t c0 = ((item_u0 + 1) * ctas - 1) / total, c1 = ((u1 + 1) * ctas - 1) / total;
+      // who has tiles of this item
+      const int64_t first_tile = item_lo + skip, last_tile = item_lo + item_cost - 1;
+      const int64_t c0 = ((first_tile + 1) * ctas - 1) / total, c1 = ((last_tile + 1) * ctas - 1) / total;
       if (c0 == c1) {
         if (warp == 0)
 #pragma unroll
@@ -647,56 +838,103 @@ __global__ void __launch_bounds__(kThreads, kPerSM) k_attend(const AttendArgs a)
             for (int i = 0; i < D / 4; i++) y[i] = out_at<D>(o, half, i);
             if (r < a.T * a.G) write_row<BF16>(a, cur.b, h, r, y, D / 4 * t, top[half], sum[half], t == 0);
           }
-      } else {
+      } else if (warp == 0) {
         // slot 1: the CTA's last part, where another came before it
-        const int64_t begin = max(lo, item_u0);
-        float *part = a.parts + (2 * int64_t(blockIdx.x) + (begin > lo)) * kRows * (D + 2);
-        if (warp == 0)
+        const bool second = seg > 0;
+        float *part = a.parts + (2 * int64_t(blockIdx.x) + second) * kRows * (D + 2);
 #pragma unroll
-          for (int half = 0; half < 2; half++) {
-            const int r = g + 8 * half;
+        for (int half = 0; half < 2; half++) {
+          const int r = g + 8 * half;
 #pragma unroll
-            for (int i = 0; i < D / 4; i += 4)
-              *reinterpret_cast<float4 *>(part + r * D + D / 4 * t + i) =
-                  make_float4(out_at<D>(o, half, i), out_at<D>(o, half, i + 1), out_at<D>(o, half, i + 2), out_at<D>(o, half, i + 3));
-            if (t == 0) part[kRows * D + r] = top[half], part[kRows * D + kRows + r] = sum[half];
-          }
-        __threadfence();
-        __syncthreads();
-        if (threadIdx.x == 0)
-          sm.last = atomicAdd(&a.count[int64_t(cur.b) * a.HR + cur.hr], 1) == int(c1 - c0);
-        __syncthreads();
-        if (sm.last) {
-          __threadfence();
-          auto slot_of = [&](int64_t c) {  // every part but the first is the first of its CTA
-            return a.parts + (2 * c + (c == c0 && total * c / ctas < item_u0)) * kRows * (D + 2);
-          };
-          constexpr int kLanes = D / 8;  // threads of a row, eight channels each
-          const int rows = min(kRows, a.T * a.G - r0);
-          for (int r = threadIdx.x / kLanes; r < rows; r += kThreads / kLanes) {
-            const int ch = threadIdx.x % kLanes * 8;
-            float tp = -INFINITY, sum_l = 0.0f, y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            for (int64_t c = c0; c <= c1; c++) tp = fmaxf(tp, __ldcg(slot_of(c) + kRows * D + r));
-#pragma unroll 4
-            for (int64_t c = c0; c <= c1; c++) {
-              const float *p = slot_of(c);
-              const float mm = __ldcg(p + kRows * D + r), f = mm == -INFINITY ? 0.0f : ex2(mm - tp);
-              sum_l += f * __ldcg(p + kRows * D + kRows + r);
-              const float4 y0 = __ldcg(reinterpret_cast<const float4 *>(p + r * D + ch));
-              const float4 y1 = __ldcg(reinterpret_cast<const float4 *>(p + r * D + ch + 4));
-              y[0] += f * y0.x, y[1] += f * y0.y, y[2] += f * y0.z, y[3] += f * y0.w;
-              y[4] += f * y1.x, y[5] += f * y1.y, y[6] += f * y1.z, y[7] += f * y1.w;
-            }
-            write_row<BF16>(a, cur.b, h, r0 + r, y, ch, tp, sum_l, ch == 0);
-          }
+          for (int i = 0; i < D / 4; i += 4)
+            *reinterpret_cast<float4 *>(part + r * D + D / 4 * t + i) =
+                make_float4(out_at<D>(o, half, i), out_at<D>(o, half, i + 1), out_at<D>(o, half, i + 2), out_at<D>(o, half, i + 3));
+          if (t == 0) part[kRows * D + r] = top[half], part[kRows * D + kRows + r] = sum[half];
+        }
+        if (lane == 0 && int64_t(blockIdx.x) == c0) {
+          Note &note = a.notes[blockIdx.x];
+          note.parts = int(c1 - c0 + 1), note.second = second, note.b = cur.b, note.h = h, note.rt = cur.rt;
         }
       }
       first = true;
-      item_u0 += cur.tiles;
+      seg++;
+      item_lo += item_cost;
+      if (u + 1 < units) {
+        next_item(a, cur);
+        item_cost = cost_of(cur.tiles);
+      }
+    } else {
+      cur.tile++;
     }
-    if (u + 1 < units) step(a, cur);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0) a.notes[blockIdx.x].errors = sm.errors;
+}
+
+// Joins the parts of items that several CTAs had: one CTA per CTA that has the
+// first part of such an item, and four rows; a warp per row, four channels a
+// lane, sixteen parts' loads in flight.  It is launched with the first kernel
+// and waits for its end here.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(128) k_join(const AttendArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && blockIdx.y == 0) {  // the status of the call
+    __shared__ uint32_t s_errors;
+    if (threadIdx.x == 0) s_errors = 0;
+    __syncthreads();
+    uint32_t e = 0;
+    for (int i = threadIdx.x; i < int(gridDim.x); i += 128) e |= __ldcg(&a.notes[i].errors);
+    if (e) atomicOr(&s_errors, e);
+    __syncthreads();
+    if (threadIdx.x == 0) *a.status = s_errors;
+  }
+  const Note note = a.notes[blockIdx.x];
+  const int r = blockIdx.y * 4 + warp, row = note.rt * kRows + r;
+  if (note.parts == 0 || row >= a.T * a.G) return;
+  auto part = [&](int i) { return a.parts + (2 * (int64_t(blockIdx.x) + i) + (i == 0 ? note.second : 0)) * kRows * (D + 2); };
+  float top = -INFINITY, sum = 0.0f, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int base = 0; base < note.parts; base += 32) {
+    const int n = min(32, note.parts - base);
+    float m = -INFINITY, l = 0.0f;  // lane i: of part base + i
+    if (lane < n) m = __ldcg(part(base + lane) + kRows * D + r), l = __ldcg(part(base + lane) + kRows * D + kRows + r);
+    float now = m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
+    now = fmaxf(now, top);
+    const float keep = top == -INFINITY ? 0.0f : ex2(top - now);
+    const float w = m == -INFINITY ? 0.0f : ex2(m - now);
+    top = now;
+    sum *= keep;
+#pragma unroll
+    for (int k = 0; k < 4; k++) y[k] *= keep;
+    float lw = l * w;  // of a part that saw nothing 0, of one with a NaN a NaN
+#pragma unroll
+    for (int o = 16; o; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+    sum += lw;
+    for (int i0 = 0; i0 < n; i0 += 16) {
+      float4 v[16];
+#pragma unroll
+      for (int i = 0; i < 16; i++)
+        if (i0 + i < n && lane * 4 < D) v[i] = __ldcg(reinterpret_cast<const float4 *>(part(base + i0 + i) + r * D) + lane);
+#pragma unroll
+      for (int i = 0; i < 16; i++)
+        if (i0 + i < n) {
+          const float f = __shfl_sync(0xffffffffu, w, i0 + i);
+          if (lane * 4 < D) y[0] += f * v[i].x, y[1] += f * v[i].y, y[2] += f * v[i].z, y[3] += f * v[i].w;
+        }
+    }
+  }
+  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int t = row / a.G;
+  const int64_t at = (int64_t(note.b) * a.T + t) * a.Hq + note.h * a.G + row % a.G;
+  if (lane * 4 < a.d) {
+    const uint32_t w0 = uint32_t(elem_of<BF16>(y[0] * f)) | uint32_t(elem_of<BF16>(y[1] * f)) << 16;
+    const uint32_t w1 = uint32_t(elem_of<BF16>(y[2] * f)) | uint32_t(elem_of<BF16>(y[3] * f)) << 16;
+    *reinterpret_cast<uint2 *>(a.out + at * a.d + lane * 4) = make_uint2(w0, w1);
+  }
+  if (lane == 0 && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (top - kLift + log2f(sum)) * 0.6931471805599453f;
 }
 
 int row_tiles(const cg_cache *c, const cg_attend *t) {
@@ -710,21 +948,33 @@ bool attend_ok(const cg_cache *c, const cg_attend *t) {
   for (int64_t s : t->q_stride)
     if (s % 8) return false;
   return t->n_seq <= (1 << 20) && t->q_tokens <= (1 << 16) && t->Hq <= 65535 &&
-         int64_t(t->n_seq) * c->H * row_tiles(c, t) <= (1 << 28);
+         int64_t(t->q_tokens) * (t->Hq / c->H) <= (1 << 28) && int64_t(t->n_seq) * c->H * row_tiles(c, t) <= (1 << 28);
 }
 
-uint64_t counts_bytes(const cg_cache *c, const cg_attend *t) {
-  return pad256(256 + 4 * uint64_t(t->n_seq) * c->H * row_tiles(c, t));
-}
+constexpr uint64_t kNotes = 256 + ((sizeof(Note) * kGrid + 255) & ~uint64_t(255));  // the status word, then the notes
 
 int padded(int d) { return d <= 64 ? 64 : 128; }
 
+template <int FMT, int D, bool BF16, bool PLAIN>
+cudaError_t launch_kernel(const AttendArgs &a, unsigned grid, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(k_attend<FMT, D, BF16, PLAIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             int(sizeof(Smem<D>)));
+  if (e != cudaSuccess) return e;
+  k_attend<FMT, D, BF16, PLAIN><<<grid, kThreads, sizeof(Smem<D>), st>>>(a);
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid, unsigned((min(kRows, a.T * a.G) + 3) / 4)), cfg.blockDim = dim3(128), cfg.stream = st;
+  cfg.attrs = &early, cfg.numAttrs = 1;
+  const cudaError_t e2 = cudaLaunchKernelEx(&cfg, k_join<D, BF16>, a);
+  return e2 != cudaSuccess ? e2 : cudaGetLastError();
+}
+
 template <int FMT, int D, bool BF16>
 cudaError_t launch(const AttendArgs &a, unsigned grid, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(k_attend<FMT, D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(Smem<D>)));
-  if (e != cudaSuccess) return e;
-  k_attend<FMT, D, BF16><<<grid, kThreads, sizeof(Smem<D>), st>>>(a);
-  return cudaGetLastError();
+  return a.bt % 16 == 0 && a.d == D ? launch_kernel<FMT, D, BF16, true>(a, grid, st)
+                                    : launch_kernel<FMT, D, BF16, false>(a, grid, st);
 }
 
 template <int FMT>
@@ -739,7 +989,7 @@ cudaError_t launch_format(const AttendArgs &a, bool bf16, unsigned grid, cudaStr
 extern "C" size_t cg_cache_workspace_bytes(const cg_cache *cache, const cg_attend *attend) {
   using namespace cg;
   if (!attend_ok(cache, attend)) return 0;
-  return size_t(counts_bytes(cache, attend) + 4 * uint64_t(2 * kGrid) * kRows * (padded(cache->d) + 2));
+  return size_t(kNotes + 4 * uint64_t(2 * kGrid) * kRows * (padded(cache->d) + 2));
 }
 
 extern "C" cg_status cg_cache_attend(const cg_cache *cache, const cg_attend *attend, const void *q_dev,
@@ -757,21 +1007,20 @@ extern "C" cg_status cg_cache_attend(const cg_cache *cache, const cg_attend *att
     return CG_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t *ws = static_cast<uint8_t *>(ws_dev);
-  const uint64_t counts = counts_bytes(cache, attend);
-  if (cudaMemsetAsync(ws, 0, counts, st) != cudaSuccess) return CG_ERR_CUDA;
   AttendArgs a{};
   a.q = static_cast<const uint16_t *>(q_dev);
   a.kp = static_cast<const uint8_t *>(k_pool), a.vp = static_cast<const uint8_t *>(v_pool);
   a.ks = k_scale, a.vs = v_scale, a.table = table_dev, a.len = len_dev;
   a.out = static_cast<uint16_t *>(out_dev), a.lse = lse_dev;
   a.status = reinterpret_cast<uint32_t *>(ws);
-  a.count = reinterpret_cast<int32_t *>(ws + 256);
-  a.parts = reinterpret_cast<float *>(ws + counts);
+  a.notes = reinterpret_cast<Note *>(ws + 256);
+  a.parts = reinterpret_cast<float *>(ws + kNotes);
   a.q_seq = attend->q_stride[0], a.q_tok = attend->q_stride[1], a.q_head = attend->q_stride[2];
   a.B = attend->n_seq, a.T = attend->q_tokens, a.Hq = attend->Hq, a.H = cache->H, a.d = cache->d;
-  a.G = a.Hq / a.H, a.HR = a.H * row_tiles(cache, attend);
+  a.G = a.Hq / a.H, a.RT = row_tiles(cache, attend), a.HR = a.H * a.RT;
   a.bt = cache->block_tokens, a.n_blocks = cache->n_blocks, a.stride = attend->table_stride;
   a.scale_log2 = attend->scale * 1.4426950408889634f;
+  a.by_bt = Divisor(uint32_t(a.bt));
   const int64_t most = (int64_t(a.stride) * a.bt + kUnit - 1) / kUnit;  // units of an item
   const int64_t items = int64_t(a.B) * a.HR;
   const unsigned grid = unsigned(most >= kGrid || items * most >= kGrid ? kGrid : items * most);
