@@ -1,0 +1,88 @@
+// cg_tma.cuh -- tensor maps, mbarriers and tiled copies, shared by the
+// attention kernels.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace cg {
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's cuTensorMapEncodeTiled, found once (the library does not link against the driver).
+inline EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess) {
+      (void)cudaGetLastError();
+      p = nullptr;
+    }
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+__device__ inline uint32_t smem_of(const void *p) { return uint32_t(__cvta_generic_to_shared(p)); }
+
+__device__ inline void bar_init(uint64_t *bar, int count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_of(bar)), "r"(count) : "memory");
+}
+
+// Makes initialised barriers visible to the async proxy.
+__device__ inline void bar_init_fence() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
+
+__device__ inline void bar_expect(uint64_t *bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_of(bar)), "r"(bytes) : "memory");
+}
+
+__device__ inline void bar_arrive(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_of(bar)) : "memory");
+}
+
+__device__ inline bool bar_try(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{.reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p;}"
+      : "=r"(ok)
+      : "r"(smem_of(bar)), "r"(parity)
+      : "memory");
+  return ok;
+}
+
+// A wait ends after this many tries (each suspends the thread for a while, so
+// that this is seconds, where a tile takes microseconds); false means that the
+// memory system failed.
+constexpr int kWaitTries = 1 << 22;
+
+__device__ inline bool bar_wait(uint64_t *bar, uint32_t parity) {
+  for (int i = 0; i < kWaitTries; i++)
+    if (bar_try(bar, parity)) return true;
+  return false;
+}
+
+__device__ inline void tma_2d(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+               "l"(map), "r"(smem_of(bar)), "r"(x), "r"(y)
+               : "memory");
+}
+
+__device__ inline void tma_3d(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+               "l"(map), "r"(smem_of(bar)), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
+__device__ inline void tma_prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// Orders this thread's accesses of shared memory before later ones of the async proxy.
+__device__ inline void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+}  // namespace cg
