@@ -112,7 +112,7 @@ struct Smem {
   uint32_t valid[kWarps][kStages];
   int64_t sum[kWarps][2], prefix;
   int most[kWarps], b;
-  uint32_t errors;
+  uint32_t errors, dead;
   int len[kLens];
 };
 
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, Shape<NB>::kPerSM) k_attend(const __
 
   asm volatile("griddepcontrol.launch_dependents;");
   if (threadIdx.x == 0) {
-    sm.errors = 0;
+    sm.errors = sm.dead = 0;
     a.notes[blockIdx.x].parts = 0;
   }
   // The items of the call and what they cost.  An item costs its units and
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, Shape<NB>::kPerSM) k_attend(const __
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
     const int s = slot_now;
     bool landed = true;
-    if (PLAIN) landed = bar_wait(&sm.full[warp][s], phase);
+    if (PLAIN) landed = bar_wait(&sm.full[warp][s], phase, &sm.dead);
     if (!landed) atomicOr(&sm.errors, kStTimeout);
     __syncwarp();
     if (++slot_now == kStages) slot_now = 0, phase ^= 1;

@@ -1,73 +1,676 @@
 // cg_prompt.cu -- cg_prompt_attend: causal attention of packed prompts.
+//
+// The G = Hq / H query heads that share a KV head are rows of one matrix: row
+// r of a tile of 128 is token r / G, head r % G (128 / G tokens, whole ones).
+// An item is two such tiles, a and b, of one sequence and KV head; it goes over
+// its keys in tiles of 128, and per tile and 128 rows there are two products of
+// 128 x 128 x d on tcgen05: S = Q K^T into TMEM, and O += P V with P, the
+// probabilities in the rows' type, read back from TMEM.
+//
+// What bounds it is those products (4 d operations a visible pair); the
+// exponentials come next.  So the two tiles take turns: while the tensor cores
+// work for one, a warpgroup computes the other's probabilities, one row a
+// thread.  Warps: 0-3 and 4-7 the softmax of tiles a and b, 8 the loads (TMA),
+// 9 the products.  TMEM: S of both tiles (P lies over S), O of both.
+//
+//   products:  S_a(0) S_b(0) | PV_a(j) S_a(j+1) PV_b(j) S_b(j+1) ...
+//   softmax a: waits for S_a(j): maximum, exponentials, P_a(j); O_a is scaled
+//              only when a maximum grows by more than 2^8
+//
+// A product is issued when its operands are there; tcgen05 runs them in the
+// order of issue, so S_a(j+1) may overwrite P_a(j) behind PV_a(j), and S_a(j+1)
+// being done says that O_a rests.
+//
+// The key tiles of all items are dealt in equal runs to one CTA per SM: the
+// causal triangle needs no other balance, and a short question on a long
+// context takes the whole GPU.  What a CTA has of an item that others share goes
+// to the workspace as maximum, sum and output, and a second kernel joins the
+// parts in their order.
 #include "cg_cache.cuh"
+#include "cg_tma.cuh"
 
 namespace cg {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 384;
+// Registers a thread: 384 are launched with 168 each; the softmax warpgroups
+// take 208, which the third leaves them (2 * 208 + 80 <= 3 * 168).
+constexpr int kSoftRegs = 208, kOtherRegs = 80;
+constexpr int kTile = 128;   // rows of a tile, keys of a tile
+constexpr int kRows = 2 * kTile;
+constexpr int kGrid = kSMs;
+constexpr int kShort = 4;    // key tiles of an item that one CTA takes where items are few
+constexpr float kLift = 7.0f, kLag = 8.0f;  // p = 2^(s - m + kLift) < 2^15, m at most kLag under the maximum
+
+struct Note {
+  uint32_t errors;
+  int32_t parts;   // of the item that this CTA has the first but not the last part of, or 0
+  int32_t second;  // the first part is in this CTA's second slot
+  int32_t b, h, q;
+};
 
 struct PromptArgs {
-  const uint16_t *q, *k, *v;
+  CUtensorMap q_map, k_map, v_map;
   const int32_t *cu_q, *cu_k;
   uint16_t *out;
   float *lse;
   uint32_t *status;
-  int64_t qs[2], ks[2], vs[2];
-  int n_seq, Hq, H, d, max_q, max_k, n_q, n_k;
+  Note *notes;
+  float *parts;  // [2 * kGrid][kRows][D + 2]
+  int n_seq, Hq, H, G, TG, W, d, max_q, max_k, n_q, n_k;  // TG: tokens of a tile; W: of an item
   float scale_log2;  // scale * log2(e)
 };
 
-// One CTA per (query row of a sequence, head); each warp takes every fourth
-// key and keeps its own running maximum, sum and output.
+template <int D>
+struct Smem {
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kChunks = D / 64;  // of 64 channels: 128 bytes, a swizzled row
+  uint8_t q[2][kChunks][kTile * 128];
+  uint8_t kv[kStages][kChunks][kTile * 128];
+  uint64_t q_full, q_empty, kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2], o_full[2];
+  uint32_t tmem, errors, dead;
+  int most[kThreads / 32], b;
+  int64_t sum[kThreads / 32][2], prefix;
+};
+
+// ---- items ------------------------------------------------------------------
+// sum of floor((a i + b) / m), i < n; a, b >= 0
+__device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+  int64_t r = 0;
+  while (n > 0) {
+    r += (n - 1) * n / 2 * (a / m) + n * (b / m);
+    a %= m, b %= m;
+    const int64_t top = a * n + b;
+    if (top < m) break;
+    n = top / m, b = top % m;
+    const int64_t t = m;
+    m = a, a = t;
+  }
+  return r;
+}
+
+struct Seq {
+  int q0, nq, k0, nk, items;
+};
+
+__device__ inline bool load_seq(const PromptArgs &a, int b, Seq &s) {
+  s.q0 = a.cu_q[b], s.k0 = a.cu_k[b];
+  const int q1 = a.cu_q[b + 1], k1 = a.cu_k[b + 1];
+  s.nq = q1 - s.q0, s.nk = k1 - s.k0;
+  const bool ok = s.q0 >= 0 && q1 >= s.q0 && q1 <= a.n_q && s.nq <= a.max_q && s.k0 >= 0 && k1 >= s.k0 && k1 <= a.n_k && s.nk <= a.max_k;
+  if (!ok) s.nq = 0;
+  s.items = (s.nq + a.W - 1) / a.W;
+  return ok;
+}
+
+// Key tiles that tokens before `tok` of a sequence see; at least one, so that
+// every row gets an output.
+__device__ inline int key_tiles(const Seq &s, int tok) {
+  const int64_t seen = min(int64_t(s.nk), int64_t(s.nk) - s.nq + tok);
+  return seen <= kTile ? 1 : int((seen + kTile - 1) / kTile);
+}
+
+// What the items before item i of a sequence and head cost: each its key
+// tiles and one more (its way in and out take about as long).
+__device__ inline int64_t cost_before(const PromptArgs &a, const Seq &s, int i) {
+  const bool all = i == s.items && i > 0;  // the last item may be a short one
+  const int64_t n = all ? i - 1 : i;
+  const int64_t base = int64_t(s.nk) - s.nq;  // item j < items - 1 sees base + (j + 1) W keys
+  const int64_t ones = max(int64_t(0), min(n, base > kTile ? int64_t(0) : (kTile - base) / a.W));
+  return n + ones + floor_sum(n - ones, kTile, a.W, base + (ones + 1) * a.W + kTile - 1) + (all ? key_tiles(s, s.nq) + 1 : 0);
+}
+
+struct Walk {
+  Seq s;
+  int b, h, q, n;   // item q of sequence b, head h, with n key tiles
+  int64_t lo;       // where its cost begins
+};
+
+__device__ inline void set_item(const PromptArgs &a, Walk &w) { w.n = key_tiles(w.s, min(w.s.nq, (w.q + 1) * a.W)); }
+
+// The next item; the caller knows that there is one.
+__device__ inline void next_item(const PromptArgs &a, Walk &w, int skip) {
+  w.lo += skip ? w.n + 1 : 1;
+  if (++w.q == w.s.items) {
+    w.q = 0;
+    if (++w.h == a.H) {
+      w.h = 0;
+      do {
+        w.b++;
+        load_seq(a, w.b, w.s);
+      } while (w.s.items == 0);
+    }
+  }
+  set_item(a, w);
+}
+
+// A part of an item: key tiles j0 .. j0 + max(cnt) - 1, of which tile a of the rows
+// has the first cnt[0] and tile b the first cnt[1].
+struct Part {
+  int b, h, q, q0, nq, k0, nk, j0, tok[2], cnt[2];
+  int64_t lo, cost;
+};
+
+// The parts of a CTA's run [lo, hi), one after the other.
+struct Run {
+  Walk w;
+  int64_t at, hi;
+  int skip;  // 1: costs; 0: each item is one
+
+  __device__ bool next(const PromptArgs &a, Part &p) {
+    while (at < hi) {
+      const int64_t cost = skip ? w.n + 1 : 1, end = min(hi, w.lo + cost);
+      const int j0 = skip ? int(max(int64_t(0), at - w.lo - 1)) : 0, j1 = skip ? int(max(int64_t(0), end - w.lo - 1)) : w.n;
+      p.b = w.b, p.h = w.h, p.q = w.q, p.q0 = w.s.q0, p.nq = w.s.nq, p.k0 = w.s.k0, p.nk = w.s.nk, p.j0 = j0, p.lo = w.lo, p.cost = cost;
+      for (int t = 0; t < 2; t++) {
+        p.tok[t] = w.q * a.W + t * a.TG;
+        const int n = p.tok[t] < w.s.nq ? key_tiles(w.s, min(w.s.nq, p.tok[t] + a.TG)) : 0;
+        p.cnt[t] = max(0, min(j1, n) - j0);
+      }
+      at = end;
+      if (at < hi) next_item(a, w, skip);
+      if (j1 > j0) return true;
+    }
+    return false;
+  }
+};
+
+// ---- tcgen05 ----------------------------------------------------------------
+// Operands in shared memory: rows of 128 bytes, swizzled; eight rows make 1024
+// bytes.  For a K-major operand the stride between groups of eight rows is
+// 1024; for V, whose rows are keys, 1024 is the stride between groups of eight
+// keys and `lead` the one between groups of 64 channels.
+__device__ inline uint64_t operand(uint32_t addr, uint32_t lead) {
+  return uint64_t(addr >> 4 & 0x3fff) | uint64_t(lead >> 4) << 16 | uint64_t(1024 >> 4) << 32 | uint64_t(1) << 46 | uint64_t(2) << 61;
+}
+
+__device__ inline void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{.reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+      "r"(uint32_t(add))
+      : "memory");
+}
+
+__device__ inline void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{.reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+      "r"(uint32_t(add))
+      : "memory");
+}
+
+// The barrier gets an arrival when all products issued so far are done.
+__device__ inline void mma_commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_of(bar)) : "memory");
+}
+
+__device__ inline void tm_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ inline void tm_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ inline void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ inline void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+#define CG_R8(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), "=r"(x[i + 4]), "=r"(x[i + 5]), "=r"(x[i + 6]), "=r"(x[i + 7])
+#define CG_I8(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]), "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
+
+// 32 columns of this thread's lane.
+__device__ inline void tm_load(uint32_t addr, uint32_t *x) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,"
+      "%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : CG_R8(x, 0), CG_R8(x, 8), CG_R8(x, 16), CG_R8(x, 24)
+      : "r"(addr));
+}
+
+__device__ inline void tm_store32(uint32_t addr, const uint32_t *x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
+      "%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      CG_I8(x, 0), CG_I8(x, 8), CG_I8(x, 16), CG_I8(x, 24)
+      : "memory");
+}
+
+__device__ inline void tm_store16(uint32_t addr, const uint32_t *x) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+               CG_I8(x, 0), CG_I8(x, 8)
+               : "memory");
+}
+
+// ---- arithmetic ---------------------------------------------------------------
+__device__ inline float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ inline float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+__device__ inline float2 fma2(float2 a, float2 b, float2 c) {
+  float2 y;
+  asm("{.reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7};"
+      " fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d;}"
+      : "=f"(y.x), "=f"(y.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return y;
+}
+__device__ inline float2 add2(float2 a, float2 b) {
+  float2 y;
+  asm("{.reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d;}"
+      : "=f"(y.x), "=f"(y.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
+}
+__device__ inline float2 mul2(float2 a, float2 b) {
+  float2 y;
+  asm("{.reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mul.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d;}"
+      : "=f"(y.x), "=f"(y.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
+}
+
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) k_prompt(const PromptArgs a) {
-  const int b = blockIdx.y, i = blockIdx.x, hq = blockIdx.z, h = hq / (a.Hq / a.H);
+__device__ inline uint32_t pack(float lo, float hi) {
+  uint32_t r;
+  if (BF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// ---- the kernel -----------------------------------------------------------------
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ PromptArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Smem<D> &sm = *reinterpret_cast<Smem<D> *>(smem_raw);
+  constexpr int kStages = Smem<D>::kStages, kChunks = Smem<D>::kChunks;
+  constexpr uint32_t kTileBytes = kChunks * kTile * 128;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int q0 = a.cu_q[b], nq = a.cu_q[b + 1] - q0, k0 = a.cu_k[b], nk = a.cu_k[b + 1] - k0;
-  if (q0 < 0 || nq < 0 || nq > a.max_q || nq > a.n_q - q0 || k0 < 0 || nk < 0 || nk > a.max_k || nk > a.n_k - k0) {
-    if (i == 0 && hq == 0 && threadIdx.x == 0) atomicOr(a.status, kStBadArg);
-    return;
+
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (threadIdx.x == 0) {
+    sm.errors = sm.dead = 0;
+    a.notes[blockIdx.x].parts = 0;
+    bar_init(&sm.q_full, 1), bar_init(&sm.q_empty, 1);
+    for (int i = 0; i < kStages; i++) bar_init(&sm.kv_full[i], 1), bar_init(&sm.kv_empty[i], 1);
+    for (int t = 0; t < 2; t++) bar_init(&sm.s_full[t], 1), bar_init(&sm.p_full[t], kTile), bar_init(&sm.o_full[t], 1);
+    bar_init_fence();
   }
-  if (i >= nq) return;
-  const int seen = i + nk - nq + 1;
-  const uint16_t *q = a.q + int64_t(q0 + i) * a.qs[0] + hq * a.qs[1];
-  float qf[4], o[4] = {0.0f, 0.0f, 0.0f, 0.0f}, m = -INFINITY, l = 0.0f;
-#pragma unroll
-  for (int x = 0; x < 4; x++) qf[x] = 4 * lane + x < a.d ? elem<BF16>(q[4 * lane + x]) : 0.0f;
-  for (int j = warp; j < seen; j += kThreads / 32) {
-    uint2 kc = make_uint2(0, 0), vc = make_uint2(0, 0);
-    if (4 * lane < a.d) {
-      kc = *reinterpret_cast<const uint2 *>(a.k + int64_t(k0 + j) * a.ks[0] + h * a.ks[1] + 4 * lane);
-      vc = *reinterpret_cast<const uint2 *>(a.v + int64_t(k0 + j) * a.vs[0] + h * a.vs[1] + 4 * lane);
-    }
-    float s = 0.0f;
-#pragma unroll
-    for (int x = 0; x < 4; x++) s += qf[x] * elem<BF16>(uint16_t((x < 2 ? kc.x : kc.y) >> (16 * (x & 1))));
-#pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= a.scale_log2;
-    const float top = fmaxf(m, s), keep = exp2f(m - top), p = exp2f(s - top);
-    l = l * keep + p;
-#pragma unroll
-    for (int x = 0; x < 4; x++) o[x] = o[x] * keep + p * elem<BF16>(uint16_t((x < 2 ? vc.x : vc.y) >> (16 * (x & 1))));
-    m = top;
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_of(&sm.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  __shared__ float s_m[4], s_l[4], s_o[4][128];
-  if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+  // The items of the call and what they cost.
+  const int per = (a.n_seq + kThreads - 1) / kThreads, b0 = threadIdx.x * per, b1 = min(a.n_seq, b0 + per);
+  int64_t cost = 0, items = 0;
+  int most = 0;
+  bool bad = false;
+  for (int b = b0; b < b1; b++) {
+    Seq s;
+    bad |= !load_seq(a, b, s);
+    if (s.items == 0) continue;
+    cost += cost_before(a, s, s.items) * a.H;
+    items += int64_t(s.items) * a.H;
+    most = max(most, key_tiles(s, s.nq));
+  }
+  int64_t cost_to = cost, items_to = items;
 #pragma unroll
-  for (int x = 0; x < 4; x++) s_o[warp][4 * lane + x] = o[x];
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, cost_to, o), z = __shfl_up_sync(0xffffffffu, items_to, o);
+    if (lane >= o) cost_to += y, items_to += z;
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) sm.sum[warp][0] = cost_to, sm.sum[warp][1] = items_to, sm.most[warp] = most;
+  tm_before();
   __syncthreads();
-  float top = -INFINITY, sum = 0.0f, x = 0.0f;
-  for (int w = 0; w < 4; w++) top = fmaxf(top, s_m[w]);
-  if (seen > 0)
-    for (int w = 0; w < 4; w++) {
-      const float f = s_m[w] == -INFINITY ? 0.0f : exp2f(s_m[w] - top);
-      sum += f * s_l[w];
-      x += f * s_o[w][threadIdx.x];
+  tm_after();
+  int64_t total = 0, n_items = 0;
+  for (int w = 0; w < kThreads / 32; w++) {
+    if (w < warp) cost_to += sm.sum[w][0], items_to += sm.sum[w][1];
+    total += sm.sum[w][0], n_items += sm.sum[w][1];
+    most = max(most, sm.most[w]);
+  }
+  const int skip = most <= kShort && n_items <= gridDim.x ? 0 : 1;  // 0: a CTA per item
+  if (!skip) total = n_items, cost = items, cost_to = items_to;
+  const int64_t before = cost_to - cost;
+  if (blockIdx.x == 0 && bad) atomicOr(&sm.errors, kStBadArg);
+  const int64_t ctas = min(int64_t(gridDim.x), total);
+  const int64_t lo = ctas ? total * blockIdx.x / ctas : 0, hi = ctas ? total * (blockIdx.x + 1) / ctas : 0;
+  const bool busy = int64_t(blockIdx.x) < ctas;
+  if (busy && lo >= before && lo < before + cost) {  // one thread's sequences hold the first cost
+    int64_t at = before;
+    int b = b0;
+    for (;; b++) {
+      Seq s;
+      load_seq(a, b, s);
+      const int64_t n = s.items == 0 ? 0 : (skip ? cost_before(a, s, s.items) : s.items) * a.H;
+      if (lo < at + n) break;
+      at += n;
     }
-  const int64_t r = int64_t(q0 + i) * a.Hq + hq;
-  if (int(threadIdx.x) < a.d) a.out[r * a.d + threadIdx.x] = elem_of<BF16>(sum == 0.0f ? 0.0f : x / sum);
-  if (threadIdx.x == 0 && a.lse) a.lse[r] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    sm.b = b;
+    sm.prefix = at;
+  }
+  __syncthreads();
+  const uint32_t tmem = sm.tmem;
+
+  if (busy) {
+    Run run;
+    run.at = lo, run.hi = hi, run.skip = skip;
+    Walk &w = run.w;
+    w.b = sm.b;
+    load_seq(a, w.b, w.s);
+    {
+      const int64_t head = skip ? cost_before(a, w.s, w.s.items) : w.s.items, in = lo - sm.prefix;
+      w.h = int(in / head);
+      const int64_t rest = in - w.h * head;
+      int l = 0, r = w.s.items - 1;  // the last item that begins at or before `rest`
+      while (l < r) {
+        const int mid = (l + r + 1) / 2;
+        if ((skip ? cost_before(a, w.s, mid) : mid) <= rest)
+          l = mid;
+        else
+          r = mid - 1;
+      }
+      w.q = l;
+      w.lo = sm.prefix + w.h * head + (skip ? cost_before(a, w.s, l) : l);
+      set_item(a, w);
+    }
+    Part p;
+    if (warp >= 8) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+      if (warp == 8) {
+      // ---- loads ----
+      if (lane == 0) {
+        int stage = 0;
+        uint32_t kv_phase = 1, q_phase = 1;  // the first pass over the ring finds it empty
+        bool ok = true;
+        const uint32_t q_bytes = uint32_t(kChunks) * 128 * a.G * a.TG;
+        while (ok && run.next(a, p)) {
+          const int n = max(p.cnt[0], p.cnt[1]);
+          if (!(ok = bar_wait(&sm.q_empty, q_phase, &sm.dead))) break;
+          q_phase ^= 1;
+          bar_expect(&sm.q_full, q_bytes * ((p.cnt[0] > 0) + (p.cnt[1] > 0)));
+          for (int t = 0; t < 2; t++)
+            if (p.cnt[t] > 0)
+              for (int c = 0; c < kChunks; c++) tma_3d(smem_of(sm.q[t][c]), &a.q_map, &sm.q_full, 64 * c, p.h * a.G, p.q0 + p.tok[t]);
+          for (int j = 0; j < 2 * n && ok; j++) {  // K, V, K, V ...
+            if (!(ok = bar_wait(&sm.kv_empty[stage], kv_phase, &sm.dead))) break;
+            bar_expect(&sm.kv_full[stage], kTileBytes);
+            const CUtensorMap *map = j & 1 ? &a.v_map : &a.k_map;
+            for (int c = 0; c < kChunks; c++)
+              tma_3d(smem_of(sm.kv[stage][c]), map, &sm.kv_full[stage], 64 * c, p.k0 + (p.j0 + j / 2) * kTile, p.h);
+            if (++stage == kStages) stage = 0, kv_phase ^= 1;
+          }
+        }
+      }
+    } else if (warp == 9) {
+      // ---- products ----
+      constexpr uint32_t kType = BF16 ? 1u : 0u;
+      constexpr uint32_t kCommon = 1u << 4 | kType << 7 | kType << 10 | uint32_t(kTile >> 4) << 24;
+      constexpr uint32_t kS = kCommon | uint32_t(kTile >> 3) << 17, kO = kCommon | 1u << 16 | uint32_t(D >> 3) << 17;
+      int stage = 0;
+      uint32_t kv_phase = 0, q_phase = 0, p_phase[2] = {0, 0};
+      bool ok = true;
+      auto advance = [&] {
+        if (++stage == kStages) stage = 0, kv_phase ^= 1;
+      };
+      auto s_product = [&](int t, int st) {  // S_t = Q_t K^T
+        if (lane == 0) {
+#pragma unroll
+          for (int k = 0; k < D / 16; k++)
+            mma_ss(tmem + t * kTile, operand(smem_of(sm.q[t][k / 4]) + k % 4 * 32, 16), operand(smem_of(sm.kv[st][k / 4]) + k % 4 * 32, 16), kS, k > 0);
+          mma_commit(&sm.s_full[t]);
+        }
+      };
+      while (ok && run.next(a, p)) {
+        const int n = max(p.cnt[0], p.cnt[1]);
+        ok = bar_wait(&sm.q_full, q_phase, &sm.dead) && bar_wait(&sm.kv_full[stage], kv_phase, &sm.dead);
+        if (!ok) break;
+        q_phase ^= 1;
+        tm_after();
+        for (int t = 0; t < 2; t++)
+          if (p.cnt[t] > 0) s_product(t, stage);
+        if (lane == 0) {
+          mma_commit(&sm.kv_empty[stage]);
+          if (n == 1) mma_commit(&sm.q_empty);
+        }
+        advance();
+        for (int j = 0; j < n && ok; j++) {
+          const int vs = stage;
+          const uint32_t v_phase = kv_phase;
+          advance();
+          const int ks = stage;
+          const uint32_t k_phase = kv_phase;
+          const bool more = j + 1 < n;
+          if (!(ok = bar_wait(&sm.kv_full[vs], v_phase, &sm.dead))) break;
+          const int left = p.nk - (p.j0 + j) * kTile;  // keys from here on
+          if (left < kTile) {  // what lies behind the last key must not reach a product: 0 * NaN
+            for (int i = lane; i < kTile * 8 * kChunks; i += 32)
+              if (i / 8 % kTile >= left) reinterpret_cast<uint4 *>(sm.kv[vs][0])[i] = make_uint4(0, 0, 0, 0);
+            fence_async();
+            __syncwarp();
+          }
+          for (int t = 0; t < 2 && ok; t++) {
+            if (j >= p.cnt[t]) continue;
+            if (!(ok = bar_wait(&sm.p_full[t], p_phase[t], &sm.dead))) break;
+            p_phase[t] ^= 1;
+            tm_after();
+            if (lane == 0)
+#pragma unroll
+              for (int k = 0; k < kTile / 16; k++)  // O_t += P_t V
+                mma_ts(tmem + 2 * kTile + t * kTile, tmem + t * kTile + k * 8, operand(smem_of(sm.kv[vs][0]) + k * 2048, kTile * 128), kO, j > 0 || k > 0);
+            if (j + 1 < p.cnt[t]) {
+              if (!(ok = bar_wait(&sm.kv_full[ks], k_phase, &sm.dead))) break;
+              s_product(t, ks);
+            } else if (lane == 0) {
+              mma_commit(&sm.o_full[t]);
+            }
+          }
+          if (!ok) break;
+          if (lane == 0) mma_commit(&sm.kv_empty[vs]);
+          if (more) {
+            if (lane == 0) {
+              mma_commit(&sm.kv_empty[ks]);
+              if (j + 2 == n) mma_commit(&sm.q_empty);
+            }
+            advance();
+          }
+        }
+      }
+      }
+    } else {
+      // ---- softmax: a row a thread ----
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+      const int t = warp >> 2, r = threadIdx.x & (kTile - 1);
+      const uint32_t row = uint32_t(warp & 3) << 21;  // the warp's lanes of TMEM
+      const uint32_t s_at = tmem + row + t * kTile, o_at = tmem + row + 2 * kTile + t * kTile;
+      uint32_t s_phase = 0, o_phase = 0;
+      bool ok = true;
+      int seg = 0;
+      const int my_tok = r / a.G, my_head = r % a.G;
+      const float2 sc = make_float2(a.scale_log2, a.scale_log2);
+      while (ok && run.next(a, p)) {
+        const int tok = p.tok[t] + my_tok;
+        const bool mine = my_tok < a.TG && tok < p.nq;
+        const int last = min(p.nk - 1, p.nk - p.nq + tok) - p.j0 * kTile;  // the last key seen, from the part's first
+        float m = -INFINITY;
+        float2 l = make_float2(0.0f, 0.0f);
+        for (int j = 0; j < p.cnt[t]; j++) {
+          if (!(ok = bar_wait(&sm.s_full[t], s_phase, &sm.dead))) break;
+          s_phase ^= 1;
+          tm_after();
+          uint32_t x[kTile];
+#pragma unroll
+          for (int i = 0; i < 4; i++) tm_load(s_at + 32 * i, x + 32 * i);
+          tm_wait_ld();
+          const int lim = last - j * kTile;
+          if (__any_sync(0xffffffffu, lim < kTile - 1)) {
+#pragma unroll
+            for (int i = 0; i < kTile; i++)
+              if (i > lim) x[i] = 0xff800000u;
+          }
+          float top[4];
+#pragma unroll
+          for (int i = 0; i < 4; i++) top[i] = fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 4]));
+#pragma unroll
+          for (int i = 8; i < kTile; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; k++) top[k] = max3(top[k], __uint_as_float(x[i + 2 * k]), __uint_as_float(x[i + 2 * k + 1]));
+          const float now = max3(top[0], top[1], fmaxf(top[2], top[3])) * a.scale_log2;
+          float keep = 1.0f;
+          if (now > m + kLag) keep = ex2(m - now), m = now;
+          if (j > 0 && __any_sync(0xffffffffu, keep != 1.0f)) {
+            l = mul2(l, make_float2(keep, keep));
+#pragma unroll
+            for (int c = 0; c < D / 32; c++) {
+              uint32_t y[32];
+              tm_load(o_at + 32 * c, y);
+              tm_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; i++) y[i] = __float_as_uint(__uint_as_float(y[i]) * keep);
+              tm_store32(o_at + 32 * c, y);
+            }
+          }
+          const float base = kLift - (m == -INFINITY ? 0.0f : m);
+#pragma unroll
+          for (int c = 0; c < 4; c++) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+              float2 y = make_float2(__uint_as_float(x[32 * c + 2 * i]), __uint_as_float(x[32 * c + 2 * i + 1]));
+              y = fma2(y, sc, make_float2(base, base));
+              y = make_float2(ex2(y.x), ex2(y.y));
+              l = add2(l, y);
+              pk[i] = pack<BF16>(y.x, y.y);
+            }
+            tm_store16(s_at + 16 * c, pk);
+          }
+          tm_wait_st();
+          tm_before();
+          bar_arrive(&sm.p_full[t]);
+        }
+        if (!ok) break;
+        const float sum = l.x + l.y;
+        const bool some = p.cnt[t] > 0;
+        if (some) {
+          if (!(ok = bar_wait(&sm.o_full[t], o_phase, &sm.dead))) break;
+          o_phase ^= 1;
+          tm_after();
+        }
+        // who has key tiles of this item
+        const int64_t first = p.lo + skip, end = p.lo + p.cost - 1;
+        const int64_t c0 = ((first + 1) * ctas - 1) / total, c1 = ((end + 1) * ctas - 1) / total;
+        const bool whole = c0 == c1;
+        float *part = a.parts + (2 * int64_t(blockIdx.x) + (seg > 0)) * kRows * (D + 2);  // slot 1: the run's last part
+        const int64_t at = (int64_t(p.q0) + tok) * a.Hq + p.h * a.G + my_head;
+        const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+        for (int c = 0; c < D / 32; c++) {
+          uint32_t y[32];
+          if (some) {
+            tm_load(o_at + 32 * c, y);
+            tm_wait_ld();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i++) y[i] = 0;
+          }
+          if (!mine) continue;
+          if (whole) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              if (32 * c + i >= a.d) continue;
+              uint32_t w4[4];
+#pragma unroll
+              for (int k = 0; k < 4; k++) w4[k] = pack<BF16>(__uint_as_float(y[i + 2 * k]) * f, __uint_as_float(y[i + 2 * k + 1]) * f);
+              *reinterpret_cast<uint4 *>(a.out + at * a.d + 32 * c + i) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<uint4 *>(part + (t * kTile + r) * D + 32 * c + i) = make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+          }
+        }
+        tm_before();
+        if (mine) {
+          if (whole) {
+            if (a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (m - kLift + log2f(sum)) * 0.6931471805599453f;
+          } else {
+            part[kRows * D + t * kTile + r] = m, part[kRows * (D + 1) + t * kTile + r] = sum;
+          }
+        }
+        if (!whole && threadIdx.x == 0 && int64_t(blockIdx.x) == c0) {
+          Note &note = a.notes[blockIdx.x];
+          note.parts = int(c1 - c0 + 1), note.second = seg > 0, note.b = p.b, note.h = p.h, note.q = p.q;
+        }
+        seg++;
+      }
+    }
+  }
+  __syncwarp();
+  tm_before();
+  __syncthreads();
+  tm_after();
+  if (sm.dead)  // what is in flight gets a moment to land
+    for (int i = 0; i < 1000; i++) __nanosleep(1000);
+  if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  if (threadIdx.x == 0) a.notes[blockIdx.x].errors = sm.errors | (sm.dead ? kStTimeout : 0);
+}
+
+// Joins the parts of items that several CTAs had: for a CTA that has the first
+// part of such an item, a warp per row, four channels a lane.  It is launched
+// with the first kernel and waits for its end here.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) k_prompt_join(const __grid_constant__ PromptArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && blockIdx.y == 0) {  // the status of the call
+    const uint32_t e = int(threadIdx.x) < int(gridDim.x) ? __ldcg(&a.notes[threadIdx.x].errors) : 0;
+    __shared__ uint32_t s_errors;
+    if (threadIdx.x == 0) s_errors = 0;
+    __syncthreads();
+    if (e) atomicOr(&s_errors, e);
+    __syncthreads();
+    if (threadIdx.x == 0) *a.status = s_errors;
+  }
+  const Note note = a.notes[blockIdx.x];
+  if (note.parts == 0) return;
+  const int r = blockIdx.y * 8 + warp, t = r / kTile, rt = r % kTile;
+  const int tok = note.q * a.W + t * a.TG + rt / a.G, q0 = a.cu_q[note.b];
+  if (rt / a.G >= a.TG || tok >= a.cu_q[note.b + 1] - q0) return;
+  auto part = [&](int i) { return a.parts + (2 * (int64_t(blockIdx.x) + i) + (i == 0 ? note.second : 0)) * kRows * (D + 2); };
+  float top = -INFINITY, sum = 0.0f, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int base = 0; base < note.parts; base += 32) {
+    const int n = min(32, note.parts - base);
+    float m = -INFINITY, l = 0.0f;  // lane i: of part base + i
+    if (lane < n) m = __ldcg(part(base + lane) + kRows * D + r), l = __ldcg(part(base + lane) + kRows * (D + 1) + r);
+    float now = m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
+    now = fmaxf(now, top);
+    const float keep = top == -INFINITY ? 0.0f : ex2(top - now), w = m == -INFINITY ? 0.0f : ex2(m - now);
+    top = now;
+    float lw = l * w;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+    sum = sum * keep + lw;
+#pragma unroll
+    for (int k = 0; k < 4; k++) y[k] *= keep;
+    for (int i0 = 0; i0 < n; i0 += 8) {
+      float4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; i++)
+        if (i0 + i < n && lane * 4 < D) v[i] = __ldcg(reinterpret_cast<const float4 *>(part(base + i0 + i) + r * D) + lane);
+#pragma unroll
+      for (int i = 0; i < 8; i++)
+        if (i0 + i < n) {
+          const float f = __shfl_sync(0xffffffffu, w, i0 + i);
+          if (lane * 4 < D) y[0] += f * v[i].x, y[1] += f * v[i].y, y[2] += f * v[i].z, y[3] += f * v[i].w;
+        }
+    }
+  }
+  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int64_t at = (int64_t(q0) + tok) * a.Hq + note.h * a.G + rt % a.G;
+  if (lane * 4 < a.d) *reinterpret_cast<uint2 *>(a.out + at * a.d + lane * 4) = make_uint2(pack<BF16>(y[0] * f, y[1] * f), pack<BF16>(y[2] * f, y[3] * f));
+  if (lane == 0 && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (top - kLift + log2f(sum)) * 0.6931471805599453f;
 }
 
 bool prompt_ok(const cg_prompt *p) {
@@ -80,10 +683,49 @@ bool prompt_ok(const cg_prompt *p) {
   return true;
 }
 
+int padded(int d) { return d <= 64 ? 64 : 128; }
+
+// the status word, then the notes
+constexpr uint64_t kNotes = 256 + ((sizeof(Note) * kGrid + 255) & ~uint64_t(255));
+
+// A map of rows of d elements with two strides, in boxes of 64 x n1 x n2.
+bool make_map(CUtensorMap *map, const void *base, int d, int64_t size1, int64_t stride1, int n1, int64_t size2, int64_t stride2, int n2) {
+  const EncodeTiled encode = encode_tiled();
+  if (!encode) return false;
+  // an extent of one needs no stride, but the map wants a positive one
+  if (size1 == 1) stride1 = d;
+  if (size2 == 1) stride2 = d;
+  const cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(size1), cuuint64_t(size2)};
+  const cuuint64_t strides[2] = {cuuint64_t(2 * stride1), cuuint64_t(2 * stride2)};
+  const cuuint32_t box[3] = {64, cuuint32_t(n1), cuuint32_t(n2)}, ones[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool BF16>
+cudaError_t launch(const PromptArgs &a, unsigned grid, cudaStream_t st) {
+  constexpr int kSmem = int(sizeof(Smem<D>));
+  const cudaError_t e = cudaFuncSetAttribute(k_prompt<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  k_prompt<D, BF16><<<grid, kThreads, kSmem, st>>>(a);
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid, kRows / 8), cfg.blockDim = dim3(256), cfg.stream = st;
+  cfg.attrs = &early, cfg.numAttrs = 1;
+  const cudaError_t e2 = cudaLaunchKernelEx(&cfg, k_prompt_join<D, BF16>, a);
+  return e2 != cudaSuccess ? e2 : cudaGetLastError();
+}
+
 }  // namespace
 }  // namespace cg
 
-extern "C" size_t cg_prompt_workspace_bytes(const cg_prompt *prompt) { return cg::prompt_ok(prompt) ? 256 : 0; }
+extern "C" size_t cg_prompt_workspace_bytes(const cg_prompt *prompt) {
+  using namespace cg;
+  if (!prompt_ok(prompt)) return 0;
+  return size_t(kNotes + 4 * uint64_t(2 * kGrid) * kRows * (padded(prompt->d) + 2));
+}
 
 extern "C" cg_status cg_prompt_attend(const cg_prompt *prompt, const void *q_dev, const void *k_dev,
                                       const void *v_dev, const int32_t *cu_q_dev, const int32_t *cu_k_dev,
@@ -96,21 +738,29 @@ extern "C" cg_status cg_prompt_attend(const cg_prompt *prompt, const void *q_dev
       ws_bytes < cg_prompt_workspace_bytes(prompt))
     return CG_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(ws_dev, 0, 256, st) != cudaSuccess) return CG_ERR_CUDA;
-  if (prompt->max_q == 0) return CG_OK;
+  uint8_t *ws = static_cast<uint8_t *>(ws_dev);
+  const cg_prompt &p = *prompt;
+  if (p.max_q == 0 || p.n_q == 0) return cudaMemsetAsync(ws, 0, 256, st) == cudaSuccess ? CG_OK : CG_ERR_CUDA;
   PromptArgs a{};
-  a.q = static_cast<const uint16_t *>(q_dev), a.k = static_cast<const uint16_t *>(k_dev);
-  a.v = static_cast<const uint16_t *>(v_dev);
   a.cu_q = cu_q_dev, a.cu_k = cu_k_dev;
-  a.out = static_cast<uint16_t *>(out_dev), a.lse = lse_dev, a.status = static_cast<uint32_t *>(ws_dev);
-  for (int i = 0; i < 2; i++) a.qs[i] = prompt->q_stride[i], a.ks[i] = prompt->k_stride[i], a.vs[i] = prompt->v_stride[i];
-  a.n_seq = prompt->n_seq, a.Hq = prompt->Hq, a.H = prompt->H, a.d = prompt->d;
-  a.max_q = prompt->max_q, a.max_k = prompt->max_k, a.n_q = prompt->n_q, a.n_k = prompt->n_k;
-  a.scale_log2 = prompt->scale * 1.4426950408889634f;
-  const dim3 grid(unsigned(a.max_q), unsigned(a.n_seq), unsigned(a.Hq));
-  if (prompt->dtype == CG_BF16)
-    k_prompt<true><<<grid, kThreads, 0, st>>>(a);
-  else
-    k_prompt<false><<<grid, kThreads, 0, st>>>(a);
-  return launched();
+  a.out = static_cast<uint16_t *>(out_dev), a.lse = lse_dev;
+  a.status = reinterpret_cast<uint32_t *>(ws);
+  a.notes = reinterpret_cast<Note *>(ws + 256);
+  a.parts = reinterpret_cast<float *>(ws + kNotes);
+  a.n_seq = p.n_seq, a.Hq = p.Hq, a.H = p.H, a.G = p.Hq / p.H, a.TG = kTile / a.G, a.W = 2 * a.TG, a.d = p.d;
+  a.max_q = p.max_q, a.max_k = p.max_k, a.n_q = p.n_q, a.n_k = p.n_k;
+  a.scale_log2 = p.scale * 1.4426950408889634f;
+  bool ok = make_map(&a.q_map, q_dev, p.d, p.Hq, p.q_stride[1], a.G, p.n_q, p.q_stride[0], a.TG);
+  if (p.n_k > 0) {
+    ok = ok && make_map(&a.k_map, k_dev, p.d, p.n_k, p.k_stride[0], kTile, p.H, p.k_stride[1], 1);
+    ok = ok && make_map(&a.v_map, v_dev, p.d, p.n_k, p.v_stride[0], kTile, p.H, p.v_stride[1], 1);
+  } else {  // no key is seen: what is loaded in its place is masked
+    ok = ok && make_map(&a.k_map, q_dev, p.d, p.n_q, p.q_stride[0], kTile, p.Hq, p.q_stride[1], 1);
+    a.v_map = a.k_map;
+  }
+  if (!ok) return CG_ERR_INVALID_ARG;  // strides that a tensor map cannot have
+  const bool bf16 = p.dtype == CG_BF16;
+  const cudaError_t e = p.d <= 64 ? (bf16 ? launch<64, true>(a, kGrid, st) : launch<64, false>(a, kGrid, st))
+                                  : (bf16 ? launch<128, true>(a, kGrid, st) : launch<128, false>(a, kGrid, st));
+  return e == cudaSuccess ? CG_OK : CG_ERR_CUDA;
 }

@@ -55,15 +55,22 @@ __device__ inline bool bar_try(uint64_t *bar, uint32_t parity) {
   return ok;
 }
 
-// A wait ends after this many tries (each suspends the thread for a while, so
-// that this is seconds, where a tile takes microseconds); false means that the
-// memory system failed.
-constexpr int kWaitTries = 1 << 22;
+// A wait ends when it takes this many cycles (about two seconds, where a tile
+// takes microseconds), or when another wait of the CTA has ended so; false
+// means that the memory system failed.
+constexpr long long kWaitCycles = 4000000000ll;
 
-__device__ inline bool bar_wait(uint64_t *bar, uint32_t parity) {
-  for (int i = 0; i < kWaitTries; i++)
-    if (bar_try(bar, parity)) return true;
-  return false;
+__device__ inline bool bar_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *dead) {
+  if (bar_try(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!bar_try(bar, parity)) {
+    if (*dead) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *dead = 1;
+      return false;
+    }
+  }
+  return true;
 }
 
 __device__ inline void tma_2d(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int y) {
