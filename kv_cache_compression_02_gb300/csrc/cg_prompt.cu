@@ -34,8 +34,8 @@ namespace {
 
 constexpr int kThreads = 384;
 // Registers a thread: 384 are launched with 168 each; the softmax warpgroups
-// take 208, which the third leaves them (2 * 208 + 80 <= 3 * 168).
-constexpr int kSoftRegs = 208, kOtherRegs = 80;
+// take 200, which the third leaves them (2 * 200 + 104 = 3 * 168).
+constexpr int kSoftRegs = 200, kOtherRegs = 104;
 constexpr int kTile = 128;   // rows of a tile, keys of a tile
 constexpr int kRows = 2 * kTile;
 constexpr int kGrid = kSMs;
@@ -63,11 +63,13 @@ struct PromptArgs {
 
 template <int D>
 struct Smem {
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kChunks = D / 64;  // of 64 channels: 128 bytes, a swizzled row
   uint8_t q[2][kChunks][kTile * 128];
   uint8_t kv[kStages][kChunks][kTile * 128];
   uint64_t q_full, q_empty, kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2], o_full[2];
+  uint8_t out[8][32 * 128];  // a softmax warp's rows on their way out, 64 channels at a time
+  int todo[2][4];            // for the products: of the item, by its turn: cnt[0], cnt[1], keys from its first on
   uint32_t tmem, errors, dead;
   int most[kThreads / 32], b;
   int64_t sum[kThreads / 32][2], prefix;
@@ -180,22 +182,30 @@ struct Run {
 // bytes.  For a K-major operand the stride between groups of eight rows is
 // 1024; for V, whose rows are keys, 1024 is the stride between groups of eight
 // keys and `lead` the one between groups of 64 channels.
-__device__ inline uint64_t operand(uint32_t addr, uint32_t lead) {
-  return uint64_t(addr >> 4 & 0x3fff) | uint64_t(lead >> 4) << 16 | uint64_t(1024 >> 4) << 32 | uint64_t(1) << 46 | uint64_t(2) << 61;
-}
+constexpr uint32_t kOperandHi = 1024 >> 4 | 1u << 14 | 2u << 29;
+__device__ inline uint32_t operand_lo(const void *p, uint32_t lead) { return smem_of(p) >> 4 | lead >> 4 << 16; }
 
-__device__ inline void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ inline void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{.reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-      "r"(uint32_t(add))
+      "{.reg .pred p; .reg .b64 a, b; setp.ne.u32 p, %5, 0; mov.b64 a, {%1, %3}; mov.b64 b, {%2, %3};"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;}" ::"r"(d), "r"(a), "r"(b), "r"(kOperandHi), "r"(idesc), "r"(uint32_t(add))
       : "memory");
 }
 
-__device__ inline void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ inline void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{.reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-      "r"(uint32_t(add))
+      "{.reg .pred p; .reg .b64 b; setp.ne.u32 p, %5, 0; mov.b64 b, {%2, %3}; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;}" ::"r"(d),
+      "r"(a), "r"(b), "r"(kOperandHi), "r"(idesc), "r"(uint32_t(add))
       : "memory");
+}
+
+// True in one thread of a warp that runs together.  (tcgen05 wants its operands
+// in uniform registers; a branch on this keeps them there, one on a lane's
+// number costs about 60 cycles an instruction.)
+__device__ inline bool elected() {
+  uint32_t ok;
+  asm volatile("{.reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p;}" : "=r"(ok));
+  return ok;
 }
 
 // The barrier gets an arrival when all products issued so far are done.
@@ -292,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
     a.notes[blockIdx.x].parts = 0;
     bar_init(&sm.q_full, 1), bar_init(&sm.q_empty, 1);
     for (int i = 0; i < kStages; i++) bar_init(&sm.kv_full[i], 1), bar_init(&sm.kv_empty[i], 1);
-    for (int t = 0; t < 2; t++) bar_init(&sm.s_full[t], 1), bar_init(&sm.p_full[t], kTile), bar_init(&sm.o_full[t], 1);
+    for (int t = 0; t < 2; t++) bar_init(&sm.s_full[t], 1), bar_init(&sm.p_full[t], kTile / 32), bar_init(&sm.o_full[t], 1);
     bar_init_fence();
   }
   if (warp == 9) {
@@ -380,14 +390,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
       if (warp == 8) {
       // ---- loads ----
       if (lane == 0) {
-        int stage = 0;
+        int stage = 0, turn = 0;
         uint32_t kv_phase = 1, q_phase = 1;  // the first pass over the ring finds it empty
         bool ok = true;
         const uint32_t q_bytes = uint32_t(kChunks) * 128 * a.G * a.TG;
-        while (ok && run.next(a, p)) {
+        for (;;) {
+          const bool more = run.next(a, p);
           const int n = max(p.cnt[0], p.cnt[1]);
           if (!(ok = bar_wait(&sm.q_empty, q_phase, &sm.dead))) break;
           q_phase ^= 1;
+          int *todo = sm.todo[turn];
+          if (!more) {  // the end
+            todo[0] = todo[1] = 0;
+            bar_arrive(&sm.q_full);
+            break;
+          }
+          todo[0] = p.cnt[0], todo[1] = p.cnt[1], todo[2] = p.nk - p.j0 * kTile;
+          turn ^= 1;
           bar_expect(&sm.q_full, q_bytes * ((p.cnt[0] > 0) + (p.cnt[1] > 0)));
           for (int t = 0; t < 2; t++)
             if (p.cnt[t] > 0)
@@ -407,29 +426,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
       constexpr uint32_t kType = BF16 ? 1u : 0u;
       constexpr uint32_t kCommon = 1u << 4 | kType << 7 | kType << 10 | uint32_t(kTile >> 4) << 24;
       constexpr uint32_t kS = kCommon | uint32_t(kTile >> 3) << 17, kO = kCommon | 1u << 16 | uint32_t(D >> 3) << 17;
-      int stage = 0;
+      constexpr uint32_t kChunk = kTile * 128 >> 4, kStage = kTileBytes >> 4;
+      const uint32_t q_lo = operand_lo(sm.q[0], 16), k_lo = operand_lo(sm.kv[0], 16), v_lo = operand_lo(sm.kv[0], kTile * 128);
+      int stage = 0, turn = 0;
       uint32_t kv_phase = 0, q_phase = 0, p_phase[2] = {0, 0};
       bool ok = true;
       auto advance = [&] {
         if (++stage == kStages) stage = 0, kv_phase ^= 1;
       };
       auto s_product = [&](int t, int st) {  // S_t = Q_t K^T
-        if (lane == 0) {
+        const uint32_t a0 = q_lo + t * kStage, b0 = k_lo + st * kStage;
+        if (elected()) {
 #pragma unroll
           for (int k = 0; k < D / 16; k++)
-            mma_ss(tmem + t * kTile, operand(smem_of(sm.q[t][k / 4]) + k % 4 * 32, 16), operand(smem_of(sm.kv[st][k / 4]) + k % 4 * 32, 16), kS, k > 0);
+            mma_ss(tmem + t * kTile, a0 + k / 4 * kChunk + k % 4 * 2, b0 + k / 4 * kChunk + k % 4 * 2, kS, k > 0);
           mma_commit(&sm.s_full[t]);
         }
       };
-      while (ok && run.next(a, p)) {
-        const int n = max(p.cnt[0], p.cnt[1]);
-        ok = bar_wait(&sm.q_full, q_phase, &sm.dead) && bar_wait(&sm.kv_full[stage], kv_phase, &sm.dead);
-        if (!ok) break;
+      for (;;) {
+        if (!(ok = bar_wait(&sm.q_full, q_phase, &sm.dead))) break;
         q_phase ^= 1;
+        const int cnt[2] = {sm.todo[turn][0], sm.todo[turn][1]}, keys = sm.todo[turn][2];
+        turn ^= 1;
+        const int n = max(cnt[0], cnt[1]);
+        if (n == 0) break;
+        if (!(ok = bar_wait(&sm.kv_full[stage], kv_phase, &sm.dead))) break;
         tm_after();
+#pragma unroll
         for (int t = 0; t < 2; t++)
-          if (p.cnt[t] > 0) s_product(t, stage);
-        if (lane == 0) {
+          if (cnt[t] > 0) s_product(t, stage);
+        if (elected()) {
           mma_commit(&sm.kv_empty[stage]);
           if (n == 1) mma_commit(&sm.q_empty);
         }
@@ -442,39 +468,39 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
           const uint32_t k_phase = kv_phase;
           const bool more = j + 1 < n;
           if (!(ok = bar_wait(&sm.kv_full[vs], v_phase, &sm.dead))) break;
-          const int left = p.nk - (p.j0 + j) * kTile;  // keys from here on
+          const int left = keys - j * kTile;  // keys from here on
           if (left < kTile) {  // what lies behind the last key must not reach a product: 0 * NaN
             for (int i = lane; i < kTile * 8 * kChunks; i += 32)
               if (i / 8 % kTile >= left) reinterpret_cast<uint4 *>(sm.kv[vs][0])[i] = make_uint4(0, 0, 0, 0);
             fence_async();
             __syncwarp();
           }
-          for (int t = 0; t < 2 && ok; t++) {
-            if (j >= p.cnt[t]) continue;
+          if (more && !(ok = bar_wait(&sm.kv_full[ks], k_phase, &sm.dead))) break;
+#pragma unroll
+          for (int t = 0; t < 2; t++) {
+            if (j >= cnt[t]) continue;
             if (!(ok = bar_wait(&sm.p_full[t], p_phase[t], &sm.dead))) break;
             p_phase[t] ^= 1;
             tm_after();
-            if (lane == 0)
+            const uint32_t b0 = v_lo + vs * kStage;
+            if (elected())
 #pragma unroll
               for (int k = 0; k < kTile / 16; k++)  // O_t += P_t V
-                mma_ts(tmem + 2 * kTile + t * kTile, tmem + t * kTile + k * 8, operand(smem_of(sm.kv[vs][0]) + k * 2048, kTile * 128), kO, j > 0 || k > 0);
-            if (j + 1 < p.cnt[t]) {
-              if (!(ok = bar_wait(&sm.kv_full[ks], k_phase, &sm.dead))) break;
+                mma_ts(tmem + 2 * kTile + t * kTile, tmem + t * kTile + k * 8, b0 + k * (2048 >> 4), kO, j > 0 || k > 0);
+            if (j + 1 < cnt[t])
               s_product(t, ks);
-            } else if (lane == 0) {
+            else if (elected())
               mma_commit(&sm.o_full[t]);
-            }
           }
           if (!ok) break;
-          if (lane == 0) mma_commit(&sm.kv_empty[vs]);
-          if (more) {
-            if (lane == 0) {
-              mma_commit(&sm.kv_empty[ks]);
-              if (j + 2 == n) mma_commit(&sm.q_empty);
-            }
-            advance();
+          if (elected()) {
+            mma_commit(&sm.kv_empty[vs]);
+            if (more) mma_commit(&sm.kv_empty[ks]);
+            if (j + 2 == n) mma_commit(&sm.q_empty);
           }
+          if (more) advance();
         }
+        if (!ok) break;
       }
       }
     } else {
@@ -546,7 +572,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
           }
           tm_wait_st();
           tm_before();
-          bar_arrive(&sm.p_full[t]);
+          __syncwarp();
+          if (lane == 0) bar_arrive(&sm.p_full[t]);
         }
         if (!ok) break;
         const float sum = l.x + l.y;
@@ -563,30 +590,44 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
         float *part = a.parts + (2 * int64_t(blockIdx.x) + (seg > 0)) * kRows * (D + 2);  // slot 1: the run's last part
         const int64_t at = (int64_t(p.q0) + tok) * a.Hq + p.h * a.G + my_head;
         const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const uint32_t live = __ballot_sync(0xffffffffu, mine);
 #pragma unroll
-        for (int c = 0; c < D / 32; c++) {
-          uint32_t y[32];
-          if (some) {
-            tm_load(o_at + 32 * c, y);
-            tm_wait_ld();
-          } else {
+        for (int c2 = 0; c2 < D / 64; c2++) {
 #pragma unroll
-            for (int i = 0; i < 32; i++) y[i] = 0;
-          }
-          if (!mine) continue;
-          if (whole) {
+          for (int c = 2 * c2; c < 2 * c2 + 2; c++) {
+            uint32_t y[32];
+            if (some) {
+              tm_load(o_at + 32 * c, y);
+              tm_wait_ld();
+            } else {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              if (32 * c + i >= a.d) continue;
-              uint32_t w4[4];
-#pragma unroll
-              for (int k = 0; k < 4; k++) w4[k] = pack<BF16>(__uint_as_float(y[i + 2 * k]) * f, __uint_as_float(y[i + 2 * k + 1]) * f);
-              *reinterpret_cast<uint4 *>(a.out + at * a.d + 32 * c + i) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+              for (int i = 0; i < 32; i++) y[i] = 0;
             }
-          } else {
+            if (whole) {  // to the warp's rows of 128 bytes, swizzled
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<uint4 *>(part + (t * kTile + r) * D + 32 * c + i) = make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+              for (int i = 0; i < 32; i += 8) {
+                uint32_t w4[4];
+#pragma unroll
+                for (int k = 0; k < 4; k++) w4[k] = pack<BF16>(__uint_as_float(y[i + 2 * k]) * f, __uint_as_float(y[i + 2 * k + 1]) * f);
+                const int chunk = c % 2 * 4 + i / 8;
+                *reinterpret_cast<uint4 *>(sm.out[warp] + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+              }
+            } else if (mine) {  // four channels of 32 rows lie together
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<uint4 *>(part + ((8 * c + i / 4) * kRows + t * kTile + r) * 4) = make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+            }
+          }
+          if (whole) {  // eight lanes write 128 bytes of a row
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+              const int rr = 4 * i + lane / 8, chunk = lane % 8, ch = 64 * c2 + 8 * chunk;
+              const int64_t to = __shfl_sync(0xffffffffu, at, rr);
+              if ((live >> rr & 1) && ch < a.d)
+                *reinterpret_cast<uint4 *>(a.out + to * a.d + ch) = *reinterpret_cast<const uint4 *>(sm.out[warp] + rr * 128 + ((chunk ^ (rr & 7)) << 4));
+            }
+            __syncwarp();
           }
         }
         tm_before();
@@ -616,61 +657,56 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
 }
 
 // Joins the parts of items that several CTAs had: for a CTA that has the first
-// part of such an item, a warp per row, four channels a lane.  It is launched
-// with the first kernel and waits for its end here.
+// part of such an item, eight rows a CTA, four channels a thread.  It is
+// launched with the first kernel and waits for its end here.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(256) k_prompt_join(const __grid_constant__ PromptArgs a) {
+__global__ void __launch_bounds__(2 * D) k_prompt_join(const __grid_constant__ PromptArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && blockIdx.y == 0) {  // the status of the call
-    const uint32_t e = int(threadIdx.x) < int(gridDim.x) ? __ldcg(&a.notes[threadIdx.x].errors) : 0;
     __shared__ uint32_t s_errors;
     if (threadIdx.x == 0) s_errors = 0;
     __syncthreads();
+    uint32_t e = 0;
+    for (int i = threadIdx.x; i < int(gridDim.x); i += 2 * D) e |= __ldcg(&a.notes[i].errors);
     if (e) atomicOr(&s_errors, e);
     __syncthreads();
     if (threadIdx.x == 0) *a.status = s_errors;
   }
   const Note note = a.notes[blockIdx.x];
   if (note.parts == 0) return;
-  const int r = blockIdx.y * 8 + warp, t = r / kTile, rt = r % kTile;
+  const int r = blockIdx.y * 8 + threadIdx.x % 8, c = threadIdx.x / 8, t = r / kTile, rt = r % kTile;
   const int tok = note.q * a.W + t * a.TG + rt / a.G, q0 = a.cu_q[note.b];
   if (rt / a.G >= a.TG || tok >= a.cu_q[note.b + 1] - q0) return;
   auto part = [&](int i) { return a.parts + (2 * (int64_t(blockIdx.x) + i) + (i == 0 ? note.second : 0)) * kRows * (D + 2); };
   float top = -INFINITY, sum = 0.0f, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int base = 0; base < note.parts; base += 32) {
-    const int n = min(32, note.parts - base);
-    float m = -INFINITY, l = 0.0f;  // lane i: of part base + i
-    if (lane < n) m = __ldcg(part(base + lane) + kRows * D + r), l = __ldcg(part(base + lane) + kRows * (D + 1) + r);
-    float now = m;
+  for (int base = 0; base < note.parts; base += 8) {
+    float m[8], l[8], now = top;
+    float4 v[8];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
-    now = fmaxf(now, top);
-    const float keep = top == -INFINITY ? 0.0f : ex2(top - now), w = m == -INFINITY ? 0.0f : ex2(m - now);
+    for (int i = 0; i < 8; i++)
+      if (base + i < note.parts) {
+        const float *p = part(base + i);
+        m[i] = __ldcg(p + kRows * D + r), l[i] = __ldcg(p + kRows * (D + 1) + r);
+        v[i] = __ldcg(reinterpret_cast<const float4 *>(p) + c * kRows + r);
+        now = fmaxf(now, m[i]);
+      }
+    const float keep = top == -INFINITY ? 0.0f : ex2(top - now);
     top = now;
-    float lw = l * w;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
-    sum = sum * keep + lw;
+    sum *= keep;
 #pragma unroll
     for (int k = 0; k < 4; k++) y[k] *= keep;
-    for (int i0 = 0; i0 < n; i0 += 8) {
-      float4 v[8];
 #pragma unroll
-      for (int i = 0; i < 8; i++)
-        if (i0 + i < n && lane * 4 < D) v[i] = __ldcg(reinterpret_cast<const float4 *>(part(base + i0 + i) + r * D) + lane);
-#pragma unroll
-      for (int i = 0; i < 8; i++)
-        if (i0 + i < n) {
-          const float f = __shfl_sync(0xffffffffu, w, i0 + i);
-          if (lane * 4 < D) y[0] += f * v[i].x, y[1] += f * v[i].y, y[2] += f * v[i].z, y[3] += f * v[i].w;
-        }
-    }
+    for (int i = 0; i < 8; i++)
+      if (base + i < note.parts) {
+        const float w = m[i] == -INFINITY ? 0.0f : ex2(m[i] - now);
+        sum += w * l[i];
+        y[0] += w * v[i].x, y[1] += w * v[i].y, y[2] += w * v[i].z, y[3] += w * v[i].w;
+      }
   }
   const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
   const int64_t at = (int64_t(q0) + tok) * a.Hq + note.h * a.G + rt % a.G;
-  if (lane * 4 < a.d) *reinterpret_cast<uint2 *>(a.out + at * a.d + lane * 4) = make_uint2(pack<BF16>(y[0] * f, y[1] * f), pack<BF16>(y[2] * f, y[3] * f));
-  if (lane == 0 && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (top - kLift + log2f(sum)) * 0.6931471805599453f;
+  if (c * 4 < a.d) *reinterpret_cast<uint2 *>(a.out + at * a.d + c * 4) = make_uint2(pack<BF16>(y[0] * f, y[1] * f), pack<BF16>(y[2] * f, y[3] * f));
+  if (c == 0 && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (top - kLift + log2f(sum)) * 0.6931471805599453f;
 }
 
 bool prompt_ok(const cg_prompt *p) {
@@ -712,7 +748,7 @@ cudaError_t launch(const PromptArgs &a, unsigned grid, cudaStream_t st) {
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, kRows / 8), cfg.blockDim = dim3(256), cfg.stream = st;
+  cfg.gridDim = dim3(grid, kRows / 8), cfg.blockDim = dim3(2 * D), cfg.stream = st;
   cfg.attrs = &early, cfg.numAttrs = 1;
   const cudaError_t e2 = cudaLaunchKernelEx(&cfg, k_prompt_join<D, BF16>, a);
   return e2 != cudaSuccess ? e2 : cudaGetLastError();
