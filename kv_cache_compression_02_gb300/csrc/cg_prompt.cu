@@ -67,7 +67,7 @@ struct Smem {
   static constexpr int kChunks = D / 64;  // of 64 channels: 128 bytes, a swizzled row
   uint8_t q[2][kChunks][kTile * 128];
   uint8_t kv[kStages][kChunks][kTile * 128];
-  uint64_t q_full, q_empty, kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2], o_full[2];
+  uint64_t q_full, q_empty, kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2][2], o_full[2];  // p_full: of the first and the second 64 keys
   uint8_t out[8][32 * 128];  // a softmax warp's rows on their way out, 64 channels at a time
   int todo[2][4];            // for the products: of the item, by its turn: cnt[0], cnt[1], keys from its first on
   uint32_t tmem, errors, dead;
@@ -112,27 +112,37 @@ __device__ inline int key_tiles(const Seq &s, int tok) {
   return seen <= kTile ? 1 : int((seen + kTile - 1) / kTile);
 }
 
-// What the items before item i of a sequence and head cost: each its key
-// tiles and one more (its way in and out take about as long).
+// What an item costs: kIn for its way in and out, and for each key tile kBoth,
+// or kOne where it has rows in one tile only (the turns do not fill up then).
+// Measured: about 3000, 1900 and 7000 cycles.
+constexpr int kBoth = 3, kOne = 2, kIn = 7;
+
+__device__ inline int last_weight(const PromptArgs &a, const Seq &s) { return s.nq - (s.items - 1) * a.W > a.TG ? kBoth : kOne; }
+
+// What the items before item i of a sequence and head cost; all but the last have both tiles.
 __device__ inline int64_t cost_before(const PromptArgs &a, const Seq &s, int i) {
   const bool all = i == s.items && i > 0;  // the last item may be a short one
   const int64_t n = all ? i - 1 : i;
   const int64_t base = int64_t(s.nk) - s.nq;  // item j < items - 1 sees base + (j + 1) W keys
   const int64_t ones = max(int64_t(0), min(n, base > kTile ? int64_t(0) : (kTile - base) / a.W));
-  return n + ones + floor_sum(n - ones, kTile, a.W, base + (ones + 1) * a.W + kTile - 1) + (all ? key_tiles(s, s.nq) + 1 : 0);
+  return n * kIn + kBoth * (ones + floor_sum(n - ones, kTile, a.W, base + (ones + 1) * a.W + kTile - 1)) +
+         (all ? key_tiles(s, s.nq) * last_weight(a, s) + kIn : 0);
 }
 
 struct Walk {
   Seq s;
-  int b, h, q, n;   // item q of sequence b, head h, with n key tiles
+  int b, h, q, n, w;  // item q of sequence b, head h, with n key tiles of cost w
   int64_t lo;       // where its cost begins
 };
 
-__device__ inline void set_item(const PromptArgs &a, Walk &w) { w.n = key_tiles(w.s, min(w.s.nq, (w.q + 1) * a.W)); }
+__device__ inline void set_item(const PromptArgs &a, Walk &w) {
+  w.n = key_tiles(w.s, min(w.s.nq, (w.q + 1) * a.W));
+  w.w = w.q + 1 == w.s.items ? last_weight(a, w.s) : kBoth;
+}
 
 // The next item; the caller knows that there is one.
 __device__ inline void next_item(const PromptArgs &a, Walk &w, int skip) {
-  w.lo += skip ? w.n + 1 : 1;
+  w.lo += skip ? w.n * w.w + kIn : 1;
   if (++w.q == w.s.items) {
     w.q = 0;
     if (++w.h == a.H) {
@@ -150,20 +160,23 @@ __device__ inline void next_item(const PromptArgs &a, Walk &w, int skip) {
 // has the first cnt[0] and tile b the first cnt[1].
 struct Part {
   int b, h, q, q0, nq, k0, nk, j0, tok[2], cnt[2];
-  int64_t lo, cost;
+  int64_t first, last;  // where the costs of the item's first and last key tile begin
 };
 
 // The parts of a CTA's run [lo, hi), one after the other.
 struct Run {
   Walk w;
   int64_t at, hi;
-  int skip;  // 1: costs; 0: each item is one
+  int skip;  // 1: items have their costs; 0: each is one
 
   __device__ bool next(const PromptArgs &a, Part &p) {
     while (at < hi) {
-      const int64_t cost = skip ? w.n + 1 : 1, end = min(hi, w.lo + cost);
-      const int j0 = skip ? int(max(int64_t(0), at - w.lo - 1)) : 0, j1 = skip ? int(max(int64_t(0), end - w.lo - 1)) : w.n;
-      p.b = w.b, p.h = w.h, p.q = w.q, p.q0 = w.s.q0, p.nq = w.s.nq, p.k0 = w.s.k0, p.nk = w.s.nk, p.j0 = j0, p.lo = w.lo, p.cost = cost;
+      // a key tile belongs to the run in which its cost begins
+      const int64_t cost = skip ? w.n * w.w + kIn : 1, end = min(hi, w.lo + cost);
+      auto tiles_before = [&](int64_t x) { return int(max(int64_t(0), x - w.lo - kIn + w.w - 1) / w.w); };
+      const int j0 = skip ? tiles_before(at) : 0, j1 = skip ? tiles_before(end) : w.n;
+      p.b = w.b, p.h = w.h, p.q = w.q, p.q0 = w.s.q0, p.nq = w.s.nq, p.k0 = w.s.k0, p.nk = w.s.nk, p.j0 = j0;
+      p.first = w.lo + (skip ? kIn : 0), p.last = p.first + (skip ? (w.n - 1) * w.w : 0);
       for (int t = 0; t < 2; t++) {
         p.tok[t] = w.q * a.W + t * a.TG;
         const int n = p.tok[t] < w.s.nq ? key_tiles(w.s, min(w.s.nq, p.tok[t] + a.TG)) : 0;
@@ -302,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
     a.notes[blockIdx.x].parts = 0;
     bar_init(&sm.q_full, 1), bar_init(&sm.q_empty, 1);
     for (int i = 0; i < kStages; i++) bar_init(&sm.kv_full[i], 1), bar_init(&sm.kv_empty[i], 1);
-    for (int t = 0; t < 2; t++) bar_init(&sm.s_full[t], 1), bar_init(&sm.p_full[t], kTile / 32), bar_init(&sm.o_full[t], 1);
+    for (int t = 0; t < 2; t++) bar_init(&sm.s_full[t], 1), bar_init(&sm.p_full[t][0], kTile / 32), bar_init(&sm.p_full[t][1], kTile / 32), bar_init(&sm.o_full[t], 1);
     bar_init_fence();
   }
   if (warp == 9) {
@@ -343,7 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
   if (!skip) total = n_items, cost = items, cost_to = items_to;
   const int64_t before = cost_to - cost;
   if (blockIdx.x == 0 && bad) atomicOr(&sm.errors, kStBadArg);
-  const int64_t ctas = min(int64_t(gridDim.x), total);
+  // no run is shorter than a key tile: each has one of every item that goes through it
+  const int64_t ctas = min(int64_t(gridDim.x), skip ? (total + kBoth - 1) / kBoth : total);
   const int64_t lo = ctas ? total * blockIdx.x / ctas : 0, hi = ctas ? total * (blockIdx.x + 1) / ctas : 0;
   const bool busy = int64_t(blockIdx.x) < ctas;
   if (busy && lo >= before && lo < before + cost) {  // one thread's sequences hold the first cost
@@ -479,14 +493,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
 #pragma unroll
           for (int t = 0; t < 2; t++) {
             if (j >= cnt[t]) continue;
-            if (!(ok = bar_wait(&sm.p_full[t], p_phase[t], &sm.dead))) break;
-            p_phase[t] ^= 1;
-            tm_after();
             const uint32_t b0 = v_lo + vs * kStage;
-            if (elected())
 #pragma unroll
-              for (int k = 0; k < kTile / 16; k++)  // O_t += P_t V
-                mma_ts(tmem + 2 * kTile + t * kTile, tmem + t * kTile + k * 8, b0 + k * (2048 >> 4), kO, j > 0 || k > 0);
+            for (int half = 0; half < 2; half++) {  // O_t += P_t V
+              if (!(ok = bar_wait(&sm.p_full[t][half], p_phase[t], &sm.dead))) break;
+              tm_after();
+              if (elected())
+#pragma unroll
+                for (int k = half * 4; k < half * 4 + 4; k++)
+                  mma_ts(tmem + 2 * kTile + t * kTile, tmem + t * kTile + k * 8, b0 + k * (2048 >> 4), kO, j > 0 || k > 0);
+            }
+            if (!ok) break;
+            p_phase[t] ^= 1;
             if (j + 1 < cnt[t])
               s_product(t, ks);
             else if (elected())
@@ -557,6 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
             }
           }
           const float base = kLift - (m == -INFINITY ? 0.0f : m);
+          float2 sums[4] = {l, make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
           for (int c = 0; c < 4; c++) {
             uint32_t pk[16];
@@ -565,15 +584,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
               float2 y = make_float2(__uint_as_float(x[32 * c + 2 * i]), __uint_as_float(x[32 * c + 2 * i + 1]));
               y = fma2(y, sc, make_float2(base, base));
               y = make_float2(ex2(y.x), ex2(y.y));
-              l = add2(l, y);
+              sums[i & 3] = add2(sums[i & 3], y);
               pk[i] = pack<BF16>(y.x, y.y);
             }
             tm_store16(s_at + 16 * c, pk);
+            if (c & 1) {  // half of P is there
+              tm_wait_st();
+              tm_before();
+              __syncwarp();
+              if (lane == 0) bar_arrive(&sm.p_full[t][c >> 1]);
+            }
           }
-          tm_wait_st();
-          tm_before();
-          __syncwarp();
-          if (lane == 0) bar_arrive(&sm.p_full[t]);
+          l = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
         }
         if (!ok) break;
         const float sum = l.x + l.y;
@@ -584,8 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
           tm_after();
         }
         // who has key tiles of this item
-        const int64_t first = p.lo + skip, end = p.lo + p.cost - 1;
-        const int64_t c0 = ((first + 1) * ctas - 1) / total, c1 = ((end + 1) * ctas - 1) / total;
+        const int64_t c0 = ((p.first + 1) * ctas - 1) / total, c1 = ((p.last + 1) * ctas - 1) / total;
         const bool whole = c0 == c1;
         float *part = a.parts + (2 * int64_t(blockIdx.x) + (seg > 0)) * kRows * (D + 2);  // slot 1: the run's last part
         const int64_t at = (int64_t(p.q0) + tok) * a.Hq + p.h * a.G + my_head;
