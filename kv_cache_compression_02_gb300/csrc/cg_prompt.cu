@@ -61,15 +61,22 @@ struct PromptArgs {
   float scale_log2;  // scale * log2(e)
 };
 
+// What a part's products and softmax need to know.
+struct Todo {
+  int cnt[2], tok[2];   // as in Part; cnt[0] < 0: the end
+  int nq, nk, keys;     // keys: from the part's first on
+  int q0, head, slot;   // head: the first query head; slot of the workspace, or -1: the item is whole
+};
+
 template <int D>
 struct Smem {
   static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kChunks = D / 64;  // of 64 channels: 128 bytes, a swizzled row
   uint8_t q[2][kChunks][kTile * 128];
   uint8_t kv[kStages][kChunks][kTile * 128];
-  uint64_t q_full, q_empty, kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2][2], o_full[2];  // p_full: of the first and the second 64 keys
+  uint64_t todo_full[2], todo_empty[2], q_full, q_empty, kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2][2], o_full[2];  // p_full: of the first and the second 64 keys
   uint8_t out[8][32 * 128];  // a softmax warp's rows on their way out, 64 channels at a time
-  int todo[2][4];            // for the products: of the item, by its turn: cnt[0], cnt[1], keys from its first on
+  Todo todo[2];              // the parts of the run, by turns, from the loading warp to the others
   uint32_t tmem, errors, dead;
   int most[kThreads / 32], b;
   int64_t sum[kThreads / 32][2], prefix;
@@ -314,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
     sm.errors = sm.dead = 0;
     a.notes[blockIdx.x].parts = 0;
     bar_init(&sm.q_full, 1), bar_init(&sm.q_empty, 1);
+    for (int i = 0; i < 2; i++) bar_init(&sm.todo_full[i], 1), bar_init(&sm.todo_empty[i], 9);  // the products' warp and eight
     for (int i = 0; i < kStages; i++) bar_init(&sm.kv_full[i], 1), bar_init(&sm.kv_empty[i], 1);
     for (int t = 0; t < 2; t++) bar_init(&sm.s_full[t], 1), bar_init(&sm.p_full[t][0], kTile / 32), bar_init(&sm.p_full[t][1], kTile / 32), bar_init(&sm.o_full[t], 1);
     bar_init_fence();
@@ -377,50 +385,62 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
   const uint32_t tmem = sm.tmem;
 
   if (busy) {
-    Run run;
-    run.at = lo, run.hi = hi, run.skip = skip;
-    Walk &w = run.w;
-    w.b = sm.b;
-    load_seq(a, w.b, w.s);
-    {
-      const int64_t head = skip ? cost_before(a, w.s, w.s.items) : w.s.items, in = lo - sm.prefix;
-      w.h = int(in / head);
-      const int64_t rest = in - w.h * head;
-      int l = 0, r = w.s.items - 1;  // the last item that begins at or before `rest`
-      while (l < r) {
-        const int mid = (l + r + 1) / 2;
-        if ((skip ? cost_before(a, w.s, mid) : mid) <= rest)
-          l = mid;
-        else
-          r = mid - 1;
-      }
-      w.q = l;
-      w.lo = sm.prefix + w.h * head + (skip ? cost_before(a, w.s, l) : l);
-      set_item(a, w);
-    }
-    Part p;
     if (warp >= 8) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
       if (warp == 8) {
       // ---- loads ----
       if (lane == 0) {
-        int stage = 0, turn = 0;
-        uint32_t kv_phase = 1, q_phase = 1;  // the first pass over the ring finds it empty
+        Run run;
+        Part p;
+        run.at = lo, run.hi = hi, run.skip = skip;
+        Walk &w = run.w;
+        w.b = sm.b;
+        load_seq(a, w.b, w.s);
+        {
+          const int64_t head = skip ? cost_before(a, w.s, w.s.items) : w.s.items, in = lo - sm.prefix;
+          w.h = int(in / head);
+          const int64_t rest = in - w.h * head;
+          int l = 0, r = w.s.items - 1;  // the last item that begins at or before `rest`
+          while (l < r) {
+            const int mid = (l + r + 1) / 2;
+            if ((skip ? cost_before(a, w.s, mid) : mid) <= rest)
+              l = mid;
+            else
+              r = mid - 1;
+          }
+          w.q = l;
+          w.lo = sm.prefix + w.h * head + (skip ? cost_before(a, w.s, l) : l);
+          set_item(a, w);
+        }
+        int stage = 0, turn = 0, seg = 0;
+        uint32_t kv_phase = 1, q_phase = 1, todo_phase = 1;  // the first pass over a ring finds it empty
         bool ok = true;
         const uint32_t q_bytes = uint32_t(kChunks) * 128 * a.G * a.TG;
         for (;;) {
           const bool more = run.next(a, p);
+          if (!(ok = bar_wait(&sm.todo_empty[turn], todo_phase, &sm.dead))) break;
+          Todo &todo = sm.todo[turn];
+          if (!more) {
+            todo.cnt[0] = -1;
+            bar_arrive(&sm.todo_full[turn]);
+            break;
+          }
+          // who has key tiles of this item
+          const int64_t c0 = ((p.first + 1) * ctas - 1) / total, c1 = ((p.last + 1) * ctas - 1) / total;
+          for (int t = 0; t < 2; t++) todo.cnt[t] = p.cnt[t], todo.tok[t] = p.tok[t];
+          todo.nq = p.nq, todo.nk = p.nk, todo.keys = p.nk - p.j0 * kTile, todo.q0 = p.q0, todo.head = p.h * a.G;
+          todo.slot = c0 == c1 ? -1 : 2 * int(blockIdx.x) + (seg > 0);  // slot 1: the run's last part
+          bar_arrive(&sm.todo_full[turn]);
+          if (c0 != c1 && int64_t(blockIdx.x) == c0) {
+            Note &note = a.notes[blockIdx.x];
+            note.parts = int(c1 - c0 + 1), note.second = seg > 0, note.b = p.b, note.h = p.h, note.q = p.q;
+          }
+          seg++;
+          turn ^= 1;
+          if (turn == 0) todo_phase ^= 1;
           const int n = max(p.cnt[0], p.cnt[1]);
           if (!(ok = bar_wait(&sm.q_empty, q_phase, &sm.dead))) break;
           q_phase ^= 1;
-          int *todo = sm.todo[turn];
-          if (!more) {  // the end
-            todo[0] = todo[1] = 0;
-            bar_arrive(&sm.q_full);
-            break;
-          }
-          todo[0] = p.cnt[0], todo[1] = p.cnt[1], todo[2] = p.nk - p.j0 * kTile;
-          turn ^= 1;
           bar_expect(&sm.q_full, q_bytes * ((p.cnt[0] > 0) + (p.cnt[1] > 0)));
           for (int t = 0; t < 2; t++)
             if (p.cnt[t] > 0)
@@ -443,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
       constexpr uint32_t kChunk = kTile * 128 >> 4, kStage = kTileBytes >> 4;
       const uint32_t q_lo = operand_lo(sm.q[0], 16), k_lo = operand_lo(sm.kv[0], 16), v_lo = operand_lo(sm.kv[0], kTile * 128);
       int stage = 0, turn = 0;
-      uint32_t kv_phase = 0, q_phase = 0, p_phase[2] = {0, 0};
+      uint32_t kv_phase = 0, q_phase = 0, todo_phase = 0, p_phase[2] = {0, 0};
       bool ok = true;
       auto advance = [&] {
         if (++stage == kStages) stage = 0, kv_phase ^= 1;
@@ -458,12 +478,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
         }
       };
       for (;;) {
+        if (!(ok = bar_wait(&sm.todo_full[turn], todo_phase, &sm.dead))) break;
+        const int cnt[2] = {sm.todo[turn].cnt[0], sm.todo[turn].cnt[1]}, keys = sm.todo[turn].keys;
+        __syncwarp();
+        if (lane == 0) bar_arrive(&sm.todo_empty[turn]);
+        turn ^= 1;
+        if (turn == 0) todo_phase ^= 1;
+        if (cnt[0] < 0) break;
+        const int n = max(cnt[0], cnt[1]);
         if (!(ok = bar_wait(&sm.q_full, q_phase, &sm.dead))) break;
         q_phase ^= 1;
-        const int cnt[2] = {sm.todo[turn][0], sm.todo[turn][1]}, keys = sm.todo[turn][2];
-        turn ^= 1;
-        const int n = max(cnt[0], cnt[1]);
-        if (n == 0) break;
         if (!(ok = bar_wait(&sm.kv_full[stage], kv_phase, &sm.dead))) break;
         tm_after();
 #pragma unroll
@@ -527,18 +551,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
       const int t = warp >> 2, r = threadIdx.x & (kTile - 1);
       const uint32_t row = uint32_t(warp & 3) << 21;  // the warp's lanes of TMEM
       const uint32_t s_at = tmem + row + t * kTile, o_at = tmem + row + 2 * kTile + t * kTile;
-      uint32_t s_phase = 0, o_phase = 0;
+      uint32_t s_phase = 0, o_phase = 0, todo_phase = 0;
+      int turn = 0;
       bool ok = true;
-      int seg = 0;
       const int my_tok = r / a.G, my_head = r % a.G;
       const float2 sc = make_float2(a.scale_log2, a.scale_log2);
-      while (ok && run.next(a, p)) {
-        const int tok = p.tok[t] + my_tok;
-        const bool mine = my_tok < a.TG && tok < p.nq;
-        const int last = min(p.nk - 1, p.nk - p.nq + tok) - p.j0 * kTile;  // the last key seen, from the part's first
+      for (;;) {
+        if (!(ok = bar_wait(&sm.todo_full[turn], todo_phase, &sm.dead))) break;
+        const Todo &todo = sm.todo[turn];
+        const int cnt = todo.cnt[0] < 0 ? -1 : todo.cnt[t], tok = todo.tok[t] + my_tok, slot = todo.slot;
+        const bool mine = my_tok < a.TG && tok < todo.nq;
+        // the last key seen, from the part's first
+        const int last = min(todo.nk - 1, todo.nk - todo.nq + tok) - (todo.nk - todo.keys);
+        const int64_t at = (int64_t(todo.q0) + tok) * a.Hq + todo.head + my_head;
+        __syncwarp();
+        if (lane == 0) bar_arrive(&sm.todo_empty[turn]);
+        turn ^= 1;
+        if (turn == 0) todo_phase ^= 1;
+        if (cnt < 0) break;
         float m = -INFINITY;
         float2 l = make_float2(0.0f, 0.0f);
-        for (int j = 0; j < p.cnt[t]; j++) {
+        for (int j = 0; j < cnt; j++) {
           if (!(ok = bar_wait(&sm.s_full[t], s_phase, &sm.dead))) break;
           s_phase ^= 1;
           tm_after();
@@ -599,17 +632,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
         }
         if (!ok) break;
         const float sum = l.x + l.y;
-        const bool some = p.cnt[t] > 0;
+        const bool some = cnt > 0;
         if (some) {
           if (!(ok = bar_wait(&sm.o_full[t], o_phase, &sm.dead))) break;
           o_phase ^= 1;
           tm_after();
         }
-        // who has key tiles of this item
-        const int64_t c0 = ((p.first + 1) * ctas - 1) / total, c1 = ((p.last + 1) * ctas - 1) / total;
-        const bool whole = c0 == c1;
-        float *part = a.parts + (2 * int64_t(blockIdx.x) + (seg > 0)) * kRows * (D + 2);  // slot 1: the run's last part
-        const int64_t at = (int64_t(p.q0) + tok) * a.Hq + p.h * a.G + my_head;
+        const bool whole = slot < 0;
+        float *part = a.parts + int64_t(slot) * kRows * (D + 2);
         const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
         const uint32_t live = __ballot_sync(0xffffffffu, mine);
 #pragma unroll
@@ -659,11 +689,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
             part[kRows * D + t * kTile + r] = m, part[kRows * (D + 1) + t * kTile + r] = sum;
           }
         }
-        if (!whole && threadIdx.x == 0 && int64_t(blockIdx.x) == c0) {
-          Note &note = a.notes[blockIdx.x];
-          note.parts = int(c1 - c0 + 1), note.second = seg > 0, note.b = p.b, note.h = p.h, note.q = p.q;
-        }
-        seg++;
       }
     }
   }
