@@ -83,17 +83,21 @@ struct Smem {
 };
 
 // ---- items ------------------------------------------------------------------
-// sum of floor((a i + b) / m), i < n; a, b >= 0
-__device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
-  int64_t r = 0;
-  while (n > 0) {
-    r += (n - 1) * n / 2 * (a / m) + n * (b / m);
-    a %= m, b %= m;
-    const int64_t top = a * n + b;
+// sum of floor((a i + b) / 128), i < n; a < 2^16, b >= 0
+__device__ inline int64_t tiles_sum(int64_t n, uint32_t a, int64_t b) {
+  int64_t r = (n - 1) * n / 2 * (a / kTile) + n * (b / kTile);
+  uint32_t m = kTile, c = uint32_t(b % kTile);
+  a %= kTile;
+  while (n > 0) {  // as points under a line, with the axes exchanged at each turn
+    const uint64_t top = uint64_t(a) * n + c;
     if (top < m) break;
-    n = top / m, b = top % m;
-    const int64_t t = m;
+    const bool small = top >> 32 == 0;
+    n = small ? uint32_t(top) / m : int64_t(top / m);
+    c = small ? uint32_t(top) % m : uint32_t(top % m);
+    const uint32_t t = m;
     m = a, a = t;
+    r += (n - 1) * n / 2 * (a / m) + n * (c / m);
+    a %= m, c %= m;
   }
   return r;
 }
@@ -119,37 +123,33 @@ __device__ inline int key_tiles(const Seq &s, int tok) {
   return seen <= kTile ? 1 : int((seen + kTile - 1) / kTile);
 }
 
-// What an item costs: kIn for its way in and out, and for each key tile kBoth,
-// or kOne where it has rows in one tile only (the turns do not fill up then).
-// Measured: about 3000, 1900 and 7000 cycles.
-constexpr int kBoth = 3, kOne = 2, kIn = 7;
+// What an item costs: kIn for its way in and out and kTileCost for each key
+// tile (measured: about 7000 and 2800 cycles; rows in one tile only cost as
+// much as rows in both, for then the turns do not fill up).
+constexpr int kTileCost = 3, kIn = 7;
 
-__device__ inline int last_weight(const PromptArgs &a, const Seq &s) { return s.nq - (s.items - 1) * a.W > a.TG ? kBoth : kOne; }
-
-// What the items before item i of a sequence and head cost; all but the last have both tiles.
+// What the items before item i of a sequence and head cost.
 __device__ inline int64_t cost_before(const PromptArgs &a, const Seq &s, int i) {
   const bool all = i == s.items && i > 0;  // the last item may be a short one
   const int64_t n = all ? i - 1 : i;
   const int64_t base = int64_t(s.nk) - s.nq;  // item j < items - 1 sees base + (j + 1) W keys
   const int64_t ones = max(int64_t(0), min(n, base > kTile ? int64_t(0) : (kTile - base) / a.W));
-  return n * kIn + kBoth * (ones + floor_sum(n - ones, kTile, a.W, base + (ones + 1) * a.W + kTile - 1)) +
-         (all ? key_tiles(s, s.nq) * last_weight(a, s) + kIn : 0);
+  return n * kIn + kTileCost * (ones + tiles_sum(n - ones, a.W, base + (ones + 1) * a.W + kTile - 1)) + (all ? key_tiles(s, s.nq) * kTileCost + kIn : 0);
 }
 
 struct Walk {
   Seq s;
-  int b, h, q, n, w;  // item q of sequence b, head h, with n key tiles of cost w
+  int b, h, q, n;  // item q of sequence b, head h, with n key tiles
   int64_t lo;       // where its cost begins
 };
 
 __device__ inline void set_item(const PromptArgs &a, Walk &w) {
-  w.n = key_tiles(w.s, min(w.s.nq, (w.q + 1) * a.W));
-  w.w = w.q + 1 == w.s.items ? last_weight(a, w.s) : kBoth;
+  w.n = key_tiles(w.s, int(min(int64_t(w.s.nq), (int64_t(w.q) + 1) * a.W)));
 }
 
 // The next item; the caller knows that there is one.
 __device__ inline void next_item(const PromptArgs &a, Walk &w, int skip) {
-  w.lo += skip ? w.n * w.w + kIn : 1;
+  w.lo += skip ? w.n * kTileCost + kIn : 1;
   if (++w.q == w.s.items) {
     w.q = 0;
     if (++w.h == a.H) {
@@ -179,11 +179,11 @@ struct Run {
   __device__ bool next(const PromptArgs &a, Part &p) {
     while (at < hi) {
       // a key tile belongs to the run in which its cost begins
-      const int64_t cost = skip ? w.n * w.w + kIn : 1, end = min(hi, w.lo + cost);
-      auto tiles_before = [&](int64_t x) { return int(max(int64_t(0), x - w.lo - kIn + w.w - 1) / w.w); };
+      const int64_t cost = skip ? w.n * kTileCost + kIn : 1, end = min(hi, w.lo + cost);
+      auto tiles_before = [&](int64_t x) { return int(max(int64_t(0), x - w.lo - kIn + kTileCost - 1)) / kTileCost; };
       const int j0 = skip ? tiles_before(at) : 0, j1 = skip ? tiles_before(end) : w.n;
       p.b = w.b, p.h = w.h, p.q = w.q, p.q0 = w.s.q0, p.nq = w.s.nq, p.k0 = w.s.k0, p.nk = w.s.nk, p.j0 = j0;
-      p.first = w.lo + (skip ? kIn : 0), p.last = p.first + (skip ? (w.n - 1) * w.w : 0);
+      p.first = w.lo + (skip ? kIn : 0), p.last = p.first + (skip ? (w.n - 1) * kTileCost : 0);
       for (int t = 0; t < 2; t++) {
         p.tok[t] = w.q * a.W + t * a.TG;
         const int n = p.tok[t] < w.s.nq ? key_tiles(w.s, min(w.s.nq, p.tok[t] + a.TG)) : 0;
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
   const int64_t before = cost_to - cost;
   if (blockIdx.x == 0 && bad) atomicOr(&sm.errors, kStBadArg);
   // no run is shorter than a key tile: each has one of every item that goes through it
-  const int64_t ctas = min(int64_t(gridDim.x), skip ? (total + kBoth - 1) / kBoth : total);
+  const int64_t ctas = min(int64_t(gridDim.x), skip ? (total + kTileCost - 1) / kTileCost : total);
   const int64_t lo = ctas ? total * blockIdx.x / ctas : 0, hi = ctas ? total * (blockIdx.x + 1) / ctas : 0;
   const bool busy = int64_t(blockIdx.x) < ctas;
   if (busy && lo >= before && lo < before + cost) {  // one thread's sequences hold the first cost
@@ -389,29 +389,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
       if (warp == 8) {
       // ---- loads ----
+      Run run;
+      Part p;
+      run.at = lo, run.hi = hi, run.skip = skip;
+      Walk &w = run.w;
+      w.b = sm.b;
+      load_seq(a, w.b, w.s);
+      const int64_t head = skip ? cost_before(a, w.s, w.s.items) : w.s.items;
+      w.h = int((lo - sm.prefix) / head);
+      const int64_t rest = lo - sm.prefix - w.h * head;
+      int l = 0, n = w.s.items;  // the last item that begins at or before `rest` is one of l .. l + n - 1
+      while (n > 1) {            // 32 of them at a time
+        const int step = (n + 31) / 32, at = l + lane * step;
+        const bool behind = lane > 0 && (at >= l + n || (skip ? cost_before(a, w.s, at) : at) > rest);
+        const uint32_t first = __ballot_sync(0xffffffffu, behind);
+        const int k = first ? __ffs(first) - 2 : 31;
+        n = min(step, l + n - (l + k * step));
+        l += k * step;
+      }
+      w.q = l;
+      w.lo = sm.prefix + w.h * head + (skip ? cost_before(a, w.s, l) : l);
+      set_item(a, w);
       if (lane == 0) {
-        Run run;
-        Part p;
-        run.at = lo, run.hi = hi, run.skip = skip;
-        Walk &w = run.w;
-        w.b = sm.b;
-        load_seq(a, w.b, w.s);
-        {
-          const int64_t head = skip ? cost_before(a, w.s, w.s.items) : w.s.items, in = lo - sm.prefix;
-          w.h = int(in / head);
-          const int64_t rest = in - w.h * head;
-          int l = 0, r = w.s.items - 1;  // the last item that begins at or before `rest`
-          while (l < r) {
-            const int mid = (l + r + 1) / 2;
-            if ((skip ? cost_before(a, w.s, mid) : mid) <= rest)
-              l = mid;
-            else
-              r = mid - 1;
-          }
-          w.q = l;
-          w.lo = sm.prefix + w.h * head + (skip ? cost_before(a, w.s, l) : l);
-          set_item(a, w);
-        }
         int stage = 0, turn = 0, seg = 0;
         uint32_t kv_phase = 1, q_phase = 1, todo_phase = 1;  // the first pass over a ring finds it empty
         bool ok = true;
@@ -585,6 +584,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
             for (int i = 0; i < kTile; i++)
               if (i > lim) x[i] = 0xff800000u;
           }
+          float base = kLift - (m == -INFINITY ? 0.0f : m);
+          float2 sums[4];
+          uint32_t pk[16];
+          auto quarter = [&](int c) {  // 32 probabilities
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+              float2 y = make_float2(__uint_as_float(x[32 * c + 2 * i]), __uint_as_float(x[32 * c + 2 * i + 1]));
+              y = fma2(y, sc, make_float2(base, base));
+              y = make_float2(ex2(y.x), ex2(y.y));
+              sums[i & 3] = c == 0 && i < 4 ? y : add2(sums[i & 3], y);
+              pk[i] = pack<BF16>(y.x, y.y);
+            }
+          };
+          // The maximum, and meanwhile the first quarter under the maximum so
+          // far, which holds for most tiles.
+          if (j > 0) quarter(0);
           float top[4];
 #pragma unroll
           for (int i = 0; i < 4; i++) top[i] = fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 4]));
@@ -593,33 +608,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
 #pragma unroll
             for (int k = 0; k < 4; k++) top[k] = max3(top[k], __uint_as_float(x[i + 2 * k]), __uint_as_float(x[i + 2 * k + 1]));
           const float now = max3(top[0], top[1], fmaxf(top[2], top[3])) * a.scale_log2;
-          float keep = 1.0f;
-          if (now > m + kLag) keep = ex2(m - now), m = now;
-          if (j > 0 && __any_sync(0xffffffffu, keep != 1.0f)) {
-            l = mul2(l, make_float2(keep, keep));
+          const bool moved = now > m + kLag;
+          if (j == 0 || __any_sync(0xffffffffu, moved)) {
+            const float keep = moved ? ex2(m - now) : 1.0f;
+            if (moved) m = now;
+            base = kLift - (m == -INFINITY ? 0.0f : m);
+            if (j > 0) {
+              l = mul2(l, make_float2(keep, keep));
 #pragma unroll
-            for (int c = 0; c < D / 32; c++) {
-              uint32_t y[32];
-              tm_load(o_at + 32 * c, y);
-              tm_wait_ld();
+              for (int c = 0; c < D / 32; c++) {
+                uint32_t y[32];
+                tm_load(o_at + 32 * c, y);
+                tm_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; i++) y[i] = __float_as_uint(__uint_as_float(y[i]) * keep);
-              tm_store32(o_at + 32 * c, y);
+                for (int i = 0; i < 32; i++) y[i] = __float_as_uint(__uint_as_float(y[i]) * keep);
+                tm_store32(o_at + 32 * c, y);
+              }
             }
+            quarter(0);
           }
-          const float base = kLift - (m == -INFINITY ? 0.0f : m);
-          float2 sums[4] = {l, make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
           for (int c = 0; c < 4; c++) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; i++) {
-              float2 y = make_float2(__uint_as_float(x[32 * c + 2 * i]), __uint_as_float(x[32 * c + 2 * i + 1]));
-              y = fma2(y, sc, make_float2(base, base));
-              y = make_float2(ex2(y.x), ex2(y.y));
-              sums[i & 3] = add2(sums[i & 3], y);
-              pk[i] = pack<BF16>(y.x, y.y);
-            }
+            if (c > 0) quarter(c);
             tm_store16(s_at + 16 * c, pk);
             if (c & 1) {  // half of P is there
               tm_wait_st();
@@ -628,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
               if (lane == 0) bar_arrive(&sm.p_full[t][c >> 1]);
             }
           }
-          l = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
+          l = add2(l, add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
         }
         if (!ok) break;
         const float sum = l.x + l.y;
@@ -706,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
 // part of such an item, eight rows a CTA, four channels a thread.  It is
 // launched with the first kernel and waits for its end here.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(2 * D) k_prompt_join(const __grid_constant__ PromptArgs a) {
+__global__ void __launch_bounds__(2 * D, 2048 / (2 * D)) k_prompt_join(const __grid_constant__ PromptArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (blockIdx.x == 0 && blockIdx.y == 0) {  // the status of the call
     __shared__ uint32_t s_errors;
@@ -725,11 +735,11 @@ __global__ void __launch_bounds__(2 * D) k_prompt_join(const __grid_constant__ P
   if (rt / a.G >= a.TG || tok >= a.cu_q[note.b + 1] - q0) return;
   auto part = [&](int i) { return a.parts + (2 * (int64_t(blockIdx.x) + i) + (i == 0 ? note.second : 0)) * kRows * (D + 2); };
   float top = -INFINITY, sum = 0.0f, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int base = 0; base < note.parts; base += 8) {
-    float m[8], l[8], now = top;
-    float4 v[8];
+  for (int base = 0; base < note.parts; base += 2) {
+    float m[2], l[2], now = top;
+    float4 v[2];
 #pragma unroll
-    for (int i = 0; i < 8; i++)
+    for (int i = 0; i < 2; i++)
       if (base + i < note.parts) {
         const float *p = part(base + i);
         m[i] = __ldcg(p + kRows * D + r), l[i] = __ldcg(p + kRows * (D + 1) + r);
@@ -742,7 +752,7 @@ __global__ void __launch_bounds__(2 * D) k_prompt_join(const __grid_constant__ P
 #pragma unroll
     for (int k = 0; k < 4; k++) y[k] *= keep;
 #pragma unroll
-    for (int i = 0; i < 8; i++)
+    for (int i = 0; i < 2; i++)
       if (base + i < note.parts) {
         const float w = m[i] == -INFINITY ? 0.0f : ex2(m[i] - now);
         sum += w * l[i];
