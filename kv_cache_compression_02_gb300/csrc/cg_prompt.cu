@@ -124,9 +124,9 @@ __device__ inline int key_tiles(const Seq &s, int tok) {
 }
 
 // What an item costs: kIn for its way in and out and kTileCost for each key
-// tile (measured: about 7000 and 2800 cycles; rows in one tile only cost as
-// much as rows in both, for then the turns do not fill up).
-constexpr int kTileCost = 3, kIn = 7;
+// tile (measured: 4.8 and 1.4 us; rows in one tile only cost nearly as much as
+// rows in both, for then the turns do not fill up).
+constexpr int kTileCost = 2, kIn = 7;
 
 // What the items before item i of a sequence and head cost.
 __device__ inline int64_t cost_before(const PromptArgs &a, const Seq &s, int i) {
