@@ -121,17 +121,16 @@ def lib() -> ctypes.CDLL:
 
 
 def _ptr(t) -> int:
-    if t is None:
-        return 0
-    if isinstance(t, int):
-        return t
-    return int(t.data_ptr())
+    try:
+        return t.data_ptr()
+    except AttributeError:
+        return 0 if t is None else int(t)
 
 
 def _stream(s) -> int | None:
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream or None
+        from torch import _C  # the current stream's handle, without a Stream object around it
+        return _C._cuda_getCurrentRawStream(_C._cuda_getDevice()) or None
     return getattr(s, "cuda_stream", s) or None
 
 
@@ -159,7 +158,7 @@ class Cache:
     """A paged cache: 2*L pools of n_blocks pages [H][block_tokens][d], fp16 or 8-bit codes (CG_CACHE_*)."""
 
     def __init__(self, L, H, d, block_tokens, n_blocks, format=CG_CACHE_E4M3):
-        self.c = cg_cache(L, H, d, block_tokens, n_blocks, format)
+        self.c, self.d = cg_cache(L, H, d, block_tokens, n_blocks, format), d
         self.ref = ctypes.addressof(self.c)
 
 
@@ -176,15 +175,15 @@ class Attend:
     heads have head_dim elements (filled in from the cache by the call)."""
 
     def __init__(self, n_seq, q_tokens, Hq, dtype, table_stride, scale, q_stride=None):
-        self.contiguous = q_stride is None
+        self.contiguous, self.d = q_stride is None, 0
         self.c = cg_attend(n_seq, q_tokens, Hq, dtype, table_stride, scale,
                            (ctypes.c_int64 * 3)(*([0, 0, 0] if q_stride is None else q_stride)))
         self.ref = ctypes.addressof(self.c)
 
     def for_cache(self, cache):
-        if self.contiguous:
-            d, hq = cache.c.d, self.c.Hq
-            self.c.q_stride[:] = [self.c.q_tokens * hq * d, hq * d, d]
+        if self.contiguous and self.d != cache.d:
+            self.d, hq = cache.d, self.c.Hq
+            self.c.q_stride[:] = [self.c.q_tokens * hq * self.d, hq * self.d, self.d]
         return self.ref
 
 
@@ -352,7 +351,7 @@ def cg_entropy_bound(cfg: Config, ws_fit, level: int = 0) -> float:
 
 # ---- serving a decoded context (include/cachegen_cache.h) -------------------
 def _bytes(ws) -> int:
-    return ws.numel() * ws.element_size()
+    return ws.nbytes
 
 
 def cg_cache_write(cache: Cache, rows: Rows, k, v, cu_new, start, table, k_pool, v_pool, k_scale, v_scale, ws,

@@ -18,6 +18,28 @@ constexpr int kSMs = 152;  // of a GB300
 
 inline bool is_aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Clears a call's status word.  The kernel that follows is launched early: it
+// may begin while this one ends, when what ran before this one is done, and
+// waits for it (status_cleared) before it sets a bit.
+static __global__ void k_clear(uint32_t *status) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (threadIdx.x == 0) *status = 0;
+}
+
+__device__ inline void status_cleared() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launches a kernel that may begin while the one before it ends.
+template <typename... Args>
+inline cudaError_t launch_early(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const Args &...args) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid, cfg.blockDim = block, cfg.dynamicSmemBytes = smem, cfg.stream = st;
+  cfg.attrs = &early, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 inline cg_status launched() { return cudaGetLastError() == cudaSuccess ? CG_OK : CG_ERR_CUDA; }
 
 inline bool cache_ok(const cg_cache *c) {
@@ -49,11 +71,21 @@ struct QMax<CG_CACHE_INT8> {
   static constexpr float v = 127.0f;
 };
 
-// The nearest code, halves to even, saturating.
+// Four codes, nearest and halves to even.  e4m3 saturates; for int8 the values
+// must be within 127.5 (an addition of 1.5 2^23 rounds them to integers, whose
+// low bytes are the codes).
 template <int FMT>
-__device__ inline uint32_t code_of(float x) {
-  if (FMT == CG_CACHE_E4M3) return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
-  return uint32_t(__float2int_rn(fminf(fmaxf(x, -127.0f), 127.0f))) & 0xffu;
+__device__ inline uint32_t codes_of(float a, float b, float c, float d) {
+  if (FMT == CG_CACHE_E4M3) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return uint32_t(lo) | uint32_t(hi) << 16;
+  }
+  constexpr float kRound = 12582912.0f;
+  const uint32_t ab = __byte_perm(__float_as_uint(__fadd_rn(a, kRound)), __float_as_uint(__fadd_rn(b, kRound)), 0x0040);
+  const uint32_t cd = __byte_perm(__float_as_uint(__fadd_rn(c, kRound)), __float_as_uint(__fadd_rn(d, kRound)), 0x0040);
+  return __byte_perm(ab, cd, 0x5410);
 }
 
 // The value a code stands for, without its scale.

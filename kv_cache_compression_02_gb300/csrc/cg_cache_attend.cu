@@ -36,7 +36,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTok = 32;              // positions of a warp's tile
 constexpr int kUnit = kTok * kWarps;  // positions of a unit
-constexpr int kShort = 8;             // units of an item that one CTA takes where items are few
+constexpr int kShort = 2;             // units of an item that one CTA takes where items are few
 constexpr int kLens = 512;            // sequences whose lengths are kept in shared memory
 
 // NB blocks of eight query rows make an item.  One block leaves room for three
@@ -1013,13 +1013,7 @@ cudaError_t launch_kernels(const AttendArgs &a, unsigned grid, cudaStream_t st) 
   const cudaError_t e = cudaFuncSetAttribute(k_attend<FMT, D, NB, BF16, PLAIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   k_attend<FMT, D, NB, BF16, PLAIN><<<grid, kThreads, kSmem, st>>>(a);
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, unsigned((min(8 * NB, a.rows) + 3) / 4)), cfg.blockDim = dim3(128), cfg.stream = st;
-  cfg.attrs = &early, cfg.numAttrs = 1;
-  const cudaError_t e2 = cudaLaunchKernelEx(&cfg, k_join<D, NB, BF16>, a);
+  const cudaError_t e2 = launch_early(k_join<D, NB, BF16>, dim3(grid, unsigned((min(8 * NB, a.rows) + 3) / 4)), dim3(128), 0, st, a);
   return e2 != cudaSuccess ? e2 : cudaGetLastError();
 }
 

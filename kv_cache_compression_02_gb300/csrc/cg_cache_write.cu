@@ -17,40 +17,54 @@ struct WriteArgs {
   int H, d, bt, n_blocks, n_rows, max_new, stride, per_seq;
 };
 
-// Eight values; one that is not finite becomes 0 and sets `bad`.
+// The exponent of Inf and NaN, in both halves of a word.
 template <bool BF16>
-__device__ inline void finite8(uint4 w, float (&x)[8], bool &bad) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 8; i++) {
-    const uint16_t b = uint16_t(u[i >> 1] >> (16 * (i & 1)));
-    constexpr uint16_t kExp = BF16 ? 0x7f80 : 0x7c00;
-    const bool fin = (b & kExp) != kExp;
-    bad |= !fin;
-    x[i] = fin ? elem<BF16>(b) : 0.0f;
-  }
+constexpr uint32_t kExp = BF16 ? 0x7f807f80u : 0x7c007c00u;
+
+// The larger magnitudes of two pairs: as integers, without the signs, 16-bit
+// floats are in the order of their magnitudes, Inf and NaN above all.
+__device__ inline uint32_t max_pair(uint32_t top, uint4 w) {
+  top = __vmaxu2(top, __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu));
+  return __vmaxu2(top, __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
 }
 
-template <int FMT>
-__device__ inline uint2 codes8(const float (&x)[8], float r) {
-  uint32_t c[8];
-#pragma unroll
-  for (int i = 0; i < 8; i++) c[i] = code_of<FMT>(__fmul_rn(x[i], r));
-  return make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
+// Values that are not finite become 0.
+template <bool BF16>
+__device__ inline uint4 finite(uint4 w) {
+  auto one = [](uint32_t x) {
+    const uint32_t bad = __vcmpeq2(x & kExp<BF16>, kExp<BF16>);
+    return x & ~bad;
+  };
+  return make_uint4(one(w.x), one(w.y), one(w.z), one(w.w));
+}
+
+template <bool BF16>
+__device__ inline float2 pair(uint32_t w) {
+  if (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+template <int FMT, bool BF16>
+__device__ inline uint2 codes8(uint4 w, float r) {
+  const float2 a = pair<BF16>(w.x), b = pair<BF16>(w.y), c = pair<BF16>(w.z), d = pair<BF16>(w.w);
+  return make_uint2(codes_of<FMT>(__fmul_rn(a.x, r), __fmul_rn(a.y, r), __fmul_rn(b.x, r), __fmul_rn(b.y, r)),
+                    codes_of<FMT>(__fmul_rn(c.x, r), __fmul_rn(c.y, r), __fmul_rn(d.x, r), __fmul_rn(d.y, r)));
 }
 
 // One CTA per (page that gets rows, head, K or V): a pass for the largest
 // magnitude, one that writes codes.  A page of up to 128 x 64 values stays in
 // registers between the two; what is longer is read twice (the second time
-// from L2).
+// from L2).  Bound by HBM.
 template <int FMT, bool BF16>
 __global__ void __launch_bounds__(kThreads) k_write(const WriteArgs a) {
   const int b = blockIdx.x / a.per_seq, p = blockIdx.x % a.per_seq;
   const int h = blockIdx.y >> 1, kv = blockIdx.y & 1;
   const int r0 = a.cu[b], r1 = a.cu[b + 1], pos = a.start[b];
-  const int n = r1 - r0;
+  const int64_t n = int64_t(r1) - r0;
+  status_cleared();
+  auto report = [&](uint32_t bit) { atomicOr(a.status, bit); };
   if (r0 < 0 || r1 > a.n_rows || n < 0 || n > a.max_new || pos < 0 || int64_t(pos) + n > int64_t(a.stride) * a.bt) {
-    if (p == 0 && threadIdx.x == 0) atomicOr(a.status, kStBadArg);
+    if (p == 0 && threadIdx.x == 0) report(kStBadArg);
     return;
   }
   const int blk = pos / a.bt + p;
@@ -59,7 +73,7 @@ __global__ void __launch_bounds__(kThreads) k_write(const WriteArgs a) {
   if (t0 >= t1) return;
   const int page = a.table[int64_t(b) * a.stride + blk];
   if (uint32_t(page) >= uint32_t(a.n_blocks)) {
-    if (threadIdx.x == 0) atomicOr(a.status, kStBadArg);
+    if (threadIdx.x == 0) report(kStBadArg);
     return;
   }
   const int vpr = a.d >> 3, nv = int(t1 - t0) * vpr, s0 = int(t0 - first);
@@ -68,55 +82,61 @@ __global__ void __launch_bounds__(kThreads) k_write(const WriteArgs a) {
   float *scale = a.scale[kv] + int64_t(page) * a.H + h;
 
   uint4 held[kHeld];
-  float top = 0.0f;
-  bool bad = false;
+  uint32_t top2 = 0;
   auto load = [&](int i) { return *reinterpret_cast<const uint4 *>(src + int64_t(i / vpr) * a.st + (i % vpr) * 8); };
-  auto max8 = [&](uint4 w) {
-    float x[8];
-    finite8<BF16>(w, x, bad);
-#pragma unroll
-    for (int i = 0; i < 8; i++) top = fmaxf(top, fabsf(x[i]));
-  };
 #pragma unroll
   for (int k = 0; k < kHeld; k++)
     if (int(threadIdx.x) + k * kThreads < nv) held[k] = load(threadIdx.x + k * kThreads);
+  const float before = s0 > 0 ? *scale : 0.0f;
 #pragma unroll
   for (int k = 0; k < kHeld; k++)
-    if (int(threadIdx.x) + k * kThreads < nv) max8(held[k]);
-  for (int i = threadIdx.x + kHeld * kThreads; i < nv; i += kThreads) max8(load(i));
+    if (int(threadIdx.x) + k * kThreads < nv) top2 = max_pair(top2, held[k]);
+  for (int i = threadIdx.x + kHeld * kThreads; i < nv; i += kThreads) top2 = max_pair(top2, load(i));
 
-  __shared__ float s_top[kThreads / 32];
-  const float before = s0 > 0 ? *scale : 0.0f;
-  top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // not negative: ordered as integers
-  if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
-  if (__syncthreads_or(bad) && threadIdx.x == 0) atomicOr(a.status, kStNonfinite);
+  __shared__ uint32_t s_top[kThreads / 32];
+  auto join = [&](uint32_t pair) {  // over the CTA
+    const uint32_t t = __reduce_max_sync(0xffffffffu, max(pair & 0xffffu, pair >> 16));
+    if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = t;
+    __syncthreads();
+    uint32_t m = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; w++) top = fmaxf(top, s_top[w]);
-  float now = __fmul_rn(top, 1.0f / QMax<FMT>::v);
+    for (int w = 0; w < kThreads / 32; w++) m = max(m, s_top[w]);
+    return m;
+  };
+  uint32_t top = join(top2);
+  const bool bad = top >= (kExp<BF16> & 0xffffu);
+  if (bad) {  // rare: once more, without them
+    if (threadIdx.x == 0) report(kStNonfinite);
+    top2 = 0;
+#pragma unroll
+    for (int k = 0; k < kHeld; k++)
+      if (int(threadIdx.x) + k * kThreads < nv) held[k] = finite<BF16>(held[k]), top2 = max_pair(top2, held[k]);
+    for (int i = threadIdx.x + kHeld * kThreads; i < nv; i += kThreads) top2 = max_pair(top2, finite<BF16>(load(i)));
+    __syncthreads();
+    top = join(top2);
+  }
+  float now = __fmul_rn(pair<BF16>(top).x, 1.0f / QMax<FMT>::v);
   if (now < 0x1p-100f) now = 0.0f;
   if (s0 > 0) now = fmaxf(now, before);
   if (s0 > 0 && now > before) {  // the rows that were there, in the larger step
     const float ratio = __fdiv_rn(before, now);
-    for (int i = threadIdx.x; i < s0 * vpr; i += kThreads) {
-      uint2 *at = reinterpret_cast<uint2 *>(dst + int64_t(i) * 8);
-      const uint2 c = *at;
-      float x[8];
-#pragma unroll
-      for (int j = 0; j < 8; j++) x[j] = value_of<FMT>(((j < 4 ? c.x : c.y) >> (8 * (j & 3))) & 0xffu);
-      *at = codes8<FMT>(x, ratio);
+    for (int i = threadIdx.x; i < s0 * vpr * 2; i += kThreads) {
+      uint32_t *at = reinterpret_cast<uint32_t *>(dst + int64_t(i) * 4);
+      const uint32_t c = *at;
+      *at = codes_of<FMT>(__fmul_rn(value_of<FMT>(c & 0xff), ratio), __fmul_rn(value_of<FMT>(c >> 8 & 0xff), ratio),
+                          __fmul_rn(value_of<FMT>(c >> 16 & 0xff), ratio), __fmul_rn(value_of<FMT>(c >> 24), ratio));
     }
   }
   if (threadIdx.x == 0) *scale = now;
   const float r = now > 0.0f ? __fdiv_rn(1.0f, now) : 0.0f;
-  auto store = [&](int i, uint4 w) {
-    float x[8];
-    finite8<BF16>(w, x, bad);
-    *reinterpret_cast<uint2 *>(dst + int64_t(s0) * a.d + int64_t(i) * 8) = codes8<FMT>(x, r);
-  };
+  uint2 *to = reinterpret_cast<uint2 *>(dst + int64_t(s0) * a.d);
 #pragma unroll
   for (int k = 0; k < kHeld; k++)
-    if (int(threadIdx.x) + k * kThreads < nv) store(threadIdx.x + k * kThreads, held[k]);
-  for (int i = threadIdx.x + kHeld * kThreads; i < nv; i += kThreads) store(i, load(i));
+    if (int(threadIdx.x) + k * kThreads < nv) to[threadIdx.x + k * kThreads] = codes8<FMT, BF16>(held[k], r);
+  for (int i = threadIdx.x + kHeld * kThreads; i < nv; i += kThreads) {
+    const uint4 w = load(i);
+    to[i] = codes8<FMT, BF16>(bad ? finite<BF16>(w) : w, r);
+  }
 }
 
 }  // namespace
@@ -142,8 +162,8 @@ extern "C" cg_status cg_cache_write(const cg_cache *cache, const cg_rows *rows, 
   const int64_t gx = per_seq * rows->n_seq;
   if (gx > 0x7fffffff || 2 * int64_t(cache->H) > 65535) return CG_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(ws_dev, 0, 256, st) != cudaSuccess) return CG_ERR_CUDA;
-  if (rows->max_new == 0 || gx == 0) return CG_OK;
+  k_clear<<<1, 32, 0, st>>>(static_cast<uint32_t *>(ws_dev));
+  if (rows->max_new == 0) return launched();
   WriteArgs a{};
   a.src[0] = static_cast<const uint16_t *>(k_dev), a.src[1] = static_cast<const uint16_t *>(v_dev);
   a.pool[0] = static_cast<uint8_t *>(k_pool), a.pool[1] = static_cast<uint8_t *>(v_pool);
@@ -155,9 +175,8 @@ extern "C" cg_status cg_cache_write(const cg_cache *cache, const cg_rows *rows, 
   a.n_rows = rows->n_rows, a.max_new = rows->max_new, a.stride = rows->table_stride, a.per_seq = int(per_seq);
   const dim3 grid(unsigned(gx), unsigned(2 * cache->H));
   const bool e4m3 = cache->format == CG_CACHE_E4M3, bf16 = rows->dtype == CG_BF16;
-  if (e4m3 && bf16) k_write<CG_CACHE_E4M3, true><<<grid, kThreads, 0, st>>>(a);
-  if (e4m3 && !bf16) k_write<CG_CACHE_E4M3, false><<<grid, kThreads, 0, st>>>(a);
-  if (!e4m3 && bf16) k_write<CG_CACHE_INT8, true><<<grid, kThreads, 0, st>>>(a);
-  if (!e4m3 && !bf16) k_write<CG_CACHE_INT8, false><<<grid, kThreads, 0, st>>>(a);
-  return launched();
+  auto *const kernel = e4m3 ? (bf16 ? k_write<CG_CACHE_E4M3, true> : k_write<CG_CACHE_E4M3, false>)
+                            : (bf16 ? k_write<CG_CACHE_INT8, true> : k_write<CG_CACHE_INT8, false>);
+  const cudaError_t e = launch_early(kernel, grid, dim3(kThreads), 0, st, a);
+  return e == cudaSuccess ? launched() : CG_ERR_CUDA;
 }

@@ -1,10 +1,10 @@
 // cg_pages.cu -- the bookkeeping of pages that sequences share: extend, fork,
 // free, copy and compact.
 //
-// Each call that takes or renumbers pages has a plan, made by one CTA (the
-// plans are a scan over the reference counts, one pass of int32, and hold
-// their order without atomics whose order could change the result), and an
-// apply step over the whole GPU that moves pages and rewrites table rows.
+// A fork or a compaction has a plan, made by one CTA (a scan over the reference
+// counts, in order, so that no order of atomics can change the result), and a
+// step over the whole GPU that carries it out: table rows, counts, and the
+// pages that move.  That kernel is launched with the plan and waits for it.
 #include "cg_cache.cuh"
 
 namespace cg {
@@ -36,8 +36,8 @@ struct MoveArgs {
   float *const *scales;
   uint64_t page_bytes;
   int n_pools, H, n_blocks, parts;  // parts: pieces of kMoveBytes of a page
-  const int32_t *src, *dst, *n_dev;
-  int n;  // entries, where n_dev is null
+  const int32_t *src, *dst;
+  int n;  // entries of a copy
   uint32_t *status;
 };
 
@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(kPlan) k_extend(const PageArgs g) {
 // fork: a = parents, b = children
 __global__ void __launch_bounds__(kPlan) k_fork_plan(const PageArgs g) {
   const Book &w = g.w;
+  asm volatile("griddepcontrol.launch_dependents;");
   for (int i = threadIdx.x; i < g.n_seqs; i += kPlan) w.marks[i] = 0;
   __syncthreads();
   bool bad = false;
@@ -199,11 +200,10 @@ __global__ void __launch_bounds__(kPlan) k_fork_plan(const PageArgs g) {
   }
 }
 
-// The children's rows, counts and lengths: one CTA per pair.
-__global__ void __launch_bounds__(kMove) k_fork_rows(const PageArgs g) {
+// A fork's pair i: the child's row, counts and length, by one CTA.
+__device__ void fork_row(const PageArgs &g, int i) {
   const Book &w = g.w;
-  if (!*w.go) return;
-  const int i = blockIdx.x, len = g.len[g.a[i]], used = pages_of(len, g.bt), r = w.rank[i];
+  const int len = g.len[g.a[i]], used = pages_of(len, g.bt), r = w.rank[i];
   const int32_t *row = g.table + int64_t(g.a[i]) * g.stride;
   int32_t *to = g.table + int64_t(g.b[i]) * g.stride;
   for (int j = threadIdx.x; j < g.stride; j += kMove) {
@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(kMove) k_fork_rows(const PageArgs g) {
 // free: a = sequences, one CTA each
 __global__ void __launch_bounds__(kMove) k_free(const PageArgs g) {
   const int s = g.a[blockIdx.x];
+  status_cleared();
   if (uint32_t(s) >= uint32_t(g.n_seqs)) {
     if (threadIdx.x == 0) atomicOr(g.w.status, kStBadArg);
     return;
@@ -254,6 +255,7 @@ __global__ void __launch_bounds__(kMove) k_free(const PageArgs g) {
 // page p's move, as a hole (p < n_live) or a mover, or -1.  marks is not used.
 __global__ void __launch_bounds__(kPlan) k_compact_plan(const PageArgs g, int32_t *n_live_out, int32_t *moved_refs) {
   const Book &w = g.w;
+  asm volatile("griddepcontrol.launch_dependents;");
   int mine = 0, n_live;
   for (int64_t p = threadIdx.x; p < g.n_blocks; p += kPlan) mine += g.refs[p] > 0;
   scan(mine, &n_live);
@@ -277,8 +279,8 @@ __global__ void __launch_bounds__(kPlan) k_compact_plan(const PageArgs g, int32_
   }
 }
 
-__global__ void __launch_bounds__(kMove) k_compact_book(const PageArgs g, int32_t *refs_out, int32_t *table_out,
-                                                        const int32_t *moved_refs) {
+// A compaction's counts and table, by the whole grid.
+__device__ void compact_book(const PageArgs &g, int32_t *refs_out, int32_t *table_out, const int32_t *moved_refs) {
   const Book &w = g.w;
   const int n_live = *w.n_live;
   const int64_t entries = int64_t(g.n_seqs) * g.stride, step = int64_t(gridDim.x) * kMove;
@@ -296,11 +298,21 @@ __global__ void __launch_bounds__(kMove) k_compact_book(const PageArgs g, int32_
   }
 }
 
-// Pages src[i] -> dst[i] of every pool, with their scales.  Bound by HBM: a
-// CTA moves 32 KB at a time, each thread with four 16-byte loads in flight.
-template <typename V>
-__global__ void __launch_bounds__(kMove) k_move(const MoveArgs g) {
-  const int n = g.n_dev ? *g.n_dev : g.n;
+enum What { kCopy, kFork, kCompact };
+
+// Pages src[i] -> dst[i] of every pool, with their scales, and the rest of
+// what a plan asks for.  Bound by HBM: a CTA moves 32 KB at a time, each thread
+// with eight 16-byte loads in flight.
+template <What W, typename V>
+__global__ void __launch_bounds__(kMove) k_move(const MoveArgs g, const PageArgs b, int32_t *refs_out, int32_t *table_out,
+                                                const int32_t *moved_refs) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (W == kFork) {
+    if (!*b.w.go) return;
+    for (int i = blockIdx.x; i < b.n; i += gridDim.x) fork_row(b, i);
+  }
+  if (W == kCompact) compact_book(b, refs_out, table_out, moved_refs);
+  const int n = W == kCopy ? g.n : *b.w.moves;
   const int64_t units = int64_t(g.n_pools) * n * g.parts;
   constexpr int kVecs = kMoveBytes / int(sizeof(V));
   const int64_t page_vecs = int64_t(g.page_bytes / sizeof(V));
@@ -321,12 +333,12 @@ __global__ void __launch_bounds__(kMove) k_move(const MoveArgs g) {
     V *to = reinterpret_cast<V *>(base + g.page_bytes * uint64_t(t)) + int64_t(part) * kVecs;
     const int m = int(min(int64_t(kVecs), page_vecs - int64_t(part) * kVecs));
     int x = threadIdx.x;
-    for (; x + 3 * kMove < m; x += 4 * kMove) {
-      V v[4];
+    for (; x + 7 * kMove < m; x += 8 * kMove) {
+      V v[8];
 #pragma unroll
-      for (int k = 0; k < 4; k++) v[k] = from[x + k * kMove];
+      for (int k = 0; k < 8; k++) v[k] = from[x + k * kMove];
 #pragma unroll
-      for (int k = 0; k < 4; k++) to[x + k * kMove] = v[k];
+      for (int k = 0; k < 8; k++) to[x + k * kMove] = v[k];
     }
     for (; x < m; x += kMove) to[x] = from[x];
     if (part == 0 && g.scales) {
@@ -362,23 +374,23 @@ PageArgs page_args(const cg_cache *c, const cg_pages *p, int32_t n, const int32_
   return g;
 }
 
-cg_status move_pages(const cg_cache *c, void *const *pools, float *const *scales, int64_t n, const int32_t *src,
-                     const int32_t *dst, const int32_t *n_dev, void *ws, cudaStream_t st) {
+// Launches k_move behind a plan (or k_clear); n: the most pages that can move.
+template <What W>
+cg_status move_pages(const cg_cache *c, void *const *pools, float *const *scales, int64_t n, const int32_t *src, const int32_t *dst,
+                     const PageArgs &g, int32_t *refs_out, int32_t *table_out, const int32_t *moved_refs, void *ws, cudaStream_t st) {
   MoveArgs m{};
   m.pools = reinterpret_cast<uint8_t *const *>(pools);
   m.scales = scales;
   m.page_bytes = page_bytes(c);
   m.n_pools = 2 * c->L, m.H = c->H, m.n_blocks = c->n_blocks;
   m.parts = int((m.page_bytes + kMoveBytes - 1) / kMoveBytes);
-  m.src = src, m.dst = dst, m.n_dev = n_dev, m.n = int(n);
+  m.src = src, m.dst = dst, m.n = int(n);
   m.status = static_cast<uint32_t *>(ws);
   const int64_t units = n * m.n_pools * m.parts, most = kSMs * 8;
-  const unsigned grid = unsigned(units < most ? units : most);
-  if (m.page_bytes % 16 == 0)
-    k_move<uint4><<<grid, kMove, 0, st>>>(m);
-  else
-    k_move<uint2><<<grid, kMove, 0, st>>>(m);
-  return launched();
+  const dim3 grid(unsigned(units < most ? units : most)), block(kMove);
+  const cudaError_t e = m.page_bytes % 16 == 0 ? launch_early(k_move<W, uint4>, grid, block, 0, st, m, g, refs_out, table_out, moved_refs)
+                                               : launch_early(k_move<W, uint2>, grid, block, 0, st, m, g, refs_out, table_out, moved_refs);
+  return e == cudaSuccess ? launched() : CG_ERR_CUDA;
 }
 
 }  // namespace
@@ -411,11 +423,8 @@ extern "C" cg_status cg_pages_fork(const cg_cache *cache, const cg_pages *pages,
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const PageArgs g = page_args(cache, pages, n, parent_dev, child_dev, ws_dev);
   k_fork_plan<<<1, kPlan, 0, st>>>(g);
-  if (n > 0) k_fork_rows<<<n, kMove, 0, st>>>(g);
-  cg_status rc = launched();
-  if (rc == CG_OK && n > 0)
-    rc = move_pages(cache, pools_dev, scales_dev, n, g.w.src, g.w.dst, g.w.moves, ws_dev, st);
-  return rc;
+  if (n == 0) return launched();
+  return move_pages<kFork>(cache, pools_dev, scales_dev, n, g.w.src, g.w.dst, g, nullptr, nullptr, nullptr, ws_dev, st);
 }
 
 extern "C" cg_status cg_pages_free(const cg_cache *cache, const cg_pages *pages, int32_t n, const int32_t *seq_dev,
@@ -424,9 +433,10 @@ extern "C" cg_status cg_pages_free(const cg_cache *cache, const cg_pages *pages,
       !ws_ok(ws_dev, ws_bytes, cg_pages_workspace_bytes(cache, pages, n)))
     return CG_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(ws_dev, 0, 256, st) != cudaSuccess) return CG_ERR_CUDA;
-  if (n > 0) k_free<<<n, kMove, 0, st>>>(page_args(cache, pages, n, seq_dev, nullptr, ws_dev));
-  return launched();
+  k_clear<<<1, 32, 0, st>>>(static_cast<uint32_t *>(ws_dev));
+  if (n == 0) return launched();
+  const cudaError_t e = launch_early(k_free, dim3(unsigned(n)), dim3(kMove), 0, st, page_args(cache, pages, n, seq_dev, nullptr, ws_dev));
+  return e == cudaSuccess ? launched() : CG_ERR_CUDA;
 }
 
 extern "C" cg_status cg_pages_copy(const cg_cache *cache, void *const *pools_dev, float *const *scales_dev, int32_t n,
@@ -436,9 +446,9 @@ extern "C" cg_status cg_pages_copy(const cg_cache *cache, void *const *pools_dev
       !is_aligned(src_dev, 4) || !is_aligned(dst_dev, 4) || !ws_ok(ws_dev, ws_bytes, 256))
     return CG_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(ws_dev, 0, 256, st) != cudaSuccess) return CG_ERR_CUDA;
-  if (n == 0) return CG_OK;
-  return move_pages(cache, pools_dev, scales_dev, n, src_dev, dst_dev, nullptr, ws_dev, st);
+  k_clear<<<1, 32, 0, st>>>(static_cast<uint32_t *>(ws_dev));
+  if (n == 0) return launched();
+  return move_pages<kCopy>(cache, pools_dev, scales_dev, n, src_dev, dst_dev, PageArgs{}, nullptr, nullptr, nullptr, ws_dev, st);
 }
 
 extern "C" cg_status cg_pages_compact(const cg_cache *cache, const cg_pages *pages, void *const *pools_dev,
@@ -453,11 +463,7 @@ extern "C" cg_status cg_pages_compact(const cg_cache *cache, const cg_pages *pag
   int32_t *moved_refs = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws_dev) +
                                                     book_bytes(pages, most_of(cache, 0), nullptr, nullptr));
   k_compact_plan<<<1, kPlan, 0, st>>>(g, n_live_dev, moved_refs);
-  k_compact_book<<<kSMs, kMove, 0, st>>>(g, refs_out_dev, table_out_dev, moved_refs);
-  cg_status rc = launched();
   // at most half of the pages move
-  if (rc == CG_OK)
-    rc = move_pages(cache, pools_dev, scales_dev, (int64_t(cache->n_blocks) + 1) / 2, g.w.src, g.w.dst, g.w.moves, ws_dev,
-                    st);
-  return rc;
+  return move_pages<kCompact>(cache, pools_dev, scales_dev, (int64_t(cache->n_blocks) + 1) / 2, g.w.src, g.w.dst, g, refs_out_dev, table_out_dev,
+                              moved_refs, ws_dev, st);
 }

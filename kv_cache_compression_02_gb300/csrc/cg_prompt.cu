@@ -800,13 +800,7 @@ cudaError_t launch(const PromptArgs &a, unsigned grid, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(k_prompt<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   k_prompt<D, BF16><<<grid, kThreads, kSmem, st>>>(a);
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, kRows / 8), cfg.blockDim = dim3(2 * D), cfg.stream = st;
-  cfg.attrs = &early, cfg.numAttrs = 1;
-  const cudaError_t e2 = cudaLaunchKernelEx(&cfg, k_prompt_join<D, BF16>, a);
+  const cudaError_t e2 = launch_early(k_prompt_join<D, BF16>, dim3(grid, kRows / 8), dim3(2 * D), 0, st, a);
   return e2 != cudaSuccess ? e2 : cudaGetLastError();
 }
 
