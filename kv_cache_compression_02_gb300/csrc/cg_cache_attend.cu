@@ -37,6 +37,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kTok = 32;              // positions of a warp's tile
 constexpr int kUnit = kTok * kWarps;  // positions of a unit
 constexpr int kShort = 2;             // units of an item that one CTA takes where items are few
+constexpr int kIn = 2;                // what an item's way in and out costs, in units (measured: 2.6 and 1.4 us)
 constexpr int kLens = 512;            // sequences whose lengths are kept in shared memory
 
 // NB blocks of eight query rows make an item.  One block leaves room for three
@@ -266,9 +267,8 @@ __global__ void __launch_bounds__(kThreads, Shape<NB>::kPerSM) k_attend(const __
     sm.errors = sm.dead = 0;
     a.notes[blockIdx.x].parts = 0;
   }
-  // The items of the call and what they cost.  An item costs its units and
-  // one more (its queries' way in, the warps' join and the way out take about
-  // as long).  Where items are few and short each has a CTA of its own.
+  // The items of the call and what they cost: their units and kIn.  Where items
+  // are few and short each has a CTA of its own.
   const int per = (a.B + kThreads - 1) / kThreads, b0 = threadIdx.x * per, b1 = min(a.B, b0 + per);
   int64_t cost = 0, items = 0;
   int most = 0;
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, Shape<NB>::kPerSM) k_attend(const __
     const int n = a.len[b], fit = clamped_length(a, b), tiles = tiles_of(fit);
     bad_len |= n != fit;
     if (a.B <= kLens) sm.len[b] = fit;
-    cost += tiles ? tiles + 1 : 0;
+    cost += tiles ? tiles + kIn : 0;
     items += tiles > 0;
     most = max(most, tiles);
   }
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, Shape<NB>::kPerSM) k_attend(const __
     return;
   }
   const int64_t lo = total * blockIdx.x / ctas, hi = total * (blockIdx.x + 1) / ctas;
-  auto cost_of = [&](int tiles) { return single ? (tiles > 0) : tiles ? tiles + 1 : 0; };
+  auto cost_of = [&](int tiles) { return single ? (tiles > 0) : tiles ? tiles + kIn : 0; };
   if (lo >= before && lo < before + cost) {  // one thread's sequences hold the first unit
     int64_t at = before;
     int b = b0;
@@ -347,8 +347,8 @@ __global__ void __launch_bounds__(kThreads, Shape<NB>::kPerSM) k_attend(const __
   cur.h = item0 / a.RT, cur.rt = item0 % a.RT;
   int64_t item_lo = sm.prefix + int64_t(item0) * item_cost;  // where the item's cost begins
   // A run [lo, hi) of costs has the tiles whose costs lie in it; an item's
-  // first cost is no tile.
-  const int skip = single ? 0 : 1;
+  // first kIn costs are no tiles.
+  const int skip = single ? 0 : kIn;
   cur.tile = max(0, int(lo - item_lo) - skip);
   int units = 0;  // tiles of the run
   if (single) {
@@ -360,12 +360,12 @@ __global__ void __launch_bounds__(kThreads, Shape<NB>::kPerSM) k_attend(const __
     int w_cost = item_cost;
     while (at < hi) {  // item by item
       const int64_t end = min(hi, w_lo + w_cost);
-      units += int(max(int64_t(0), end - w_lo - 1) - max(int64_t(0), at - w_lo - 1));
+      units += int(max(int64_t(0), end - w_lo - kIn) - max(int64_t(0), at - w_lo - kIn));
       at = end;
       if (at < hi) {
         w_lo += w_cost;
         next_item(a, sm.len, w);
-        w_cost = w.tiles + 1;
+        w_cost = w.tiles + kIn;
       }
     }
   }
