@@ -34,8 +34,8 @@ namespace {
 
 constexpr int kThreads = 384;
 // Registers a thread: 384 are launched with 168 each; the softmax warpgroups
-// take 200, which the third leaves them (2 * 200 + 104 = 3 * 168).
-constexpr int kSoftRegs = 200, kOtherRegs = 104;
+// take 224, which the third leaves them (2 * 224 + 56 = 3 * 168).
+constexpr int kSoftRegs = 224, kOtherRegs = 56;
 constexpr int kTile = 128;   // rows of a tile, keys of a tile
 constexpr int kRows = 2 * kTile;
 constexpr int kGrid = kSMs;
@@ -584,22 +584,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
             for (int i = 0; i < kTile; i++)
               if (i > lim) x[i] = 0xff800000u;
           }
-          float base = kLift - (m == -INFINITY ? 0.0f : m);
-          float2 sums[4];
-          uint32_t pk[16];
-          auto quarter = [&](int c) {  // 32 probabilities
-#pragma unroll
-            for (int i = 0; i < 16; i++) {
-              float2 y = make_float2(__uint_as_float(x[32 * c + 2 * i]), __uint_as_float(x[32 * c + 2 * i + 1]));
-              y = fma2(y, sc, make_float2(base, base));
-              y = make_float2(ex2(y.x), ex2(y.y));
-              sums[i & 3] = c == 0 && i < 4 ? y : add2(sums[i & 3], y);
-              pk[i] = pack<BF16>(y.x, y.y);
-            }
-          };
-          // The maximum, and meanwhile the first quarter under the maximum so
-          // far, which holds for most tiles.
-          if (j > 0) quarter(0);
           float top[4];
 #pragma unroll
           for (int i = 0; i < 4; i++) top[i] = fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 4]));
@@ -609,27 +593,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
             for (int k = 0; k < 4; k++) top[k] = max3(top[k], __uint_as_float(x[i + 2 * k]), __uint_as_float(x[i + 2 * k + 1]));
           const float now = max3(top[0], top[1], fmaxf(top[2], top[3])) * a.scale_log2;
           const bool moved = now > m + kLag;
-          if (j == 0 || __any_sync(0xffffffffu, moved)) {
-            const float keep = moved ? ex2(m - now) : 1.0f;
-            if (moved) m = now;
-            base = kLift - (m == -INFINITY ? 0.0f : m);
-            if (j > 0) {
-              l = mul2(l, make_float2(keep, keep));
+          const float keep = moved ? ex2(m - now) : 1.0f;
+          if (moved) m = now;
+          if (j > 0 && __any_sync(0xffffffffu, moved)) {
+            l = mul2(l, make_float2(keep, keep));
 #pragma unroll
-              for (int c = 0; c < D / 32; c++) {
-                uint32_t y[32];
-                tm_load(o_at + 32 * c, y);
-                tm_wait_ld();
+            for (int c = 0; c < D / 32; c++) {
+              uint32_t y[32];
+              tm_load(o_at + 32 * c, y);
+              tm_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; i++) y[i] = __float_as_uint(__uint_as_float(y[i]) * keep);
-                tm_store32(o_at + 32 * c, y);
-              }
+              for (int i = 0; i < 32; i++) y[i] = __float_as_uint(__uint_as_float(y[i]) * keep);
+              tm_store32(o_at + 32 * c, y);
             }
-            quarter(0);
           }
+          const float base = kLift - (m == -INFINITY ? 0.0f : m);
+          float2 sums[4] = {};
 #pragma unroll
           for (int c = 0; c < 4; c++) {
-            if (c > 0) quarter(c);
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+              float2 y = make_float2(__uint_as_float(x[32 * c + 2 * i]), __uint_as_float(x[32 * c + 2 * i + 1]));
+              y = fma2(y, sc, make_float2(base, base));
+              y = make_float2(ex2(y.x), ex2(y.y));
+              sums[i & 3] = add2(sums[i & 3], y);
+              pk[i] = pack<BF16>(y.x, y.y);
+            }
             tm_store16(s_at + 16 * c, pk);
             if (c & 1) {  // half of P is there
               tm_wait_st();
