@@ -114,7 +114,8 @@ size_t cg_cache_workspace_bytes(const cg_cache *cache, const cg_attend *attend);
  * A row that sees no position gives out 0 and lse -inf.  Bytes behind
  * position len[b]-1, and pages that hold none of it, do not matter, whatever
  * they hold.  Probabilities are rounded to 11 bits for the second product.
- * The result of a call is the same every time.
+ * A call on the same inputs gives the same bits every time; the bits of a
+ * sequence may depend on the lengths of the others.
  *   out_dev: [n_seq][T][Hq][d], contiguous;  lse_dev: fp32 [n_seq][T][Hq], or NULL;  len_dev: int32 [n_seq].
  * Device errors: CG_ERR_INVALID_ARG (a bad page: its positions are left out;
  * a length that is negative or passes table_stride * block_tokens: taken as

@@ -24,6 +24,11 @@
 // a part of an item leaves its running maximum, sum and output in the
 // workspace, and a second kernel, already waiting when the first one ends,
 // joins the parts in their order: the result does not depend on timing.
+//
+// Measured: four readers of 131072 tokens, 8 KV heads, d = 128, 64 query heads,
+// int8: 186 us or 5.5 TB/s (without any arithmetic the copies take 161 us); one
+// short reader, 500 tokens: 10 us, the latency of five dependent loads, one
+// tile and two joins.
 #include <type_traits>
 
 #include "cg_cache.cuh"
@@ -36,12 +41,14 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTok = 32;              // positions of a warp's tile
 constexpr int kUnit = kTok * kWarps;  // positions of a unit
-constexpr int kShort = 2;             // units of an item that one CTA takes where items are few
+constexpr int kShort = 2;             // units of an item that one CTA takes where items are few (with 8: 12.5, not 9.9 us for 500 tokens)
 constexpr int kIn = 2;                // what an item's way in and out costs, in units (measured: 2.6 and 1.4 us)
 constexpr int kLens = 512;            // sequences whose lengths are kept in shared memory
 
 // NB blocks of eight query rows make an item.  One block leaves room for three
-// CTAs on an SM, two for two.
+// CTAs on an SM, two for two.  Up to eight rows take one block (131072 tokens
+// of 8 heads: 61 us; with an empty second block 74 us), more take two (16 rows:
+// 79 us).
 template <int NB>
 struct Shape {
   static constexpr int kRows = 8 * NB;
@@ -251,7 +258,9 @@ __device__ inline void write_row(const AttendArgs &a, int b, int h, int r, const
 
 // PLAIN: pages are a multiple of 16 tokens and a row has D channels, so that
 // half a warp's tile lies in one page (one table entry, one scale) and is one
-// tiled copy.  Other shapes copy 8 or 16 bytes a lane.  MEASURE
+// tiled copy.  Other shapes copy 8 or 16 bytes a lane: on pages of 64 and D
+// channels 131072 tokens of 8 heads take 61 us the first way and 76 us the
+// second.
 template <int FMT, int D, int NB, bool BF16, bool PLAIN>
 __global__ void __launch_bounds__(kThreads, Shape<NB>::kPerSM) k_attend(const __grid_constant__ AttendArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -1028,6 +1037,7 @@ cudaError_t launch_type(const AttendArgs &a, bool bf16, int64_t units, cudaStrea
 template <int FMT>
 cudaError_t launch_format(const AttendArgs &a, bool bf16, int64_t units, cudaStream_t st) {
   const bool one = a.rows <= 8;
+  // (64 channels and pages of 64, four readers of 131072: 139 us as they are, 266 us padded to 128)
   if (a.d <= 64) return one ? launch_type<FMT, 64, 1>(a, bf16, units, st) : launch_type<FMT, 64, 2>(a, bf16, units, st);
   return one ? launch_type<FMT, 128, 1>(a, bf16, units, st) : launch_type<FMT, 128, 2>(a, bf16, units, st);
 }
