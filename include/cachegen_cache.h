@@ -113,7 +113,8 @@ size_t cg_cache_workspace_bytes(const cg_cache *cache, const cg_attend *attend);
  *   out = sum exp(s_j - lse) v_j,   k_j, v_j = code * scale of their page.
  * A row that sees no position gives out 0 and lse -inf.  Bytes behind
  * position len[b]-1, and pages that hold none of it, do not matter, whatever
- * they hold.  Probabilities are rounded to 11 bits for the second product.
+ * they hold.  Probabilities carry 22 bits into the second product (11 where
+ * they are under 2^-26 of the largest).
  * A call on the same inputs gives the same bits every time; the bits of a
  * sequence may depend on the lengths of the others.
  *   out_dev: [n_seq][T][Hq][d], contiguous;  lse_dev: fp32 [n_seq][T][Hq], or NULL;  len_dev: int32 [n_seq].
@@ -144,10 +145,10 @@ size_t cg_prompt_workspace_bytes(const cg_prompt *prompt);
  * last ones of its keys, so query i of nq sees keys j <= i + nk - nq (a
  * prompt behind a loaded context has nk > nq; where nk < nq the first rows
  * see nothing and give out 0, lse -inf).  Formulas as at cg_cache_attend.
- * Rows of other sequences do not matter, whatever they hold; an Inf or NaN in
- * a key's V row of the same sequence may reach the rows of the same call's
- * sequence that are up to 128 positions before it.  Probabilities are rounded
- * to the type of the rows for the second product.
+ * Rows of other sequences, and keys that a row does not see, do not matter,
+ * whatever they hold.  Probabilities are rounded to the type of the rows for
+ * the second product.  A call on the same inputs gives the same bits every
+ * time; the bits of a sequence may depend on the lengths of the others.
  *   out_dev: [n_q][Hq][d], contiguous;  lse_dev: fp32 [n_q][Hq], or NULL;
  *   rows of q outside every sequence get no output.
  * Device errors: CG_ERR_INVALID_ARG (offsets that fall, pass n_q or n_k, or

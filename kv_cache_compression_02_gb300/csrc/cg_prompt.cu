@@ -11,7 +11,8 @@
 // exponentials come next.  So the two tiles take turns: while the tensor cores
 // work for one, a warpgroup computes the other's probabilities, one row a
 // thread.  Warps: 0-3 and 4-7 the softmax of tiles a and b, 8 the loads (TMA),
-// 9 the products.  TMEM: S of both tiles (P lies over S), O of both.
+// 9 the products, 10 looks after V's tiles that some row sees a part of only.
+// TMEM: S of both tiles (P lies over S), O of both.
 //
 //   products:  S_a(0) S_b(0) | PV_a(j) S_a(j+1) PV_b(j) S_b(j+1) ...
 //   softmax a: waits for S_a(j): maximum, exponentials, P_a(j); O_a is scaled
@@ -34,8 +35,8 @@ namespace {
 
 constexpr int kThreads = 384;
 // Registers a thread: 384 are launched with 168 each; the softmax warpgroups
-// take 224, which the third leaves them (2 * 224 + 56 = 3 * 168).
-constexpr int kSoftRegs = 224, kOtherRegs = 56;
+// take 216, which the third leaves them (2 * 216 + 72 = 3 * 168).
+constexpr int kSoftRegs = 216, kOtherRegs = 72;
 constexpr int kTile = 128;   // rows of a tile, keys of a tile
 constexpr int kRows = 2 * kTile;
 constexpr int kGrid = kSMs;
@@ -66,6 +67,18 @@ struct Todo {
   int cnt[2], tok[2];   // as in Part; cnt[0] < 0: the end
   int nq, nk, keys;     // keys: from the part's first on
   int q0, head, slot;   // head: the first query head; slot of the workspace, or -1: the item is whole
+  int cut;              // the part's first key tile that not every row sees all of
+  int careful;
+};
+
+// A product takes 0 * V for keys that a row does not see, which must not be
+// NaN.  V's cut tiles are looked through for values that are not finite while
+// the products run; where there is one, the CTA goes over its run once more,
+// carefully: in cut tiles such values become 0 before the product, and the
+// first keys that had one, of each channel, are kept for the way out.
+template <int D>
+struct Odd {
+  uint16_t nan[D], up[D], down[D];  // NaN, inf, -inf: keys from the first cut tile on; 0xffff: none
 };
 
 template <int D>
@@ -74,10 +87,12 @@ struct Smem {
   static constexpr int kChunks = D / 64;  // of 64 channels: 128 bytes, a swizzled row
   uint8_t q[2][kChunks][kTile * 128];
   uint8_t kv[kStages][kChunks][kTile * 128];
-  uint64_t todo_full[2], todo_empty[2], q_full, q_empty, kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2][2], o_full[2];  // p_full: of the first and the second 64 keys
+  uint64_t todo_full[2], todo_empty[2], q_full, q_empty, kv_full[kStages], kv_empty[kStages], v_ok[kStages], odd_full[2], s_full[2], p_full[2][2], o_full[2];  // p_full: of the first and the second 64 keys
   uint8_t out[8][32 * 128];  // a softmax warp's rows on their way out, 64 channels at a time
+  Odd<D> odd[2];             // of the parts, by their turns
+  uint32_t any_odd[2];
   Todo todo[2];              // the parts of the run, by turns, from the loading warp to the others
-  uint32_t tmem, errors, dead;
+  uint32_t tmem, errors, dead, again;  // again: the run is to be gone over once more
   int most[kThreads / 32], b;
   int64_t sum[kThreads / 32][2], prefix;
 };
@@ -318,11 +333,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
 
   asm volatile("griddepcontrol.launch_dependents;");
   if (threadIdx.x == 0) {
-    sm.errors = sm.dead = 0;
+    sm.errors = sm.dead = sm.again = 0;
     a.notes[blockIdx.x].parts = 0;
     bar_init(&sm.q_full, 1), bar_init(&sm.q_empty, 1);
-    for (int i = 0; i < 2; i++) bar_init(&sm.todo_full[i], 1), bar_init(&sm.todo_empty[i], 9);  // the products' warp and eight
-    for (int i = 0; i < kStages; i++) bar_init(&sm.kv_full[i], 1), bar_init(&sm.kv_empty[i], 1);
+    for (int i = 0; i < 2; i++) bar_init(&sm.todo_full[i], 1), bar_init(&sm.todo_empty[i], 10), bar_init(&sm.odd_full[i], 1);  // ten warps read it
+    for (int i = 0; i < kStages; i++) bar_init(&sm.kv_full[i], 1), bar_init(&sm.kv_empty[i], 1 + (i & 1)), bar_init(&sm.v_ok[i], 1);  // odd stages hold V
     for (int t = 0; t < 2; t++) bar_init(&sm.s_full[t], 1), bar_init(&sm.p_full[t][0], kTile / 32), bar_init(&sm.p_full[t][1], kTile / 32), bar_init(&sm.o_full[t], 1);
     bar_init_fence();
   }
@@ -415,19 +430,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
         uint32_t kv_phase = 1, q_phase = 1, todo_phase = 1;  // the first pass over a ring finds it empty
         bool ok = true;
         const uint32_t q_bytes = uint32_t(kChunks) * 128 * a.G * a.TG;
+        const Run begin = run;
+        int careful = 0;
         for (;;) {
           const bool more = run.next(a, p);
           if (!(ok = bar_wait(&sm.todo_empty[turn], todo_phase, &sm.dead))) break;
           Todo &todo = sm.todo[turn];
           if (!more) {
-            todo.cnt[0] = -1;
+            if (!careful) {  // once all is done: is it to be gone over again?
+              if (!(ok = bar_wait(&sm.todo_empty[turn ^ 1], turn ? todo_phase ^ 1 : todo_phase, &sm.dead))) break;
+              if (*static_cast<volatile uint32_t *>(&sm.again)) {
+                careful = 1;
+                run = begin;
+                seg = 0;
+                continue;
+              }
+            }
+            todo.cnt[0] = todo.cnt[1] = -1;
             bar_arrive(&sm.todo_full[turn]);
             break;
           }
+          todo.careful = careful;
           // who has key tiles of this item
           const int64_t c0 = ((p.first + 1) * ctas - 1) / total, c1 = ((p.last + 1) * ctas - 1) / total;
           for (int t = 0; t < 2; t++) todo.cnt[t] = p.cnt[t], todo.tok[t] = p.tok[t];
           todo.nq = p.nq, todo.nk = p.nk, todo.keys = p.nk - p.j0 * kTile, todo.q0 = p.q0, todo.head = p.h * a.G;
+          const int least = min(p.nk - 1, p.nk - p.nq + p.tok[p.cnt[0] > 0 ? 0 : 1]) - p.j0 * kTile;  // the last key of the first row
+          todo.cut = max(0, least + 1) / kTile;
           todo.slot = c0 == c1 ? -1 : 2 * int(blockIdx.x) + (seg > 0);  // slot 1: the run's last part
           bar_arrive(&sm.todo_full[turn]);
           if (c0 != c1 && int64_t(blockIdx.x) == c0) {
@@ -462,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
       constexpr uint32_t kChunk = kTile * 128 >> 4, kStage = kTileBytes >> 4;
       const uint32_t q_lo = operand_lo(sm.q[0], 16), k_lo = operand_lo(sm.kv[0], 16), v_lo = operand_lo(sm.kv[0], kTile * 128);
       int stage = 0, turn = 0;
-      uint32_t kv_phase = 0, q_phase = 0, todo_phase = 0, p_phase[2] = {0, 0};
+      uint32_t kv_phase = 0, q_phase = 0, todo_phase = 0, p_phase[2] = {0, 0}, v_phases = 0;
       bool ok = true;
       auto advance = [&] {
         if (++stage == kStages) stage = 0, kv_phase ^= 1;
@@ -478,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
       };
       for (;;) {
         if (!(ok = bar_wait(&sm.todo_full[turn], todo_phase, &sm.dead))) break;
-        const int cnt[2] = {sm.todo[turn].cnt[0], sm.todo[turn].cnt[1]}, keys = sm.todo[turn].keys;
+        const int cnt[2] = {sm.todo[turn].cnt[0], sm.todo[turn].cnt[1]}, cut = sm.todo[turn].cut, keys = sm.todo[turn].keys, careful = sm.todo[turn].careful;
         __syncwarp();
         if (lane == 0) bar_arrive(&sm.todo_empty[turn]);
         turn ^= 1;
@@ -505,12 +534,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
           const uint32_t k_phase = kv_phase;
           const bool more = j + 1 < n;
           if (!(ok = bar_wait(&sm.kv_full[vs], v_phase, &sm.dead))) break;
-          const int left = keys - j * kTile;  // keys from here on
-          if (left < kTile) {  // what lies behind the last key must not reach a product: 0 * NaN
-            for (int i = lane; i < kTile * 8 * kChunks; i += 32)
-              if (i / 8 % kTile >= left) reinterpret_cast<uint4 *>(sm.kv[vs][0])[i] = make_uint4(0, 0, 0, 0);
-            fence_async();
-            __syncwarp();
+          if (careful ? j >= cut : keys - j * kTile < kTile) {  // V is being put right
+            if (!(ok = bar_wait(&sm.v_ok[vs], v_phases >> vs & 1, &sm.dead))) break;
+            v_phases ^= 1u << vs;
           }
           if (more && !(ok = bar_wait(&sm.kv_full[ks], k_phase, &sm.dead))) break;
 #pragma unroll
@@ -543,6 +569,82 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
         }
         if (!ok) break;
       }
+      } else if (warp == 10) {
+        // ---- V of cut tiles ----
+        int stage = 0, turn = 0;
+        uint32_t kv_phase = 0, todo_phase = 0;
+        bool ok = true;
+        constexpr int kMine = D / 32;  // channels of a lane
+        constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;
+        for (;;) {
+          if (!(ok = bar_wait(&sm.todo_full[turn], todo_phase, &sm.dead))) break;
+          const int n = max(sm.todo[turn].cnt[0], sm.todo[turn].cnt[1]), keys = sm.todo[turn].keys, cut = sm.todo[turn].cut;
+          const bool careful = sm.todo[turn].careful;
+          uint32_t nan[kMine], up[kMine], down[kMine];
+          bool any = false;
+#pragma unroll
+          for (int k = 0; k < kMine; k++) nan[k] = up[k] = down[k] = 0xffffu;
+          for (int j = 0; j < n; j++) {
+            const int vs = stage + 1;  // K is at `stage`
+            if (!(ok = bar_wait(&sm.kv_full[vs], kv_phase, &sm.dead))) break;
+            if (j >= cut) {
+              const int left = min(kTile, keys - j * kTile);  // keys of the tile
+              uint4 *v = reinterpret_cast<uint4 *>(sm.kv[vs][0]);
+              if (left < kTile) {  // nothing behind the last key
+                for (int i = lane; i < kTile * 8 * kChunks; i += 32)
+                  if (i / 8 % kTile >= left) v[i] = make_uint4(0, 0, 0, 0);
+                fence_async();
+                __syncwarp();
+                if (!careful && lane == 0) bar_arrive(&sm.v_ok[vs]);
+              }
+              uint32_t top = 0;
+#pragma unroll 8
+              for (int i = lane; i < kTile * 8 * kChunks; i += 32) {
+                const uint4 w = v[i];
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+              }
+              const bool odd = __any_sync(0xffffffffu, max(top & 0xffffu, top >> 16) >= kInf);
+              if (odd && !careful) sm.again = 1;
+              if (odd && careful) {
+                any = true;
+                for (int r = 0; r < left; r++)
+#pragma unroll
+                  for (int k = 0; k < kMine; k++) {
+                    const int ch = lane * kMine + k;
+                    uint16_t *x = reinterpret_cast<uint16_t *>(sm.kv[vs][ch / 64] + r * 128 + ((ch % 64 / 8 ^ (r & 7)) << 4)) + ch % 8;
+                    const uint32_t w = *x, at = uint32_t(j - cut) * kTile + r;
+                    if ((w & 0x7fffu) < kInf) continue;
+                    if ((w & 0x7fffu) > kInf)
+                      nan[k] = min(nan[k], at);
+                    else if (w >> 15)
+                      down[k] = min(down[k], at);
+                    else
+                      up[k] = min(up[k], at);
+                    *x = 0;
+                  }
+                fence_async();
+              }
+              __syncwarp();
+              if (careful && lane == 0) bar_arrive(&sm.v_ok[vs]);
+            }
+            if (lane == 0) bar_arrive(&sm.kv_empty[vs]);
+            stage += 2;
+            if (stage == kStages) stage = 0, kv_phase ^= 1;
+          }
+          if (!ok || n < 0) break;
+          if (any)
+#pragma unroll
+            for (int k = 0; k < kMine; k++) {
+              const int ch = lane * kMine + k;
+              sm.odd[turn].nan[ch] = uint16_t(nan[k]), sm.odd[turn].up[ch] = uint16_t(up[k]), sm.odd[turn].down[ch] = uint16_t(down[k]);
+            }
+          if (lane == 0) sm.any_odd[turn] = any;
+          __syncwarp();
+          if (careful && lane == 0) bar_arrive(&sm.odd_full[turn]);
+          if (lane == 0) bar_arrive(&sm.todo_empty[turn]);
+          turn ^= 1;
+          if (turn == 0) todo_phase ^= 1;
+        }
       }
     } else {
       // ---- softmax: a row a thread ----
@@ -550,23 +652,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
       const int t = warp >> 2, r = threadIdx.x & (kTile - 1);
       const uint32_t row = uint32_t(warp & 3) << 21;  // the warp's lanes of TMEM
       const uint32_t s_at = tmem + row + t * kTile, o_at = tmem + row + 2 * kTile + t * kTile;
-      uint32_t s_phase = 0, o_phase = 0, todo_phase = 0;
+      uint32_t s_phase = 0, o_phase = 0, todo_phase = 0, odd_phase = 0;
       int turn = 0;
       bool ok = true;
-      const int my_tok = r / a.G, my_head = r % a.G;
+      const int my_tok = r / a.G;
       const float2 sc = make_float2(a.scale_log2, a.scale_log2);
       for (;;) {
         if (!(ok = bar_wait(&sm.todo_full[turn], todo_phase, &sm.dead))) break;
         const Todo &todo = sm.todo[turn];
-        const int cnt = todo.cnt[0] < 0 ? -1 : todo.cnt[t], tok = todo.tok[t] + my_tok, slot = todo.slot;
-        const bool mine = my_tok < a.TG && tok < todo.nq;
+        const int cnt = todo.cnt[0] < 0 ? -1 : todo.cnt[t];
         // the last key seen, from the part's first
-        const int last = min(todo.nk - 1, todo.nk - todo.nq + tok) - (todo.nk - todo.keys);
-        const int64_t at = (int64_t(todo.q0) + tok) * a.Hq + todo.head + my_head;
-        __syncwarp();
-        if (lane == 0) bar_arrive(&sm.todo_empty[turn]);
-        turn ^= 1;
-        if (turn == 0) todo_phase ^= 1;
+        const int last = min(todo.nk - 1, todo.nk - todo.nq + todo.tok[t] + my_tok) - (todo.nk - todo.keys);
         if (cnt < 0) break;
         float m = -INFINITY;
         float2 l = make_float2(0.0f, 0.0f);
@@ -638,6 +734,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
           o_phase ^= 1;
           tm_after();
         }
+        // what the loop above did not need
+        const int tok = todo.tok[t] + my_tok, slot = todo.slot, last_cut = last - todo.cut * kTile;
+        const bool mine = my_tok < a.TG && tok < todo.nq;
+        const int64_t at = (int64_t(todo.q0) + tok) * a.Hq + todo.head + r % a.G;
+        bool odd = false;
+        if (todo.careful) {
+          if (!(ok = bar_wait(&sm.odd_full[turn], odd_phase >> turn & 1, &sm.dead))) break;
+          odd_phase ^= 1u << turn;
+          odd = sm.any_odd[turn];
+        }
         const bool whole = slot < 0;
         float *part = a.parts + int64_t(slot) * kRows * (D + 2);
         const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -653,6 +759,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
             } else {
 #pragma unroll
               for (int i = 0; i < 32; i++) y[i] = 0;
+            }
+            if (odd) {  // rare
+#pragma unroll
+              for (int i = 0; i < 32; i++) {
+                const Odd<D> &w = sm.odd[turn];
+                const int ch = 32 * c + i;
+                auto seen = [&](uint16_t key) { return key != 0xffff && last_cut >= int(key); };
+                if (seen(w.nan[ch])) y[i] = 0x7fffffffu;
+                if (seen(w.up[ch])) y[i] = __float_as_uint(__uint_as_float(y[i]) + INFINITY);
+                if (seen(w.down[ch])) y[i] = __float_as_uint(__uint_as_float(y[i]) - INFINITY);
+              }
             }
             if (whole) {  // to the warp's rows of 128 bytes, swizzled
 #pragma unroll
@@ -689,6 +806,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
             part[kRows * D + t * kTile + r] = m, part[kRows * (D + 1) + t * kTile + r] = sum;
           }
         }
+        __syncwarp();
+        if (lane == 0) bar_arrive(&sm.todo_empty[turn]);
+        turn ^= 1;
+        if (turn == 0) todo_phase ^= 1;
       }
     }
   }
@@ -787,6 +908,7 @@ bool make_map(CUtensorMap *map, const void *base, int d, int64_t size1, int64_t 
 template <int D, bool BF16>
 cudaError_t launch(const PromptArgs &a, unsigned grid, cudaStream_t st) {
   constexpr int kSmem = int(sizeof(Smem<D>));
+  static_assert(kSmem <= 227 * 1024, "fits in an SM");
   const cudaError_t e = cudaFuncSetAttribute(k_prompt<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   k_prompt<D, BF16><<<grid, kThreads, kSmem, st>>>(a);

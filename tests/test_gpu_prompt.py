@@ -154,6 +154,30 @@ def test_prompt_a_key_of_nan_is_not_seen_before_it():
     assert torch.equal(got.cpu()[same], want.cpu()[same])
 
 
+@pytest.mark.parametrize("d,G,dt", [(128, 4, F16), (64, 1, BF16), (80, 3, BF16)])
+def test_prompt_a_value_of_nan_is_not_seen_before_it(d, G, dt):
+    """NaN, inf and -inf in V reach the rows that see their keys, in their channels, and no others."""
+    n, ctx = 290, 150
+    q, k, v = rows(n, 2 * G, d, dt, 1), rows(n + ctx, 2, d, dt, 2), rows(n + ctx, 2, d, dt, 3)
+    args = ([0, n], [0, n + ctx], 0.1)
+    want, zw, _ = run(q.cuda(), k.cuda(), v.cuda(), *args)
+    odd = {(ctx + 100, 0, 3): math.nan, (ctx + 101, 0, 5): math.inf, (ctx + 260, 0, 5): -math.inf, (ctx + 129, 1, 0): -math.inf,
+           (ctx + n - 1, 1, d - 1): math.nan, (ctx + 280, 1, 7): math.inf, (40, 1, 1): math.nan}
+    bad, expect = v.clone(), want.cpu().double()
+    for (j, h, c), x in odd.items():
+        bad[j, h, c] = x
+        seen = torch.arange(n) >= j - ctx
+        expect[seen, h * G:(h + 1) * G, c] += x  # inf - inf is NaN
+    got, z, st = run(q.cuda(), k.cuda(), bad.cuda(), *args)
+    assert st == cg.CG_OK and torch.equal(z, zw)
+    got = got.cpu().double()
+    assert torch.equal(got.isnan(), expect.isnan()) and torch.equal(got.isinf(), expect.isinf())
+    assert torch.equal(got[got.isinf()], expect[expect.isinf()])
+    # other channels, and rows before, keep their bits; a key's channel that became 0 or odd changes rows that see it only
+    fine = expect.isfinite()
+    assert torch.equal(got[fine], want.cpu().double()[fine])
+
+
 def test_prompt_scores_far_apart():
     """Scores of hundreds whose maximum keeps growing along the keys, and falling."""
     n, d = 700, 64
