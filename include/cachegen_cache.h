@@ -25,9 +25,14 @@
  *     written through it.
  *   - 8 <= d <= 128, d a multiple of 8.  Pools and the first rows of q, k, v
  *     and out are 16-byte aligned, and their strides are multiples of 8
- *     elements.
+ *     elements (positive ones at cg_prompt_attend).  A sequence of an
+ *     attention call has at most 2^30 positions.
  *   - Lengths, offsets and ids are int32 on the device; every byte offset is
  *     computed in 64 bits.
+ *   - Scales of pages are not negative.
+ *   - The attention calls' waits for their own copies and products are
+ *     bounded (about two seconds); a wait that runs out reports
+ *     CG_ERR_TIMEOUT, with the meaning that it has in cachegen.h.
  *   - Sums, softmax statistics and scales are fp32.
  */
 #ifndef CACHEGEN_CACHE_H

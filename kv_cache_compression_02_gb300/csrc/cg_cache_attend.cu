@@ -925,6 +925,8 @@ __global__ void __launch_bounds__(kThreads, Shape<NB>::kPerSM) k_attend(const __
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
+  if (sm.dead)  // what is in flight gets a moment to land
+    for (int i = 0; i < 1000; i++) __nanosleep(1000);
   if (threadIdx.x == 0) a.notes[blockIdx.x].errors = sm.errors;
 }
 
@@ -1007,7 +1009,7 @@ bool attend_ok(const cg_cache *c, const cg_attend *t) {
     return false;
   for (int64_t s : t->q_stride)
     if (s % 8) return false;
-  return t->n_seq <= (1 << 20) && t->q_tokens <= (1 << 16) && t->Hq <= 65535 &&
+  return int64_t(t->table_stride) * c->block_tokens <= (1 << 30) && t->n_seq <= (1 << 20) && t->q_tokens <= (1 << 16) && t->Hq <= 65535 &&
          int64_t(t->q_tokens) * (t->Hq / c->H) <= (1 << 28) && int64_t(t->n_seq) * c->H * row_tiles(c, t) <= (1 << 28);
 }
 

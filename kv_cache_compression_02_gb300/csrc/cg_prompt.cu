@@ -152,6 +152,17 @@ __device__ inline int64_t cost_before(const PromptArgs &a, const Seq &s, int i) 
   return n * kIn + kTileCost * (ones + tiles_sum(n - ones, a.W, base + (ones + 1) * a.W + kTile - 1)) + (all ? key_tiles(s, s.nq) * kTileCost + kIn : 0);
 }
 
+// How many equal runs the costs of a call's items are dealt in: the CTAs that
+// there are, or, where all items cost about the same, a few fewer, so that
+// each item has a whole number of runs.  Then the items that read the same
+// keys are at the same keys at the same time, and HBM gives them once (77
+// queries of 64 heads on 32845 keys: 82 us on 144 CTAs, 87 us on 152).
+__device__ inline int64_t aligned_runs(int64_t ctas, int64_t items, int64_t total, int64_t most) {
+  if (items == 0 || items > ctas || total * 20 < items * most * 19) return ctas;
+  const int64_t whole = ctas / items * items;
+  return whole * 10 >= ctas * 9 ? whole : ctas;
+}
+
 struct Walk {
   Seq s;
   int b, h, q, n;  // item q of sequence b, head h, with n key tiles
@@ -380,7 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
   const int64_t before = cost_to - cost;
   if (blockIdx.x == 0 && bad) atomicOr(&sm.errors, kStBadArg);
   // no run is shorter than a key tile: each has one of every item that goes through it
-  const int64_t ctas = min(int64_t(gridDim.x), skip ? (total + kTileCost - 1) / kTileCost : total);
+  int64_t ctas = min(int64_t(gridDim.x), skip ? (total + kTileCost - 1) / kTileCost : total);
+  if (skip) ctas = aligned_runs(ctas, n_items, total, int64_t(most) * kTileCost + kIn);
   const int64_t lo = ctas ? total * blockIdx.x / ctas : 0, hi = ctas ? total * (blockIdx.x + 1) / ctas : 0;
   const bool busy = int64_t(blockIdx.x) < ctas;
   if (busy && lo >= before && lo < before + cost) {  // one thread's sequences hold the first cost
@@ -879,7 +891,7 @@ __global__ void __launch_bounds__(2 * D, 2048 / (2 * D)) k_prompt_join(const __g
 bool prompt_ok(const cg_prompt *p) {
   if (!p || p->n_seq < 1 || p->n_seq > 65535 || p->H < 1 || p->Hq < 1 || p->Hq > 65535 || p->Hq % p->H ||
       p->Hq / p->H > 128 || p->d < 8 || p->d > 128 || p->d % 8 || (p->dtype != CG_F16 && p->dtype != CG_BF16) ||
-      p->max_q < 0 || p->max_k < 0 || p->n_q < 0 || p->n_k < 0 || !std::isfinite(p->scale) || !(p->scale > 0.0f))
+      p->max_q < 0 || p->max_k < 0 || p->n_q < 0 || p->n_k < 0 || p->n_q > (1 << 30) || p->n_k > (1 << 30) || !std::isfinite(p->scale) || !(p->scale > 0.0f))
     return false;
   for (int i = 0; i < 2; i++)
     if (p->q_stride[i] % 8 || p->k_stride[i] % 8 || p->v_stride[i] % 8) return false;

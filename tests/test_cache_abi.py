@@ -66,7 +66,8 @@ def test_attend_refuses(lib):
         assert refused(call(cache(**kw), att())), kw
         assert cg.cg_cache_workspace_bytes(cache(**kw), att()) == 0
     for kw in (dict(n_seq=0), dict(q_tokens=0), dict(Hq=0), dict(Hq=6), dict(dtype=-1), dict(table_stride=0), dict(scale=0.0), dict(scale=-1.0), dict(scale=nan),
-               dict(scale=inf), dict(q_stride=(1024, 1024, 100)), dict(q_stride=(1, 1024, 128))):
+               dict(scale=inf), dict(q_stride=(1024, 1024, 100)), dict(q_stride=(1, 1024, 128)),
+               dict(table_stride=(1 << 26) + 1)):
         assert refused(call(cache(), att(**kw))), kw
         assert cg.cg_cache_workspace_bytes(cache(), att(**kw)) == 0
     for name in ("q", "kp", "vp", "ks", "vs", "table", "len", "out", "ws"):
@@ -88,7 +89,7 @@ def test_prompt_refuses(lib):
         return lib.cg_prompt_attend(p if p is None else p.ref, a["q"], a["k"], a["v"], a["cq"], a["ck"], a["out"], a["lse"], a["ws"], a["nb"], None)
 
     assert refused(call(None)) and lib.cg_prompt_workspace_bytes(None) == 0
-    for kw in (dict(n_seq=0), dict(Hq=0), dict(H=0), dict(Hq=6), dict(Hq=4 * 129), dict(d=4), dict(d=20), dict(d=136), dict(dtype=2), dict(n_q=-1), dict(n_k=-1),
+    for kw in (dict(n_seq=0), dict(Hq=0), dict(H=0), dict(Hq=6), dict(Hq=4 * 129), dict(d=4), dict(d=20), dict(d=136), dict(dtype=2), dict(n_q=-1), dict(n_k=-1), dict(n_k=(1 << 30) + 1),
                dict(max_q=-1), dict(max_k=-1), dict(scale=0.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(q_stride=(1023, 128)),
                dict(k_stride=(512, 4)), dict(v_stride=(2, 128))):
         assert refused(call(prompt(**kw))), kw

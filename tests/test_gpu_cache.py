@@ -89,6 +89,7 @@ CASES = {
     "group_7": ("e4m3", F16, 3, 35, 5, 128, 16, [130, 61]),
     "page_longer_than_all": ("int8", F16, 1, 8, 8, 64, 512, [250, 1]),
     "many_sequences": ("e4m3", F16, 1, 2, 1, 64, 16, [(37 * i) % 90 for i in range(300)]),
+    "more_sequences_than_are_kept": ("int8", BF16, 1, 1, 1, 16, 8, [(7 * i) % 23 for i in range(700)]),
     "long": ("int8", BF16, 1, 8, 1, 128, 64, [9000]),
     "long_drafts": ("e4m3", F16, 4, 16, 2, 128, 64, [5001, 2]),
 }

@@ -76,6 +76,8 @@ CASES = {
     "d80": (BF16, 4, 4, 80, [(65, 66)]),
     "d120": (F16, 4, 1, 120, [(33, 260)]),
     "long_context": (F16, 2, 1, 128, [(40, 6000)]),
+    "many_sequences": (BF16, 2, 1, 16, [((5 * i) % 7, (5 * i) % 7 + (3 * i) % 11) for i in range(900)]),
+    "many_queries_few_keys": (F16, 4, 2, 64, [(700, 9), (600, 300)]),
 }
 
 
