@@ -30,6 +30,7 @@
  *   - Lengths, offsets and ids are int32 on the device; every byte offset is
  *     computed in 64 bits.
  *   - Scales of pages are not negative.
+ *   - An array without entries (rows, ids of a call for none) may be NULL.
  *   - The attention calls' waits for their own copies and products are
  *     bounded (about two seconds); a wait that runs out reports
  *     CG_ERR_TIMEOUT, with the meaning that it has in cachegen.h.

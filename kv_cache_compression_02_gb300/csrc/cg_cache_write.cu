@@ -149,7 +149,8 @@ extern "C" cg_status cg_cache_write(const cg_cache *cache, const cg_rows *rows, 
                                     void *k_pool, void *v_pool, float *k_scale, float *v_scale, void *ws_dev,
                                     size_t ws_bytes, void *stream) {
   using namespace cg;
-  if (!cache8_ok(cache) || !rows || !k_dev || !v_dev || !cu_new_dev || !start_dev || !table_dev || !k_pool ||
+  // k and v may be NULL where there are no rows
+  if (!cache8_ok(cache) || !rows || ((!k_dev || !v_dev) && rows->n_rows > 0) || !cu_new_dev || !start_dev || !table_dev || !k_pool ||
       !v_pool || !k_scale || !v_scale || !ws_dev)
     return CG_ERR_INVALID_ARG;
   if (rows->n_seq < 1 || rows->n_rows < 0 || rows->max_new < 0 || rows->table_stride < 1 || rows->reserved != 0 ||

@@ -424,7 +424,7 @@ extern "C" size_t cg_pages_workspace_bytes(const cg_cache *cache, const cg_pages
 
 extern "C" cg_status cg_pages_extend(const cg_cache *cache, const cg_pages *pages, int32_t n, const int32_t *seq_dev,
                                      const int32_t *new_len_dev, void *ws_dev, size_t ws_bytes, void *stream) {
-  if (!pages_ok(cache, pages) || n < 0 || !seq_dev || !new_len_dev || !is_aligned(seq_dev, 4) ||
+  if (!pages_ok(cache, pages) || n < 0 || (n > 0 && (!seq_dev || !new_len_dev)) || !is_aligned(seq_dev, 4) ||
       !is_aligned(new_len_dev, 4) || !ws_ok(ws_dev, ws_bytes, cg_pages_workspace_bytes(cache, pages, n)))
     return CG_ERR_INVALID_ARG;
   k_extend<<<1, kPlan, 0, static_cast<cudaStream_t>(stream)>>>(page_args(cache, pages, n, seq_dev, new_len_dev, ws_dev));
@@ -434,7 +434,7 @@ extern "C" cg_status cg_pages_extend(const cg_cache *cache, const cg_pages *page
 extern "C" cg_status cg_pages_fork(const cg_cache *cache, const cg_pages *pages, void *const *pools_dev,
                                    float *const *scales_dev, int32_t n, const int32_t *parent_dev,
                                    const int32_t *child_dev, void *ws_dev, size_t ws_bytes, void *stream) {
-  if (!pages_ok(cache, pages) || !pools_ok(cache, pools_dev, scales_dev) || n < 0 || !parent_dev || !child_dev ||
+  if (!pages_ok(cache, pages) || !pools_ok(cache, pools_dev, scales_dev) || n < 0 || (n > 0 && (!parent_dev || !child_dev)) ||
       !is_aligned(parent_dev, 4) || !is_aligned(child_dev, 4) ||
       !ws_ok(ws_dev, ws_bytes, cg_pages_workspace_bytes(cache, pages, n)))
     return CG_ERR_INVALID_ARG;
@@ -447,7 +447,7 @@ extern "C" cg_status cg_pages_fork(const cg_cache *cache, const cg_pages *pages,
 
 extern "C" cg_status cg_pages_free(const cg_cache *cache, const cg_pages *pages, int32_t n, const int32_t *seq_dev,
                                    void *ws_dev, size_t ws_bytes, void *stream) {
-  if (!pages_ok(cache, pages) || n < 0 || !seq_dev || !is_aligned(seq_dev, 4) ||
+  if (!pages_ok(cache, pages) || n < 0 || (n > 0 && !seq_dev) || !is_aligned(seq_dev, 4) ||
       !ws_ok(ws_dev, ws_bytes, cg_pages_workspace_bytes(cache, pages, n)))
     return CG_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -460,7 +460,7 @@ extern "C" cg_status cg_pages_free(const cg_cache *cache, const cg_pages *pages,
 extern "C" cg_status cg_pages_copy(const cg_cache *cache, void *const *pools_dev, float *const *scales_dev, int32_t n,
                                    const int32_t *src_dev, const int32_t *dst_dev, void *ws_dev, size_t ws_bytes,
                                    void *stream) {
-  if (!cache_ok(cache) || !pools_ok(cache, pools_dev, scales_dev) || n < 0 || !src_dev || !dst_dev ||
+  if (!cache_ok(cache) || !pools_ok(cache, pools_dev, scales_dev) || n < 0 || (n > 0 && (!src_dev || !dst_dev)) ||
       !is_aligned(src_dev, 4) || !is_aligned(dst_dev, 4) || !ws_ok(ws_dev, ws_bytes, 256))
     return CG_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

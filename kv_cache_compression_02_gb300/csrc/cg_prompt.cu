@@ -951,7 +951,9 @@ extern "C" cg_status cg_prompt_attend(const cg_prompt *prompt, const void *q_dev
                                       const void *v_dev, const int32_t *cu_q_dev, const int32_t *cu_k_dev,
                                       void *out_dev, float *lse_dev, void *ws_dev, size_t ws_bytes, void *stream) {
   using namespace cg;
-  if (!prompt_ok(prompt) || !q_dev || !k_dev || !v_dev || !cu_q_dev || !cu_k_dev || !out_dev || !ws_dev)
+  // arrays without rows may be NULL
+  if (!prompt_ok(prompt) || ((!q_dev || !out_dev) && prompt->n_q > 0) || ((!k_dev || !v_dev) && prompt->n_k > 0) || !cu_q_dev || !cu_k_dev ||
+      !ws_dev)
     return CG_ERR_INVALID_ARG;
   if (!is_aligned(q_dev, 16) || !is_aligned(k_dev, 16) || !is_aligned(v_dev, 16) || !is_aligned(out_dev, 16) ||
       !is_aligned(cu_q_dev, 4) || !is_aligned(cu_k_dev, 4) || !is_aligned(lse_dev, 4) || !is_aligned(ws_dev, 256) ||

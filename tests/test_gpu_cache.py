@@ -320,6 +320,15 @@ def test_write_nonfinite_zero_and_tiny():
     assert float(s[0][int(table[0, 1])].abs().max()) == 0.0 and float(s[0][int(table[0, 2])].abs().max()) == 0.0
 
 
+def test_write_nothing():
+    pools, scales, table = make_cache("int8", 1, 16, 8, [16, 16], seed=1)
+    x = torch.empty(0, 1, 16, dtype=F16, device="cuda")
+    p, s = dev(pools), dev(scales)
+    for most in (0, 3):
+        assert run_write("int8", x, x, [0, 0, 0], [5, 16], table.cuda(), p, s, 8, max_new=most) == cg.CG_OK
+    assert torch.equal(p[0].cpu(), pools[0]) and torch.equal(p[1].cpu(), pools[1])
+
+
 def test_write_refuses_on_the_device():
     """A bad page, offsets that fall or pass the rows, a position outside the table: reported, that much left out."""
     for what in ("page", "offsets", "rows", "many", "position", "negative"):

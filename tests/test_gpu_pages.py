@@ -172,6 +172,17 @@ def test_free_twice_bad_ids_and_pages():
     assert s.free([0]) == cg.CG_ERR_CORRUPT and int(s.refs.min()) == 0
 
 
+def test_calls_for_nothing():
+    s = Setup(12, 16, [35, 20, 1], n_seqs=12, width=9)
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    for rc in (cg.cg_pages_extend(s.cache, s.pages, none, none, s.ws), cg.cg_pages_free(s.cache, s.pages, none, s.ws),
+               cg.cg_pages_fork(s.cache, s.pages, s.pool_ptrs, s.scale_ptrs, none, none, s.ws),
+               cg.cg_pages_copy(s.cache, s.pool_ptrs, s.scale_ptrs, none, none, s.ws)):
+        assert s.status(rc) == cg.CG_OK
+    s.same_book()
+    s.same_pools([])
+
+
 def test_copy():
     s = Setup(64, 7, [], n_seqs=1, width=1, L=3, H=3, d=24)
     src, dst = [5, 9, 5, 63], [1, 0, 62, 30]

@@ -191,6 +191,19 @@ def test_prompt_scores_far_apart():
         check(out, z, q, kk, v, [0, n], [0, n], 1.0)
 
 
+def test_prompt_without_keys_or_queries():
+    """Empty tensors: every row sees nothing; no rows at all is no error."""
+    q = rows(9, 4, 64, F16, 1).cuda()
+    none = torch.empty(0, 2, 64, dtype=F16, device="cuda")
+    out, z, st = run(q, none, none, [0, 4, 9], [0, 0, 0], 0.1)
+    assert st == cg.CG_OK and not out.any() and bool((z == -math.inf).all())
+    k = rows(5, 2, 64, F16, 2).cuda()
+    _, _, st = run(q[:0], k, k, [0, 0], [0, 5], 0.1)
+    assert st == cg.CG_OK
+    out, z, st = run(q, none, none, [0, 4, 9], [0, 0, 1], 0.1, max_k=1)
+    assert st == cg.CG_ERR_INVALID_ARG and not out[:4].any() and bool(out[4:].isnan().all())
+
+
 def test_prompt_refuses_on_the_device():
     """Offsets that fall or pass the rows, and a sequence longer than said, are reported; other sequences are right."""
     d = 64
