@@ -171,7 +171,8 @@ cg_status cg_prompt_attend(const cg_prompt *prompt, const void *q_dev, const voi
  * rows belongs to that sequence alone, so that it can be written.  A call
  * that takes pages takes the free ones with the lowest ids, in the order of
  * its sequences.  Where a fork or an extension finds a bad argument or too
- * few pages, it changes nothing at all. */
+ * few pages, or a fork or a compaction that has pages to move a null or
+ * misaligned pool or scale array, it changes nothing at all. */
 typedef struct {
     int32_t n_seqs;       /* rows of the table                            */
     int32_t table_stride; /* entries of a table row                       */
@@ -198,7 +199,8 @@ cg_status cg_pages_extend(const cg_cache *cache, const cg_pages *pages, int32_t 
  *   scales_dev: device array of 2*L scale arrays [n_blocks][H], or NULL
  *               (fp16 pages have none).
  * Device errors: as for cg_pages_extend, and CG_ERR_INVALID_ARG for a child
- * that has tokens or is some entry's parent, or a null or misaligned pool. */
+ * that has tokens or is some entry's parent, or, where a page is copied, a
+ * null or misaligned pool or scale array; nothing is changed then. */
 cg_status cg_pages_fork(const cg_cache *cache, const cg_pages *pages, void *const *pools_dev,
                         float *const *scales_dev, int32_t n, const int32_t *parent_dev, const int32_t *child_dev,
                         void *ws_dev, size_t ws_bytes, void *stream);
@@ -213,7 +215,7 @@ cg_status cg_pages_free(const cg_cache *cache, const cg_pages *pages, int32_t n,
 
 /* Page dst[i] becomes a copy of page src[i] in all 2*L pools and scales.  No
  * dst may be another entry's src or dst.  Device errors: CG_ERR_INVALID_ARG
- * (an id out of range, left out; a null or misaligned pool). */
+ * (an id out of range, a null or misaligned pool or scale array: left out). */
 cg_status cg_pages_copy(const cg_cache *cache, void *const *pools_dev, float *const *scales_dev, int32_t n,
                         const int32_t *src_dev, const int32_t *dst_dev, void *ws_dev, size_t ws_bytes,
                         void *stream);
@@ -224,7 +226,9 @@ cg_status cg_pages_copy(const cg_cache *cache, void *const *pools_dev, float *co
  * and table_out_dev, which may be the arrays of `pages` themselves; the
  * lengths stay.  n_live_dev (int32) gets n_live, so a server can give back
  * the pools' tail.  Device errors: CG_ERR_INVALID_ARG (a table entry >=
- * n_blocks, or of a free page: kept as it is; a null or misaligned pool). */
+ * n_blocks, or of a free page: kept as it is; where pages move, a null or
+ * misaligned pool or scale array: nothing is changed then, and no output but
+ * the status is written). */
 cg_status cg_pages_compact(const cg_cache *cache, const cg_pages *pages, void *const *pools_dev,
                            float *const *scales_dev, int32_t *refs_out_dev, int32_t *table_out_dev,
                            int32_t *n_live_dev, void *ws_dev, size_t ws_bytes, void *stream);

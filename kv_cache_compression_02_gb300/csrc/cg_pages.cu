@@ -17,9 +17,7 @@ constexpr int kMoveBytes = 32768;  // of one page, moved by one CTA at a time
 // Workspace: the status word, then what a plan tells the apply step.
 struct Book {
   uint32_t *status;   // status bits
-  int32_t *go;        // a fork's plan holds and is carried out
-  int32_t *moves;     // pages that move
-  int32_t *n_live;
+  int4 *plan;         // of a fork or a compaction: x: it holds and is carried out, y: pages that move, z: live pages
   int32_t *marks;     // [n_seqs]
   int32_t *src, *dst, *rank;  // [most]: moved pages, where they go, a number for each
 };
@@ -46,9 +44,7 @@ uint64_t book_bytes(const cg_pages *p, uint64_t most, uint8_t *at, Book *w) {
   const uint64_t marks = pad256(4 * uint64_t(p ? p->n_seqs : 0)), list = pad256(4 * most);
   if (w) {
     w->status = reinterpret_cast<uint32_t *>(at);
-    w->go = reinterpret_cast<int32_t *>(at + 4);
-    w->moves = reinterpret_cast<int32_t *>(at + 8);
-    w->n_live = reinterpret_cast<int32_t *>(at + 12);
+    w->plan = reinterpret_cast<int4 *>(at + 16);
     w->marks = reinterpret_cast<int32_t *>(at + 256);
     w->src = reinterpret_cast<int32_t *>(at + 256 + marks);
     w->dst = reinterpret_cast<int32_t *>(at + 256 + marks + list);
@@ -103,6 +99,27 @@ __device__ int find_free(const int32_t *refs, int n_blocks, int want, int32_t *l
   return min(got, want);
 }
 
+// Whether a pool or scale array is null or misaligned.  A plan looks before
+// anything is changed: what carries it out need not.  A thread's first entries
+// are loaded where the plan begins and looked at where it ends, so that their
+// latency is not added to the plan's.
+struct PoolCheck {
+  uintptr_t pool = 16, scale = 16;
+  __device__ void load(const MoveArgs &m, int i) {
+    if (i >= m.n_pools) return;
+    pool = reinterpret_cast<uintptr_t>(m.pools[i]);
+    if (m.scales) scale = reinterpret_cast<uintptr_t>(m.scales[i]);
+  }
+  __device__ bool bad(const MoveArgs &m) {  // among this thread's share of the entries
+    bool any = false;
+    for (int i = threadIdx.x;;) {
+      any |= !pool || (pool & 15) || !scale || (scale & 3);
+      if ((i += kPlan) >= m.n_pools) return any;
+      load(m, i);
+    }
+  }
+};
+
 __device__ inline int pages_of(int64_t len, int bt) { return int((len + bt - 1) / bt); }
 
 // extend: a = sequences, b = new lengths
@@ -151,9 +168,11 @@ __global__ void __launch_bounds__(kPlan) k_extend(const PageArgs g) {
 }
 
 // fork: a = parents, b = children
-__global__ void __launch_bounds__(kPlan) k_fork_plan(const PageArgs g) {
+__global__ void __launch_bounds__(kPlan) k_fork_plan(const PageArgs g, const MoveArgs m) {
   const Book &w = g.w;
   asm volatile("griddepcontrol.launch_dependents;");
+  PoolCheck pools;
+  if (g.n > 0) pools.load(m, threadIdx.x);
   for (int i = threadIdx.x; i < g.n_seqs; i += kPlan) w.marks[i] = 0;
   __syncthreads();
   bool bad = false;
@@ -184,7 +203,7 @@ __global__ void __launch_bounds__(kPlan) k_fork_plan(const PageArgs g) {
       if (part) w.src[r] = g.table[int64_t(g.a[i]) * g.stride + g.len[g.a[i]] / g.bt];
       want += total;
     }
-    bad = __syncthreads_or(bad);
+    bad = __syncthreads_or(bad || (want > 0 && pools.bad(m)));
   }
   if (!bad)  // every page of a parent must be one: a warp per pair
     for (int i = threadIdx.x >> 5; i < g.n; i += kPlan / 32) {
@@ -196,8 +215,7 @@ __global__ void __launch_bounds__(kPlan) k_fork_plan(const PageArgs g) {
   const bool room = !bad && find_free(g.refs, g.n_blocks, min(want, g.n_blocks), w.dst) == want;
   if (threadIdx.x == 0) {
     *w.status = bad ? kStBadArg : room ? 0 : kStCapacity;
-    *w.go = room;
-    *w.moves = room ? want : 0;
+    *w.plan = make_int4(room, want, 0, 0);
   }
 }
 
@@ -254,9 +272,11 @@ __global__ void __launch_bounds__(kMove) k_free(const PageArgs g) {
 
 // compact: src = pages that move, dst = where to; rank[p] is the number of
 // page p's move, as a hole (p < n_live) or a mover, or -1.  marks is not used.
-__global__ void __launch_bounds__(kPlan) k_compact_plan(const PageArgs g, int32_t *n_live_out, int32_t *moved_refs) {
+__global__ void __launch_bounds__(kPlan, 1) k_compact_plan(const PageArgs g, const MoveArgs m, int32_t *n_live_out, int32_t *moved_refs) {
   const Book &w = g.w;
   asm volatile("griddepcontrol.launch_dependents;");
+  PoolCheck pools;
+  pools.load(m, threadIdx.x);
   int mine = 0, n_live;
 #pragma unroll 8
   for (int64_t p = threadIdx.x; p < g.n_blocks; p += kPlan) mine += g.refs[p] > 0;
@@ -285,18 +305,17 @@ __global__ void __launch_bounds__(kPlan) k_compact_plan(const PageArgs g, int32_
     }
     holes += int(sum & 0xffffffff), movers += int(sum >> 32);
   }
+  const bool bad = __syncthreads_or(movers > 0 && pools.bad(m));
   if (threadIdx.x == 0) {
-    *w.status = 0;
-    *w.moves = movers;
-    *w.n_live = n_live;
-    *n_live_out = n_live;
+    *w.status = bad ? kStBadArg : 0;
+    *w.plan = make_int4(!bad, movers, n_live, 0);
+    if (!bad) *n_live_out = n_live;
   }
 }
 
 // A compaction's counts and table, by the whole grid.
-__device__ void compact_book(const PageArgs &g, int32_t *refs_out, int32_t *table_out, const int32_t *moved_refs) {
+__device__ void compact_book(const PageArgs &g, int n_live, int32_t *refs_out, int32_t *table_out, const int32_t *moved_refs) {
   const Book &w = g.w;
-  const int n_live = *w.n_live;
   const int64_t entries = int64_t(g.n_seqs) * g.stride, step = int64_t(gridDim.x) * kMove;
   for (int64_t i = int64_t(blockIdx.x) * kMove + threadIdx.x; i < g.n_blocks; i += step) {
     const int r = w.rank[i];
@@ -323,13 +342,12 @@ template <What W, typename V>
 __global__ void __launch_bounds__(kMove) k_move(const MoveArgs g, const PageArgs b, int32_t *refs_out, int32_t *table_out,
                                                 const int32_t *moved_refs) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (W == kFork) {
-    if (!*b.w.go) return;
+  const int4 plan = W == kCopy ? make_int4(1, g.n, 0, 0) : *b.w.plan;
+  if (!plan.x) return;
+  if (W == kFork)
     for (int i = blockIdx.x; i < b.n; i += gridDim.x) fork_row(b, i);
-  }
-  if (W == kCompact) compact_book(b, refs_out, table_out, moved_refs);
-  const int n = W == kCopy ? g.n : *b.w.moves;
-  const int64_t units = int64_t(g.n_pools) * n * g.parts;
+  if (W == kCompact) compact_book(b, plan.z, refs_out, table_out, moved_refs);
+  const int64_t units = int64_t(g.n_pools) * plan.y * g.parts;
   constexpr int kVecs = kMoveBytes / int(sizeof(V));
   const int64_t page_vecs = int64_t(g.page_bytes / sizeof(V));
   const int lane = threadIdx.x % g.lanes, per_cta = kMove / g.lanes;
@@ -342,7 +360,7 @@ __global__ void __launch_bounds__(kMove) k_move(const MoveArgs g, const PageArgs
       continue;
     }
     uint8_t *base = g.pools[pool];
-    if (!base || (reinterpret_cast<uintptr_t>(base) & 15)) {
+    if (W == kCopy && (!base || (reinterpret_cast<uintptr_t>(base) & 15))) {
       if (lane == 0) atomicOr(g.status, kStBadArg);
       continue;
     }
@@ -360,7 +378,7 @@ __global__ void __launch_bounds__(kMove) k_move(const MoveArgs g, const PageArgs
     for (; x < m; x += g.lanes) to[x] = from[x];
     if (part == 0 && g.scales) {
       float *sc = g.scales[pool];
-      if (!sc || (reinterpret_cast<uintptr_t>(sc) & 3)) {
+      if (W == kCopy && (!sc || (reinterpret_cast<uintptr_t>(sc) & 3))) {
         if (lane == 0) atomicOr(g.status, kStBadArg);
       } else {
         for (int h = lane; h < g.H; h += g.lanes) sc[int64_t(t) * g.H + h] = sc[int64_t(s) * g.H + h];
@@ -391,10 +409,8 @@ PageArgs page_args(const cg_cache *c, const cg_pages *p, int32_t n, const int32_
   return g;
 }
 
-// Launches k_move behind a plan (or k_clear); n: the most pages that can move.
-template <What W>
-cg_status move_pages(const cg_cache *c, void *const *pools, float *const *scales, int64_t n, const int32_t *src, const int32_t *dst,
-                     const PageArgs &g, int32_t *refs_out, int32_t *table_out, const int32_t *moved_refs, void *ws, cudaStream_t st) {
+// What a move of up to n pages needs to know.
+MoveArgs move_args(const cg_cache *c, void *const *pools, float *const *scales, const int32_t *src, const int32_t *dst, int32_t n, void *ws) {
   MoveArgs m{};
   m.pools = reinterpret_cast<uint8_t *const *>(pools);
   m.scales = scales;
@@ -402,9 +418,15 @@ cg_status move_pages(const cg_cache *c, void *const *pools, float *const *scales
   m.n_pools = 2 * c->L, m.H = c->H, m.n_blocks = c->n_blocks;
   m.parts = int((m.page_bytes + kMoveBytes - 1) / kMoveBytes);
   m.lanes = m.page_bytes <= 16384 ? 32 : kMove;
-  m.src = src, m.dst = dst, m.n = int(n);
+  m.src = src, m.dst = dst, m.n = n;
   m.status = static_cast<uint32_t *>(ws);
-  const int64_t units = n * m.n_pools * m.parts, ctas = (units * m.lanes + kMove - 1) / kMove, most = kSMs * 8;
+  return m;
+}
+
+// Launches k_move behind a plan (or k_clear).
+template <What W>
+cg_status move_pages(const MoveArgs &m, const PageArgs &g, int32_t *refs_out, int32_t *table_out, const int32_t *moved_refs, cudaStream_t st) {
+  const int64_t units = int64_t(m.n) * m.n_pools * m.parts, ctas = (units * m.lanes + kMove - 1) / kMove, most = kSMs * 8;
   const dim3 grid(unsigned(ctas < most ? ctas : most)), block(kMove);
   const cudaError_t e = m.page_bytes % 16 == 0 ? launch_early(k_move<W, uint4>, grid, block, 0, st, m, g, refs_out, table_out, moved_refs)
                                                : launch_early(k_move<W, uint2>, grid, block, 0, st, m, g, refs_out, table_out, moved_refs);
@@ -440,9 +462,10 @@ extern "C" cg_status cg_pages_fork(const cg_cache *cache, const cg_pages *pages,
     return CG_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const PageArgs g = page_args(cache, pages, n, parent_dev, child_dev, ws_dev);
-  k_fork_plan<<<1, kPlan, 0, st>>>(g);
+  const MoveArgs m = move_args(cache, pools_dev, scales_dev, g.w.src, g.w.dst, n, ws_dev);
+  k_fork_plan<<<1, kPlan, 0, st>>>(g, m);
   if (n == 0) return launched();
-  return move_pages<kFork>(cache, pools_dev, scales_dev, n, g.w.src, g.w.dst, g, nullptr, nullptr, nullptr, ws_dev, st);
+  return move_pages<kFork>(m, g, nullptr, nullptr, nullptr, st);
 }
 
 extern "C" cg_status cg_pages_free(const cg_cache *cache, const cg_pages *pages, int32_t n, const int32_t *seq_dev,
@@ -466,7 +489,7 @@ extern "C" cg_status cg_pages_copy(const cg_cache *cache, void *const *pools_dev
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   k_clear<<<1, 32, 0, st>>>(static_cast<uint32_t *>(ws_dev));
   if (n == 0) return launched();
-  return move_pages<kCopy>(cache, pools_dev, scales_dev, n, src_dev, dst_dev, PageArgs{}, nullptr, nullptr, nullptr, ws_dev, st);
+  return move_pages<kCopy>(move_args(cache, pools_dev, scales_dev, src_dev, dst_dev, n, ws_dev), PageArgs{}, nullptr, nullptr, nullptr, st);
 }
 
 extern "C" cg_status cg_pages_compact(const cg_cache *cache, const cg_pages *pages, void *const *pools_dev,
@@ -480,8 +503,8 @@ extern "C" cg_status cg_pages_compact(const cg_cache *cache, const cg_pages *pag
   const PageArgs g = page_args(cache, pages, 0, nullptr, nullptr, ws_dev);
   int32_t *moved_refs = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws_dev) +
                                                     book_bytes(pages, most_of(cache, 0), nullptr, nullptr));
-  k_compact_plan<<<1, kPlan, 0, st>>>(g, n_live_dev, moved_refs);
   // at most half of the pages move
-  return move_pages<kCompact>(cache, pools_dev, scales_dev, (int64_t(cache->n_blocks) + 1) / 2, g.w.src, g.w.dst, g, refs_out_dev, table_out_dev,
-                              moved_refs, ws_dev, st);
+  const MoveArgs m = move_args(cache, pools_dev, scales_dev, g.w.src, g.w.dst, (cache->n_blocks + 1) / 2, ws_dev);
+  k_compact_plan<<<1, kPlan, 0, st>>>(g, m, n_live_dev, moved_refs);
+  return move_pages<kCompact>(m, g, refs_out_dev, table_out_dev, moved_refs, st);
 }

@@ -232,3 +232,67 @@ def test_graph_of_a_branch_step():
         assert s.book.extend([4, 5, 6], [40, 49, 36])
         s.same_book()
         s.same_pools(m)
+
+
+BAD_POOLS = {
+    # what: (which array, the entry, its value from the right one)
+    "null_pool": ("pool_ptrs", -1, lambda x: 0),
+    "misaligned_pool": ("pool_ptrs", 1, lambda x: x + 8),
+    "null_scale": ("scale_ptrs", -1, lambda x: 0),
+    "misaligned_scale": ("scale_ptrs", 2, lambda x: x + 2),
+}
+
+
+@pytest.mark.parametrize("what", list(BAD_POOLS))
+def test_fork_and_compact_with_a_bad_pool_change_nothing(what):
+    """A null or misaligned entry among the pools or scales is found before a count, a row, a length or a page changes;
+    where no page is copied or moved the entry does not matter."""
+    name, at, wrong = BAD_POOLS[what]
+    s = Setup(40, 16, [35, 32, 1], n_seqs=8, width=5)
+    good = getattr(s, name)[at].item()
+    getattr(s, name)[at] = wrong(good)
+    assert s.fork([1, 0], [5, 6]) == cg.CG_ERR_INVALID_ARG
+    s.same_book()
+    s.same_pools([])
+    assert s.fork([1], [5]) == cg.CG_OK and s.book.fork([1], [5]) == []
+    s.same_book()
+    n_live = i32([-9])
+    rc = cg.cg_pages_compact(s.cache, s.pages, s.pool_ptrs, s.scale_ptrs, s.refs, s.table, n_live, s.ws)
+    assert s.status(rc) == cg.CG_ERR_INVALID_ARG and n_live.tolist() == [-9]
+    s.same_book()
+    s.same_pools([])
+    refs, table = torch.full_like(s.refs, -9), torch.full_like(s.table, -9)
+    rc = cg.cg_pages_compact(s.cache, s.pages, s.pool_ptrs, s.scale_ptrs, refs, table, n_live, s.ws)
+    assert s.status(rc) == cg.CG_ERR_INVALID_ARG
+    assert bool((refs == -9).all()) and bool((table == -9).all()) and n_live.tolist() == [-9]
+    # once the entry is right the same calls go through
+    getattr(s, name)[at] = good
+    assert s.fork([0], [6]) == cg.CG_OK
+    s.same_pools(s.book.fork([0], [6]))
+    rc = cg.cg_pages_compact(s.cache, s.pages, s.pool_ptrs, s.scale_ptrs, s.refs, s.table, n_live, s.ws)
+    assert s.status(rc) == cg.CG_OK
+    live, m = s.book.compact()
+    assert n_live.tolist() == [live] and m
+    s.same_book()
+    s.same_pools(m)
+    # nothing left to move
+    getattr(s, name)[at] = wrong(good)
+    rc = cg.cg_pages_compact(s.cache, s.pages, s.pool_ptrs, s.scale_ptrs, s.refs, s.table, n_live, s.ws)
+    assert s.status(rc) == cg.CG_OK and n_live.tolist() == [live]
+    s.same_book()
+    s.same_pools([])
+
+
+def test_a_bad_pool_among_more_than_a_plan_has_threads():
+    """Layer 700's V pool of 800 layers: fork and compact look at every entry."""
+    L = 800
+    s = Setup(12, 4, [6], n_seqs=4, width=3, L=L, H=1, d=8)
+    good = s.pool_ptrs[1401].item()
+    s.pool_ptrs[1401] = 0
+    assert s.fork([0], [1]) == cg.CG_ERR_INVALID_ARG
+    s.same_book()
+    s.same_pools([])
+    s.pool_ptrs[1401] = good
+    assert s.fork([0], [1]) == cg.CG_OK
+    s.same_pools(s.book.fork([0], [1]))
+    s.same_book()
