@@ -388,6 +388,8 @@ def cg_pages_workspace_bytes(cache: Cache, pages: Pages | None, n: int) -> int:
 
 
 def cg_pages_extend(cache: Cache, pages: Pages, seqs, new_len, ws, stream=None) -> int:
+    if seqs.numel() != new_len.numel():
+        return CG_ERR_INVALID_ARG
     return lib().cg_pages_extend(cache.ref, pages.ref, seqs.numel(), _ptr(seqs), _ptr(new_len), _ptr(ws), _bytes(ws),
                                  _stream(stream))
 

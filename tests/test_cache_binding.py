@@ -1,0 +1,29 @@
+"""The binding's own checks (no GPU): what must not reach the library."""
+import pytest
+import torch
+
+from kv_cache_compression_02_gb300 import cachegen as cg
+
+
+class NoLibrary:
+    def __getattr__(self, name):
+        raise AssertionError(f"{name} was called")
+
+
+@pytest.fixture
+def no_library(monkeypatch):
+    monkeypatch.setattr(cg, "lib", NoLibrary)
+
+
+def i32(n):
+    return torch.zeros(n, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("n,m", [(3, 2), (2, 3), (1, 0), (0, 1)])
+def test_lists_of_pairs_have_one_length(no_library, n, m):
+    """An extension, a fork or a copy whose two lists differ in length would read past the shorter one."""
+    cache, pages, ws = cg.Cache(1, 1, 8, 4, 8), cg.Pages(i32(8), i32(8).view(4, 2), i32(4)), i32(256)
+    ptrs = torch.zeros(2, dtype=torch.int64)
+    assert cg.cg_pages_extend(cache, pages, i32(n), i32(m), ws, 0) == cg.CG_ERR_INVALID_ARG
+    assert cg.cg_pages_fork(cache, pages, ptrs, ptrs, i32(n), i32(m), ws, 0) == cg.CG_ERR_INVALID_ARG
+    assert cg.cg_pages_copy(cache, ptrs, ptrs, i32(n), i32(m), ws, 0) == cg.CG_ERR_INVALID_ARG
