@@ -1,4 +1,5 @@
 """The binding's own checks (no GPU): what must not reach the library."""
+import numpy as np
 import pytest
 import torch
 
@@ -27,3 +28,14 @@ def test_lists_of_pairs_have_one_length(no_library, n, m):
     assert cg.cg_pages_extend(cache, pages, i32(n), i32(m), ws, 0) == cg.CG_ERR_INVALID_ARG
     assert cg.cg_pages_fork(cache, pages, ptrs, ptrs, i32(n), i32(m), ws, 0) == cg.CG_ERR_INVALID_ARG
     assert cg.cg_pages_copy(cache, ptrs, ptrs, i32(n), i32(m), ws, 0) == cg.CG_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("x", [3.7, "7", b"7", np.int64(4096), np.zeros(1, np.int64), [4096], object()])
+def test_what_is_no_address_is_not_made_one(x):
+    with pytest.raises(AttributeError):
+        cg._ptr(x)
+
+
+def test_addresses():
+    t = i32(4)
+    assert (cg._ptr(t), cg._ptr(None), cg._ptr(4096), cg._ptr(0)) == (t.data_ptr(), 0, 4096, 0)
