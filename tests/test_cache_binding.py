@@ -39,3 +39,27 @@ def test_what_is_no_address_is_not_made_one(x):
 def test_addresses():
     t = i32(4)
     assert (cg._ptr(t), cg._ptr(None), cg._ptr(4096), cg._ptr(0)) == (t.data_ptr(), 0, 4096, 0)
+
+
+def test_the_current_stream_before_cuda_is_initialised(monkeypatch):
+    """Until torch has initialised CUDA in this process, the current stream is asked for by torch's public call, which
+    initialises it or says why it cannot."""
+    class Stream:
+        cuda_stream = 0x1230
+
+    def cannot():
+        raise RuntimeError("no CUDA here")
+
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: False)
+    monkeypatch.setattr(torch.cuda, "current_stream", Stream)
+    assert cg._stream(None) == 0x1230
+    monkeypatch.setattr(torch.cuda, "current_stream", cannot)
+    with pytest.raises(RuntimeError, match="no CUDA here"):
+        cg._stream(None)
+
+
+def test_streams_by_object_and_handle():
+    class Stream:
+        cuda_stream = 0x1230
+
+    assert (cg._stream(Stream()), cg._stream(0x1240), cg._stream(0)) == (0x1230, 0x1240, None)
