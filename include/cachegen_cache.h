@@ -28,7 +28,9 @@
  *     elements (positive ones at cg_prompt_attend).  A sequence of an
  *     attention call has at most 2^30 positions.
  *   - Lengths, offsets and ids are int32 on the device; every byte offset is
- *     computed in 64 bits.
+ *     computed in 64 bits.  Every call takes H * block_tokens up to 2^30 and
+ *     n_blocks up to 2^28; cg_cache_write takes block_tokens * d up to 2^32
+ *     and H up to 32767.
  *   - Scales of pages are not negative.
  *   - An array without entries (rows, ids of a call for none) may be NULL.
  *   - The attention calls' waits for their own copies and products are

@@ -160,6 +160,8 @@ extern "C" cg_status cg_cache_write(const cg_cache *cache, const cg_rows *rows, 
       !is_aligned(k_scale, 4) || !is_aligned(v_scale, 4) || !is_aligned(cu_new_dev, 4) ||
       !is_aligned(start_dev, 4) || !is_aligned(table_dev, 4) || !is_aligned(ws_dev, 256) || ws_bytes < 256)
     return CG_ERR_INVALID_ARG;
+  // the kernel counts a page's vectors of 4 and 8 values of a head in 32 bits
+  if (int64_t(cache->block_tokens) * cache->d > int64_t(1) << 32) return CG_ERR_INVALID_ARG;
   // a run of max_new tokens touches at most this many pages
   const int64_t per_seq = (int64_t(rows->max_new) + 2 * int64_t(cache->block_tokens) - 2) / cache->block_tokens;
   const int64_t gx = per_seq * rows->n_seq;

@@ -136,3 +136,12 @@ def test_page_calls_refuse(lib):
     assert refused(copy(c, n=-1)) and refused(copy(c, ws=None)) and refused(copy(c, nb=255))
     assert refused(extend(c, ok, t=None)) and refused(compact(c, ok, nl=None)) and refused(compact(c, ok, nl=FAKE + 2))
     assert lib.cg_pages_workspace_bytes(c.ref, ref(ok), -1) == 0
+
+
+def test_write_refuses_pages_that_its_counts_cannot_hold(lib):
+    """block_tokens * d over 2^32 (a head's codes of one page over 4 GB), which cg_cache_attend and the page calls may have."""
+    for d, bt in ((128, (1 << 25) + 1), (128, 1 << 27), (128, 1 << 30), (8, (1 << 29) + 1), (72, 1 << 29)):
+        big = cache(L=1, H=1, d=d, block_tokens=bt, n_blocks=2)
+        rows = cg.Rows(1, 8, 8, cg.CG_F16, 1, d, d)
+        assert refused(write_args(lib, big, rows)), (d, bt)
+        assert cg.cg_pages_workspace_bytes(big, None, 1) > 0
