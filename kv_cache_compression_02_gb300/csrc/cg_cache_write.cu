@@ -162,13 +162,12 @@ extern "C" cg_status cg_cache_write(const cg_cache *cache, const cg_rows *rows, 
     return CG_ERR_INVALID_ARG;
   // the kernel counts a page's vectors of 4 and 8 values of a head in 32 bits
   if (int64_t(cache->block_tokens) * cache->d > int64_t(1) << 32) return CG_ERR_INVALID_ARG;
-  // a run of max_new tokens touches at most this many pages
-  const int64_t per_seq = (int64_t(rows->max_new) + 2 * int64_t(cache->block_tokens) - 2) / cache->block_tokens;
+  // a run of max_new tokens touches at most this many pages; a CTA at least looks at a sequence's offsets
+  const int64_t touched = (int64_t(rows->max_new) + 2 * int64_t(cache->block_tokens) - 2) / cache->block_tokens, per_seq = touched ? touched : 1;
   const int64_t gx = per_seq * rows->n_seq;
   if (gx > 0x7fffffff || 2 * int64_t(cache->H) > 65535) return CG_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   k_clear<<<1, 32, 0, st>>>(static_cast<uint32_t *>(ws_dev));
-  if (rows->max_new == 0) return launched();
   WriteArgs a{};
   a.src[0] = static_cast<const uint16_t *>(k_dev), a.src[1] = static_cast<const uint16_t *>(v_dev);
   a.pool[0] = static_cast<uint8_t *>(k_pool), a.pool[1] = static_cast<uint8_t *>(v_pool);

@@ -372,3 +372,21 @@ def test_write_then_attend_token_by_token():
             ref.page_write(want[0][i], want[1][i], "int8", int(table[0, t // bt]), t % bt, x[i, t:t + 1].float())
     for i in range(2):
         assert torch.equal(pools[i].cpu(), want[0][i]) and torch.equal(scales[i].cpu(), want[1][i])
+
+
+def test_write_of_no_rows_looks_at_the_offsets():
+    """With max_new = 0 a sequence that brings rows, an offset that falls or a position outside the table is reported as
+    it is with any other limit, and nothing is written."""
+    pools, scales, table = make_cache("int8", 1, 16, 8, [16, 16], seed=1)
+    x = torch.randn(4, 1, 16, generator=torch.Generator().manual_seed(2)).to(F16).cuda()
+    for bt_pages, cu, start, want in ((8, [0, 0, 0], [5, 16], cg.CG_OK), (8, [2, 2, 2], [0, 0], cg.CG_OK), (8, [0, 2, 2], [0, 0], cg.CG_ERR_INVALID_ARG),
+                                      (8, [0, 0, 4], [0, 0], cg.CG_ERR_INVALID_ARG), (8, [2, 0, 0], [0, 0], cg.CG_ERR_INVALID_ARG),
+                                      (8, [0, 0, 0], [-1, 0], cg.CG_ERR_INVALID_ARG), (8, [0, 0, 0], [0, 17], cg.CG_ERR_INVALID_ARG),
+                                      (8, [5, 5, 5], [0, 0], cg.CG_ERR_INVALID_ARG), (1, [0, 0, 1], [0, 0], cg.CG_ERR_INVALID_ARG)):
+        p, s = dev(pools), dev(scales)
+        if bt_pages == 1:  # pages of one token: a run of none touches no page at all
+            p, s = [t.reshape(-1, 1, 1, 16).contiguous() for t in p], [t.repeat_interleave(8, 0) for t in s]
+        kept = [t.clone() for t in p], [t.clone() for t in s]
+        assert run_write("int8", x, x, cu, start, table.cuda(), p, s, bt_pages, max_new=0) == want, (cu, start)
+        for a, b in zip(kept, (p, s)):
+            assert all(torch.equal(c.view(torch.uint8), e.view(torch.uint8)) for c, e in zip(a, b))
