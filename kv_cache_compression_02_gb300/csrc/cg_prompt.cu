@@ -898,6 +898,20 @@ __global__ void __launch_bounds__(2 * D, 2048 / (2 * D)) k_prompt_join(const __g
   if (c == 0 && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (top - kLift + log2f(sum)) * 0.6931471805599453f;
 }
 
+// The status of a call without queries: only its offsets are looked at.
+__global__ void __launch_bounds__(kThreads) k_prompt_none(const int32_t *cu_q, const int32_t *cu_k, int n_seq, int max_q, int max_k, int n_q, int n_k,
+                                                          uint32_t *status) {
+  PromptArgs a{};
+  a.cu_q = cu_q, a.cu_k = cu_k, a.max_q = max_q, a.max_k = max_k, a.n_q = n_q, a.n_k = n_k, a.W = 1;
+  bool bad = false;
+  for (int b = threadIdx.x; b < n_seq; b += kThreads) {
+    Seq s;
+    bad |= !load_seq(a, b, s);
+  }
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) *status = bad ? kStBadArg : 0;
+}
+
 bool prompt_ok(const cg_prompt *p) {
   if (!p || p->n_seq < 1 || p->n_seq > 65535 || p->H < 1 || p->Hq < 1 || p->Hq > 65535 || p->Hq % p->H ||
       p->Hq / p->H > 128 || p->d < 8 || p->d > 128 || p->d % 8 || (p->dtype != CG_F16 && p->dtype != CG_BF16) ||
@@ -962,7 +976,10 @@ extern "C" cg_status cg_prompt_attend(const cg_prompt *prompt, const void *q_dev
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t *ws = static_cast<uint8_t *>(ws_dev);
   const cg_prompt &p = *prompt;
-  if (p.max_q == 0 || p.n_q == 0) return cudaMemsetAsync(ws, 0, 256, st) == cudaSuccess ? CG_OK : CG_ERR_CUDA;
+  if (p.max_q == 0 || p.n_q == 0) {
+    k_prompt_none<<<1, kThreads, 0, st>>>(cu_q_dev, cu_k_dev, p.n_seq, p.max_q, p.max_k, p.n_q, p.n_k, reinterpret_cast<uint32_t *>(ws));
+    return launched();
+  }
   PromptArgs a{};
   a.cu_q = cu_q_dev, a.cu_k = cu_k_dev;
   a.out = static_cast<uint16_t *>(out_dev), a.lse = lse_dev;

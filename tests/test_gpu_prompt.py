@@ -238,3 +238,20 @@ def test_prompt_repeats_other_stream_and_graph():
         torch.cuda.synchronize()
         again, _, _ = run(q, k, v, [0, 20, 50], [0, mid, mid + 1000], 0.1)
         assert torch.equal(out, again)
+
+
+def test_prompt_of_no_queries_looks_at_the_offsets():
+    """Without query rows, or with max_q = 0, offsets are checked as they are in any other call, and nothing is written."""
+    q, k = rows(6, 4, 64, F16, 1).cuda(), rows(9, 2, 64, F16, 2).cuda()
+    bad, ok = cg.CG_ERR_INVALID_ARG, cg.CG_OK
+    for n_q, cu_q, cu_k, max_k, want in ((6, [0, 0, 0], [0, 4, 9], 5, ok), (6, [3, 3, 3], [0, 0, 0], 0, ok), (0, [0, 0, 0], [2, 4, 9], 5, ok),
+                                         (6, [0, 2, 2], [0, 4, 9], 5, bad), (6, [2, 0, 0], [0, 4, 9], 5, bad), (6, [7, 7, 7], [0, 4, 9], 5, bad),
+                                         (6, [0, 0, 0], [0, 4, 10], 6, bad), (6, [0, 0, 0], [0, 4, 9], 4, bad), (6, [0, 0, 0], [4, 0, 5], 5, bad),
+                                         (0, [0, 0, 1], [0, 4, 9], 5, bad), (0, [-1, 0, 0], [0, 4, 9], 5, bad)):
+        out, z, st = run(q[:n_q], k, k, cu_q, cu_k, 0.1, max_q=0 if n_q else 1, max_k=max_k)
+        assert st == want, (n_q, cu_q, cu_k)
+        assert bool(out.isnan().all()) and bool(z.isnan().all())
+    many = [0] * 2001  # more sequences than threads
+    assert run(q, k, k, many, many, 0.1, max_q=0)[2] == ok
+    many[-1] = 1
+    assert run(q, k, k, many, [0] * 2001, 0.1, max_q=0)[2] == bad
