@@ -60,10 +60,13 @@ constexpr int kMostCtas = Shape<1>::kGrid;
 
 // A probability is held as p = 2^(s - m + kLift), and m may lag behind the
 // true maximum by kLag, so that p < 2^15.  For the second product it is
-// multiplied by its page's V scale over the largest so far and taken as the
-// sum of two f16 values, 22 bits from kNormal up.  Smaller ones, rare but for
-// sharp distributions, go through products of their own, raised by 2^28 each
-// time, with 11 bits.
+// multiplied by its page's V scale over a power of two above the largest so far
+// and taken as the sum of two f16 values.  The second one is subnormal where the
+// weight is under 2^-2, so that the sum is off by 2^-23 of the weight or by
+// 2^-25, whichever is more (2^-36 of the largest probability, which has at least
+// 2^12, times the largest scale).  Weights under kNormal, rare but for sharp
+// distributions, go through products of their own, raised by 2^28 each time,
+// as one f16 value: off by 2^-11 of themselves, which is under 2^-25, too.
 constexpr float kLift = 12.0f, kLag = 3.0f, kNormal = 0x1p-14f;
 
 // n / d for n < 2^31 (a multiplication by the reciprocal, rounded up).
@@ -487,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, Shape<NB>::kPerSM) k_attend(const __
           w[c] = ok && ch < a.d ? *reinterpret_cast<const uint4 *>(src + ch) : make_uint4(0, 0, 0, 0);
         }
         float scale = a.scale_log2;
-        if (BF16) {  // to f16, exactly but for what is under 2^-38 of the row's largest
+        if (BF16) {  // to f16, raised to its top: off by at most 2^-39 of the row's largest
           uint32_t top = 0;
 #pragma unroll
           for (int c = 0; c < D / 32; c++) {

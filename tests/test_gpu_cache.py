@@ -390,3 +390,64 @@ def test_write_of_no_rows_looks_at_the_offsets():
         assert run_write("int8", x, x, cu, start, table.cuda(), p, s, bt_pages, max_new=0) == want, (cu, start)
         for a, b in zip(kept, (p, s)):
             assert all(torch.equal(c.view(torch.uint8), e.view(torch.uint8)) for c, e in zip(a, b))
+
+
+def cancelling(fmt, dt, T, d, bt, seed):
+    """A sequence of eight pages whose values cancel in pairs, so that outputs are small against the weights they are made
+    of and show how exactly the weights went into the second product.  Page i alone has values in the i-th eighth of
+    the channels; every other page has a V scale 2^-8, 2^-16, 2^-24 and 2^-30 of its neighbour's.  A query row has two
+    channels, powers of two, so that its products and their sums are exact."""
+    g = torch.Generator().manual_seed(seed)
+    H, G, n = 2, 4, 8 * bt
+    k = (torch.randn(8, H, bt, d, generator=g) * 40).clamp(-100, 100)
+    k = ref.codes(k, fmt).float()
+    k[:, :, 1::2, :d // 2] = k[:, :, ::2, :d // 2]
+    v = torch.zeros(8, H, bt, d)
+    for i in range(8):
+        c = slice(i * (d // 8), (i + 1) * (d // 8))
+        v[i, :, ::2, c] = ref.codes((torch.randn(H, bt // 2, d // 8, generator=g) * 40).clamp(-100, 100), fmt).float()
+        v[i, :, 1::2, c] = -v[i, :, ::2, c]
+    scales = [torch.full((8, H), 2.0 ** -5), torch.ones(8, H)]
+    scales[1][1::2] = 2.0 ** -torch.tensor([8.0, 16.0, 24.0, 30.0])[:, None]
+    q = torch.zeros(1, T, G * H, d)
+    for t in range(T):
+        for h in range(G * H):
+            q[0, t, h, (3 * h + t) % (d // 2)], q[0, t, h, d // 2 + (5 * h + t) % (d // 2)] = 1.0, 2.0 ** -6
+    return q.to(dt), [ref.codes(x, fmt) for x in (k, v)], scales, torch.arange(8, dtype=torch.int32)[None], n
+
+
+def weight_tolerance(q, k, v_codes, v_scale, last, dtype):
+    """out and its tolerance where weights w_j = exp(s_j - lse) * (V scale of j) are off by at most 2^-23 of themselves or
+    2^-36 of the largest probability times the largest scale, whichever is more, and by 2^-11 of themselves at most.
+    Products and their sums are exact; a score is rounded four times; eight lanes share a row's sum; exp2, log2, the
+    joins and the final product take 2^-20 together; the second product sums the n / 8 positions of a page sixteen at a
+    time, each off by 2^-24 of the largest."""
+    n = k.shape[0]
+    s = q.double() @ k.double().T
+    s.masked_fill_(torch.arange(n) > last[:, None], -math.inf)
+    p = torch.softmax(s, 1)
+    w = p * v_scale.double()
+    most = p.max(1, keepdim=True).values * v_scale.max()
+    off = torch.minimum(2.0 ** -11 * w, torch.maximum(2.0 ** -23 * w, 2.0 ** -36 * most))
+    ds = 4 * 2.0 ** -24 * float(s[s.isfinite()].abs().max()) + (n / 8 + 8) * 2.0 ** -24 + 2.0 ** -20
+    out, raw = w @ v_codes.double(), (off + (2 * ds + (n / 8 + 16) * 2.0 ** -24) * w) @ v_codes.double().abs()
+    half = torch.finfo(dtype).eps / 2
+    return out, raw + half * (out.abs() + raw) + torch.finfo(dtype).smallest_normal * half, w
+
+
+@pytest.mark.parametrize("fmt,dt,T,d,bt", [("int8", BF16, 1, 128, 16), ("e4m3", BF16, 1, 64, 16), ("int8", BF16, 3, 128, 32), ("e4m3", BF16, 2, 80, 24),
+                                           ("int8", F16, 1, 64, 48)])
+def test_attend_weights_carry_their_low_part(fmt, dt, T, d, bt):
+    """Values that cancel: weights of 11 bits would be off by many times the tolerance (which is checked, too)."""
+    q, pools, scales, table, n = cancelling(fmt, dt, T, d, bt, seed=d + bt)
+    out, _, st = run_attend(fmt, q.cuda(), dev(pools), dev(scales), table.cuda(), torch.tensor([n], dtype=torch.int32).cuda(), 2, bt, 1.0)
+    assert st == cg.CG_OK
+    for h in range(2):
+        k = torch.cat([pools[0][i, h].double() * float(scales[0][i, h]) for i in range(8)])
+        v = torch.cat([pools[1][i, h].double() for i in range(8)])
+        rows = q[0, :, 4 * h:4 * h + 4].reshape(4 * T, d)
+        last = (torch.arange(T) + n - T).repeat_interleave(4)
+        want, tol, w = weight_tolerance(rows, k, v, scales[1][:, h].repeat_interleave(bt), last, dt)
+        ref.assert_close(out[0, :, 4 * h:4 * h + 4].reshape(4 * T, d), want, tol, f"head {h}")
+        coarse = torch.ldexp((torch.frexp(w)[0] * 2 ** 11).round(), torch.frexp(w)[1] - 11)  # weights of 11 bits
+        assert float((((coarse - w) @ v).abs() / tol).max()) > 4
