@@ -31,7 +31,10 @@
  *     computed in 64 bits.  Every call takes H * block_tokens up to 2^30 and
  *     n_blocks up to 2^28; cg_cache_write takes block_tokens * d up to 2^32
  *     and H up to 32767.
- *   - Scales of pages are not negative.
+ *   - Scales of pages are not negative; that of a page whose rows
+ *     cg_cache_write adds to is 0 or at least 2^-100, as it writes them.
+ *     In the attention calls a value of V times the number of positions stays
+ *     under 2^112: sums of weights up to 2^15 are taken in fp32.
  *   - An array without entries (rows, ids of a call for none) may be NULL.
  *   - The attention calls' waits for their own copies and products are
  *     bounded (about two seconds); a wait that runs out reports
