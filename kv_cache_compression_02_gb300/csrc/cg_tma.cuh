@@ -85,10 +85,6 @@ __device__ inline void tma_3d(uint32_t dst, const CUtensorMap *map, uint64_t *ba
                : "memory");
 }
 
-__device__ inline void tma_prefetch_map(const CUtensorMap *map) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
-}
-
 // Orders this thread's accesses of shared memory before later ones of the async proxy.
 __device__ inline void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
