@@ -296,3 +296,33 @@ def test_a_bad_pool_among_more_than_a_plan_has_threads():
     assert s.fork([0], [1]) == cg.CG_OK
     s.same_pools(s.book.fork([0], [1]))
     s.same_book()
+
+
+def test_extend_takes_the_last_of_many_pages_and_not_one_more():
+    """9000 pages, more than two rounds of the search for free ones: refused by one page with nothing changed, then to
+    the last page, then refused once more."""
+    n, width = 9000, 6
+    lens = [16 * (1 + i % 3) for i in range(2000)]  # whole pages, strewn over the pool
+    s = Setup(n, 16, lens, n_seqs=2500, width=width)
+    s.ws = cg.empty_u8(cg.cg_pages_workspace_bytes(s.cache, s.pages, 2500))
+    left = len(s.book.free_pages())
+    assert left == n - sum(-(-m // 16) for m in lens)
+    grow, take = [], 0
+    for q in range(2499, -1, -1):
+        more = min(width - s.book.pages(s.book.lens[q]), left - take)
+        grow.append((q, s.book.lens[q] + 16 * more))
+        take += more
+        if take == left:
+            break
+    assert take == left > 4096
+    spare = next(q for q in range(2500) if q not in dict(grow) and s.book.pages(s.book.lens[q]) < width)
+    seqs, new = [q for q, _ in grow], [m for _, m in grow]
+    over = seqs + [spare], new + [s.book.lens[spare] + 1]
+    assert s.extend(*over) == cg.CG_ERR_CAPACITY and not s.book.extend(*over)
+    s.same_book()
+    assert s.extend(seqs, new) == cg.CG_OK and s.book.extend(seqs, new)
+    assert s.book.free_pages() == [] and s.book.refs[n - 1] == 1
+    s.same_book()
+    assert s.extend([spare], [s.book.lens[spare] + 1]) == cg.CG_ERR_CAPACITY
+    s.same_book()
+    s.same_pools([])
