@@ -36,9 +36,10 @@
 // to the workspace as maximum, sum and output, and a second kernel joins the
 // parts in their order.
 //
-// Measured: 8192 tokens, 32 heads on 8, d = 128: 368 us, 1.5 PFLOP/s (the
-// products are busy for two thirds of the time; what is left is a tile's chain
-// of maximum, exponentials and hand-over).  77 queries of 64 heads on 32845
+// Measured, ten calls in a graph: 8192 tokens, 32 heads on 8, d = 128: 369 us,
+// 1.5 PFLOP/s (the products are busy for two thirds of the time; what is left is
+// a tile's chain of maximum, exponentials and hand-over; called back to back for
+// longer, under the power limit, 398 us or 1.38 PFLOP/s).  77 queries of 64 heads on 32845
 // keys: 82 us.  Rows of up to 64 channels have operands of 64 (8192 tokens, d =
 // 64: 278 us; padded to 128 they take 360).
 #include "cg_cache.cuh"
