@@ -127,7 +127,7 @@ size_t cg_cache_workspace_bytes(const cg_cache *cache, const cg_attend *attend);
  * they hold.  The weight of a position in the second product, its probability
  * times its page's V scale, is off by at most 2^-23 of itself or 2^-36 of the
  * largest probability times the largest V scale, whichever is more, and by
- * 2^-11 of itself at most (one under 2^-138 of that may count as 0).
+ * 2^-11 of itself at most (one under 2^-122 of that may count as 0).
  * A call on the same inputs gives the same bits every time; the bits of a
  * sequence may depend on the lengths of the others.
  *   out_dev: [n_seq][T][Hq][d], contiguous;  lse_dev: fp32 [n_seq][T][Hq], or NULL;  len_dev: int32 [n_seq].
