@@ -171,6 +171,24 @@ cg_status cg_prompt_attend(const cg_prompt *prompt, const void *q_dev, const voi
                            const int32_t *cu_q_dev, const int32_t *cu_k_dev, void *out_dev, float *lse_dev,
                            void *ws_dev, size_t ws_bytes, void *stream);
 
+/* ---- attention to states of another length --------------------------------- */
+/* Every query of sequence b sees keys k_begin[b] .. k_begin[b]+k_len[b]-1 and
+ * no others: the states of an encoder, or a loaded context without the rows
+ * that go on from it (out and lse of such a part can be joined with another
+ * part's).  Sequences may share keys.  prompt as at cg_prompt_attend (n_k: rows
+ * that k and v have; max_k: no k_len is more), with its workspace, its formulas
+ * and its rounding of the probabilities; a row without keys gives out 0, lse
+ * -inf.  Keys that a sequence does not see do not matter, whatever they hold.
+ *   cu_q_dev:               int32 [n_seq + 1], as at cg_prompt_attend;
+ *   k_begin_dev, k_len_dev: int32 [n_seq];
+ *   out_dev, lse_dev:       as at cg_prompt_attend.
+ * Device errors: CG_ERR_INVALID_ARG (offsets that fall, pass n_q or bring more
+ * than max_q queries; a k_begin or k_len that is negative, a k_len over max_k,
+ * keys past n_k: that sequence is left out). */
+cg_status cg_cross_attend(const cg_prompt *prompt, const void *q_dev, const void *k_dev, const void *v_dev,
+                          const int32_t *cu_q_dev, const int32_t *k_begin_dev, const int32_t *k_len_dev, void *out_dev,
+                          float *lse_dev, void *ws_dev, size_t ws_bytes, void *stream);
+
 /* ---- pages that sequences share --------------------------------------------
  * refs[p] counts the table rows that hold page p; 0 is a free page.  Of the
  * first ceil(len / block_tokens) entries of a table row, each holds a page;
@@ -239,6 +257,43 @@ cg_status cg_pages_copy(const cg_cache *cache, void *const *pools_dev, float *co
 cg_status cg_pages_compact(const cg_cache *cache, const cg_pages *pages, void *const *pools_dev,
                            float *const *scales_dev, int32_t *refs_out_dev, int32_t *table_out_dev,
                            int32_t *n_live_dev, void *ws_dev, size_t ws_bytes, void *stream);
+
+/* The rows of a step.  Sequence s of the table brings the last new[s] tokens of
+ * its len[s] (cg_pages_extend has given it their pages); their rows lie one
+ * after the other, sequences in the table's order:
+ *   cu_new_dev: int32 [n_seqs + 1], offsets of each sequence's rows;
+ *   start_dev:  int32 [n_seqs], the position of its first new token, len - new;
+ *   seq_dev, pos_dev, slot_dev: of each of n_rows rows the sequence, the
+ *     position and the place, page * block_tokens + position % block_tokens
+ *     (int32, int32, int64 [n_rows]; -1 for the rows behind the last one).
+ *     Any of them may be NULL.
+ * cu_new_dev and start_dev are what cg_cache_write takes, cu_new_dev is also
+ * the cu_q of cg_prompt_attend and cg_cross_attend; the places are for rows
+ * that go elsewhere (pages in fp16).
+ *   ws_dev: 256 bytes, 256-byte aligned.
+ * Device errors: CG_ERR_INVALID_ARG (a length that is negative or passes the
+ * table, a new[s] that is negative or more than the length: that sequence
+ * brings nothing and its start is 0; a bad page: the row's place is -1);
+ * CG_ERR_CAPACITY (more than n_rows rows: offsets stop at n_rows). */
+cg_status cg_pages_slots(const cg_cache *cache, const cg_pages *pages, int32_t n_rows, const int32_t *new_dev,
+                         int32_t *cu_new_dev, int32_t *start_dev, int32_t *seq_dev, int32_t *pos_dev, int64_t *slot_dev,
+                         void *ws_dev, size_t ws_bytes, void *stream);
+
+/* Which sequences share a prefix.  The sequences of the table that have at least
+ * min_pages whole pages, of which the min_pages-th is the same page, make a
+ * group where they are two or more (after forks and compactions they share
+ * everything before it, too).  Groups are in the order of their lowest
+ * sequences, members in ascending order:
+ *   cu_group_dev: int32 [n_seqs / 2 + 1], offsets of the groups' members;
+ *   member_dev:   int32 [n_seqs], sequences, -1 behind the last member;
+ *   shared_dev:   int32 [n_seqs / 2], whole pages that a group's rows begin with
+ *                 alike, 0 behind the last group (whose offsets end alike).
+ *   ws_dev: cg_pages_workspace_bytes(cache, pages, n_seqs).
+ * Device errors: CG_ERR_INVALID_ARG (a length that is negative or passes the
+ * table, or a bad page at min_pages - 1: that sequence is in no group; a bad
+ * page elsewhere in a group's rows is alike to none). */
+cg_status cg_pages_groups(const cg_cache *cache, const cg_pages *pages, int32_t min_pages, int32_t *cu_group_dev,
+                          int32_t *member_dev, int32_t *shared_dev, void *ws_dev, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -105,12 +105,15 @@ def lib() -> ctypes.CDLL:
             "cg_cache_attend": (ctypes.c_int, [P] * 12 + [S, P]),
             "cg_prompt_workspace_bytes": (S, [P]),
             "cg_prompt_attend": (ctypes.c_int, [P] * 9 + [S, P]),
+            "cg_cross_attend": (ctypes.c_int, [P] * 10 + [S, P]),
             "cg_pages_workspace_bytes": (S, [P, P, ctypes.c_int32]),
             "cg_pages_extend": (ctypes.c_int, [P, P, ctypes.c_int32, P, P, P, S, P]),
             "cg_pages_fork": (ctypes.c_int, [P, P, P, P, ctypes.c_int32, P, P, P, S, P]),
             "cg_pages_free": (ctypes.c_int, [P, P, ctypes.c_int32, P, P, S, P]),
             "cg_pages_copy": (ctypes.c_int, [P, P, P, ctypes.c_int32, P, P, P, S, P]),
             "cg_pages_compact": (ctypes.c_int, [P, P, P, P, P, P, P, P, S, P]),
+            "cg_pages_slots": (ctypes.c_int, [P, P, ctypes.c_int32, P, P, P, P, P, P, P, S, P]),
+            "cg_pages_groups": (ctypes.c_int, [P, P, ctypes.c_int32, P, P, P, P, S, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -390,6 +393,12 @@ def cg_prompt_attend(prompt: Prompt, q, k, v, cu_q, cu_k, out, lse, ws, stream=N
                                   _ptr(ws), _bytes(ws), _stream(stream))
 
 
+def cg_cross_attend(prompt: Prompt, q, k, v, cu_q, k_begin, k_len, out, lse, ws, stream=None) -> int:
+    """lse may be None."""
+    return lib().cg_cross_attend(prompt.ref, _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(k_begin), _ptr(k_len), _ptr(out), _ptr(lse), _ptr(ws),
+                                 _bytes(ws), _stream(stream))
+
+
 def cg_pages_workspace_bytes(cache: Cache, pages: Pages | None, n: int) -> int:
     return lib().cg_pages_workspace_bytes(cache.ref, None if pages is None else pages.ref, int(n))
 
@@ -423,6 +432,16 @@ def cg_pages_copy(cache: Cache, pools, scales, src, dst, ws, stream=None) -> int
 def cg_pages_compact(cache: Cache, pages: Pages, pools, scales, refs_out, table_out, n_live, ws, stream=None) -> int:
     return lib().cg_pages_compact(cache.ref, pages.ref, _ptr(pools), _ptr(scales), _ptr(refs_out), _ptr(table_out),
                                   _ptr(n_live), _ptr(ws), _bytes(ws), _stream(stream))
+
+
+def cg_pages_slots(cache: Cache, pages: Pages, n_rows: int, new, cu_new, start, seq, pos, slot, ws, stream=None) -> int:
+    """seq, pos and slot (int32, int32, int64) may be None."""
+    return lib().cg_pages_slots(cache.ref, pages.ref, n_rows, _ptr(new), _ptr(cu_new), _ptr(start), _ptr(seq), _ptr(pos), _ptr(slot), _ptr(ws),
+                                _bytes(ws), _stream(stream))
+
+
+def cg_pages_groups(cache: Cache, pages: Pages, min_pages: int, cu_group, member, shared, ws, stream=None) -> int:
+    return lib().cg_pages_groups(cache.ref, pages.ref, min_pages, _ptr(cu_group), _ptr(member), _ptr(shared), _ptr(ws), _bytes(ws), _stream(stream))
 
 
 def cg_read_status(ws) -> int:

@@ -1,5 +1,5 @@
 // cg_pages.cu -- the bookkeeping of pages that sequences share: extend, fork,
-// free, copy and compact.
+// free, copy and compact; the rows of a step, and who shares a prefix.
 //
 // A fork or a compaction has a plan, made by one CTA (a scan over the reference
 // counts, in order, so that no order of atomics can change the result), and a
@@ -334,6 +334,176 @@ __device__ void compact_book(const PageArgs &g, int n_live, int32_t *refs_out, i
   }
 }
 
+// ---- the rows of a step -------------------------------------------------------
+struct SlotArgs {
+  const int32_t *table, *len, *fresh;  // fresh: the tokens that each sequence brings
+  int32_t *cu, *start, *seq, *pos;
+  int64_t *slot;
+  uint32_t *status;
+  int n_seqs, stride, n_blocks, bt, n_rows;
+};
+
+// Offsets and first positions, by one CTA.
+__global__ void __launch_bounds__(kPlan) k_slots_plan(const SlotArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  bool bad = false;
+  int64_t sum = 0;
+  for (int64_t base = 0; base < a.n_seqs; base += kPlan) {
+    const int64_t s = base + threadIdx.x;
+    int64_t n = 0;
+    if (s < a.n_seqs) {
+      const int len = a.len[s];
+      n = a.fresh[s];
+      const bool ok = len >= 0 && len <= int64_t(a.stride) * a.bt && n >= 0 && n <= len;
+      if (!ok) bad = true, n = 0;
+      a.start[s] = ok ? int32_t(len - n) : 0;
+    }
+    int64_t total;
+    const int64_t at = sum + scan(n, &total);
+    if (s < a.n_seqs) a.cu[s] = int32_t(min(at, int64_t(a.n_rows)));
+    sum += total;
+  }
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) {
+    a.cu[a.n_seqs] = int32_t(min(sum, int64_t(a.n_rows)));
+    *a.status = (bad ? kStBadArg : 0) | (sum > a.n_rows ? kStCapacity : 0);
+  }
+}
+
+// A row a thread.
+__global__ void __launch_bounds__(kMove) k_slots_rows(const SlotArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t r = int64_t(blockIdx.x) * kMove + threadIdx.x;
+  if (r >= a.n_rows) return;
+  int s = -1, pos = -1;
+  int64_t slot = -1;
+  if (r < a.cu[a.n_seqs]) {
+    int lo = 0, hi = a.n_seqs;  // cu[lo] <= r < cu[hi]
+    while (hi - lo > 1) {
+      const int mid = lo + (hi - lo) / 2;
+      if (a.cu[mid] <= r)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    s = lo;
+    pos = a.start[s] + int(r - a.cu[s]);
+    const int page = a.table[int64_t(s) * a.stride + pos / a.bt];
+    if (uint32_t(page) < uint32_t(a.n_blocks))
+      slot = int64_t(page) * a.bt + pos % a.bt;
+    else
+      atomicOr(a.status, kStBadArg);
+  }
+  if (a.seq) a.seq[r] = s;
+  if (a.pos) a.pos[r] = pos;
+  if (a.slot) a.slot[r] = slot;
+}
+
+// ---- who shares a prefix ---------------------------------------------------------
+struct GroupArgs {
+  const int32_t *table, *len;
+  int32_t *cu, *member, *shared;
+  int32_t *first;   // [n_blocks]: of a page, the first sequence that has it at min_pages - 1
+  int32_t *lead;    // [n_seqs]: a sequence's first[], or -1 where it is in no group
+  int32_t *number;  // [n_seqs]: a leading sequence's group
+  int32_t *count;   // [n_seqs]: its members
+  uint32_t *status;
+  int n_seqs, stride, n_blocks, bt, min_pages;
+};
+
+// Whole pages of a sequence.
+__device__ inline int whole_pages(const GroupArgs &a, int64_t s, bool *bad) {
+  const int len = a.len[s];
+  if (len < 0 || len > int64_t(a.stride) * a.bt) {
+    *bad = true;
+    return 0;
+  }
+  return len / a.bt;
+}
+
+// The groups and their sizes, by one CTA: the lowest sequence of a page leads
+// its group, and groups are counted in the order of their leaders.
+__global__ void __launch_bounds__(kPlan) k_groups_plan(const GroupArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  bool bad = false;
+  for (int64_t s = threadIdx.x; s < a.n_seqs; s += kPlan) {
+    int page = -1;
+    if (whole_pages(a, s, &bad) >= a.min_pages) {
+      page = a.table[s * a.stride + a.min_pages - 1];
+      if (uint32_t(page) >= uint32_t(a.n_blocks)) bad = true, page = -1;
+    }
+    a.lead[s] = page;
+    a.count[s] = 0;
+    if (page >= 0) a.first[page] = 0x7fffffff;
+  }
+  __syncthreads();
+  for (int64_t s = threadIdx.x; s < a.n_seqs; s += kPlan)
+    if (a.lead[s] >= 0) atomicMin(&a.first[a.lead[s]], int(s));
+  __syncthreads();
+  for (int64_t s = threadIdx.x; s < a.n_seqs; s += kPlan)
+    if (a.lead[s] >= 0) {
+      const int lead = __ldcg(&a.first[a.lead[s]]);
+      a.lead[s] = lead;
+      atomicAdd(&a.count[lead], 1);
+    }
+  __syncthreads();
+  int64_t sums = 0;  // members below, groups above
+  for (int64_t base = 0; base < a.n_seqs; base += kPlan) {
+    const int64_t s = base + threadIdx.x;
+    int64_t mine = 0;
+    if (s < a.n_seqs && a.lead[s] == s && __ldcg(&a.count[s]) > 1) mine = int64_t(1) << 32 | __ldcg(&a.count[s]);
+    int64_t total;
+    const int64_t at = sums + scan(mine, &total);
+    if (mine) {
+      const int g = int(at >> 32);
+      a.number[s] = g;
+      a.cu[g] = int32_t(at);
+      a.shared[g] = a.len[s] / a.bt;
+    } else if (s < a.n_seqs) {
+      a.number[s] = -1;
+    }
+    sums += total;
+  }
+  const int members = int32_t(sums), groups = int(sums >> 32);
+  for (int64_t s = threadIdx.x; s < a.n_seqs; s += kPlan) {
+    if (s >= members) a.member[s] = -1;
+    if (s >= groups && s <= a.n_seqs / 2) a.cu[s] = members;
+    if (s >= groups && s < a.n_seqs / 2) a.shared[s] = 0;
+  }
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) *a.status = bad ? kStBadArg : 0;
+}
+
+// A sequence's place in its group, and how much of its leader's row it has.
+__global__ void __launch_bounds__(kMove) k_groups_members(const GroupArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int s = blockIdx.x, lead = a.lead[s], g = lead >= 0 ? a.number[lead] : -1;
+  if (g < 0) return;
+  int before = 0;
+  for (int i = threadIdx.x; i < s; i += kMove) before += a.lead[i] == lead;
+  const int most = min(a.len[s], a.len[lead]) / a.bt;
+  const int32_t *x = a.table + int64_t(s) * a.stride, *y = a.table + int64_t(lead) * a.stride;
+  int common = most;
+  bool bad = false;
+#pragma unroll 8
+  for (int j = threadIdx.x; j < most; j += kMove) {
+    const int p = x[j], q = y[j];
+    bad |= uint32_t(p) >= uint32_t(a.n_blocks);
+    if (p != q || uint32_t(p) >= uint32_t(a.n_blocks)) common = min(common, j);
+  }
+  __shared__ int s_before, s_common;
+  if (threadIdx.x == 0) s_before = 0, s_common = most;
+  __syncthreads();
+  before = __reduce_add_sync(0xffffffffu, before), common = __reduce_min_sync(0xffffffffu, common);
+  if ((threadIdx.x & 31) == 0) atomicAdd(&s_before, before), atomicMin(&s_common, common);
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) {
+    a.member[a.cu[g] + s_before] = s;
+    atomicMin(&a.shared[g], s_common);
+    if (bad) atomicOr(a.status, kStBadArg);
+  }
+}
+
 enum What { kCopy, kFork, kCompact };
 
 // Pages src[i] -> dst[i] of every pool, with their scales, and the rest of
@@ -510,4 +680,42 @@ extern "C" cg_status cg_pages_compact(const cg_cache *cache, const cg_pages *pag
   const MoveArgs m = move_args(cache, pools_dev, scales_dev, g.w.src, g.w.dst, (cache->n_blocks + 1) / 2, ws_dev);
   k_compact_plan<<<1, kPlan, 0, st>>>(g, m, n_live_dev, moved_refs);
   return move_pages<kCompact>(m, g, refs_out_dev, table_out_dev, moved_refs, st);
+}
+
+extern "C" cg_status cg_pages_slots(const cg_cache *cache, const cg_pages *pages, int32_t n_rows, const int32_t *new_dev,
+                                    int32_t *cu_new_dev, int32_t *start_dev, int32_t *seq_dev, int32_t *pos_dev,
+                                    int64_t *slot_dev, void *ws_dev, size_t ws_bytes, void *stream) {
+  if (!pages_ok(cache, pages) || n_rows < 0 || !new_dev || !cu_new_dev || !start_dev || !is_aligned(new_dev, 4) || !is_aligned(cu_new_dev, 4) ||
+      !is_aligned(start_dev, 4) || !is_aligned(seq_dev, 4) || !is_aligned(pos_dev, 4) || !is_aligned(slot_dev, 8) || !ws_ok(ws_dev, ws_bytes, 256))
+    return CG_ERR_INVALID_ARG;
+  SlotArgs a{};
+  a.table = pages->table_dev, a.len = pages->len_dev, a.fresh = new_dev;
+  a.cu = cu_new_dev, a.start = start_dev, a.seq = seq_dev, a.pos = pos_dev, a.slot = slot_dev;
+  a.status = static_cast<uint32_t *>(ws_dev);
+  a.n_seqs = pages->n_seqs, a.stride = pages->table_stride, a.n_blocks = cache->n_blocks, a.bt = cache->block_tokens, a.n_rows = n_rows;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  k_slots_plan<<<1, kPlan, 0, st>>>(a);
+  if (n_rows == 0 || (!seq_dev && !pos_dev && !slot_dev)) return launched();
+  const cudaError_t e = launch_early(k_slots_rows, dim3(unsigned((int64_t(n_rows) + kMove - 1) / kMove)), dim3(kMove), 0, st, a);
+  return e == cudaSuccess ? launched() : CG_ERR_CUDA;
+}
+
+extern "C" cg_status cg_pages_groups(const cg_cache *cache, const cg_pages *pages, int32_t min_pages, int32_t *cu_group_dev,
+                                     int32_t *member_dev, int32_t *shared_dev, void *ws_dev, size_t ws_bytes, void *stream) {
+  // (a table of one sequence has no group, and no entry of shared)
+  if (!pages_ok(cache, pages) || min_pages < 1 || !cu_group_dev || !member_dev || (!shared_dev && pages->n_seqs > 1) ||
+      !is_aligned(cu_group_dev, 4) || !is_aligned(member_dev, 4) || !is_aligned(shared_dev, 4) ||
+      !ws_ok(ws_dev, ws_bytes, cg_pages_workspace_bytes(cache, pages, pages->n_seqs)))
+    return CG_ERR_INVALID_ARG;
+  const PageArgs b = page_args(cache, pages, pages->n_seqs, nullptr, nullptr, ws_dev);
+  GroupArgs a{};
+  a.table = pages->table_dev, a.len = pages->len_dev;
+  a.cu = cu_group_dev, a.member = member_dev, a.shared = shared_dev;
+  a.first = b.w.src, a.lead = b.w.dst, a.number = b.w.rank, a.count = b.w.marks;
+  a.status = b.w.status;
+  a.n_seqs = b.n_seqs, a.stride = b.stride, a.n_blocks = b.n_blocks, a.bt = b.bt, a.min_pages = min_pages;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  k_groups_plan<<<1, kPlan, 0, st>>>(a);
+  const cudaError_t e = launch_early(k_groups_members, dim3(unsigned(a.n_seqs)), dim3(kMove), 0, st, a);
+  return e == cudaSuccess ? launched() : CG_ERR_CUDA;
 }

@@ -70,7 +70,7 @@ struct Note {
 
 struct PromptArgs {
   CUtensorMap q_map, k_map, v_map;
-  const int32_t *cu_q, *cu_k;
+  const int32_t *cu_q, *cu_k, *k_len;  // CROSS: cu_k is where each sequence's keys begin, k_len how many they are
   uint16_t *out;
   float *lse;
   uint32_t *status;
@@ -139,10 +139,12 @@ struct Seq {
   int q0, nq, k0, nk, items;
 };
 
+template <bool CROSS>
 __device__ inline bool load_seq(const PromptArgs &a, int b, Seq &s) {
   s.q0 = a.cu_q[b], s.k0 = a.cu_k[b];
-  const int q1 = a.cu_q[b + 1], k1 = a.cu_k[b + 1];
-  s.nq = q1 - s.q0, s.nk = k1 - s.k0;
+  const int q1 = a.cu_q[b + 1];
+  const int64_t k1 = CROSS ? int64_t(s.k0) + a.k_len[b] : a.cu_k[b + 1];
+  s.nq = q1 - s.q0, s.nk = int(k1 - s.k0);
   const bool ok = s.q0 >= 0 && q1 >= s.q0 && q1 <= a.n_q && s.nq <= a.max_q && s.k0 >= 0 && k1 >= s.k0 && k1 <= a.n_k && s.nk <= a.max_k;
   if (!ok) s.nq = 0;
   s.items = (s.nq + a.W - 1) / a.W;
@@ -151,8 +153,9 @@ __device__ inline bool load_seq(const PromptArgs &a, int b, Seq &s) {
 
 // Key tiles that tokens before `tok` of a sequence see; at least one, so that
 // every row gets an output.
+template <bool CROSS>
 __device__ inline int key_tiles(const Seq &s, int tok) {
-  const int64_t seen = min(int64_t(s.nk), int64_t(s.nk) - s.nq + tok);
+  const int64_t seen = CROSS ? int64_t(s.nk) : min(int64_t(s.nk), int64_t(s.nk) - s.nq + tok);
   return seen <= kTile ? 1 : int((seen + kTile - 1) / kTile);
 }
 
@@ -162,12 +165,14 @@ __device__ inline int key_tiles(const Seq &s, int tok) {
 constexpr int kTileCost = 2, kIn = 7;
 
 // What the items before item i of a sequence and head cost.
+template <bool CROSS>
 __device__ inline int64_t cost_before(const PromptArgs &a, const Seq &s, int i) {
+  if (CROSS) return int64_t(i) * (key_tiles<true>(s, 0) * kTileCost + kIn);
   const bool all = i == s.items && i > 0;  // the last item may be a short one
   const int64_t n = all ? i - 1 : i;
   const int64_t base = int64_t(s.nk) - s.nq;  // item j < items - 1 sees base + (j + 1) W keys
   const int64_t ones = max(int64_t(0), min(n, base > kTile ? int64_t(0) : (kTile - base) / a.W));
-  return n * kIn + kTileCost * (ones + tiles_sum(n - ones, a.W, base + (ones + 1) * a.W + kTile - 1)) + (all ? key_tiles(s, s.nq) * kTileCost + kIn : 0);
+  return n * kIn + kTileCost * (ones + tiles_sum(n - ones, a.W, base + (ones + 1) * a.W + kTile - 1)) + (all ? key_tiles<false>(s, s.nq) * kTileCost + kIn : 0);
 }
 
 // How many equal runs the costs of a call's items are dealt in: the CTAs that
@@ -187,11 +192,13 @@ struct Walk {
   int64_t lo;       // where its cost begins
 };
 
+template <bool CROSS>
 __device__ inline void set_item(const PromptArgs &a, Walk &w) {
-  w.n = key_tiles(w.s, int(min(int64_t(w.s.nq), (int64_t(w.q) + 1) * a.W)));
+  w.n = key_tiles<CROSS>(w.s, int(min(int64_t(w.s.nq), (int64_t(w.q) + 1) * a.W)));
 }
 
 // The next item; the caller knows that there is one.
+template <bool CROSS>
 __device__ inline void next_item(const PromptArgs &a, Walk &w, int skip) {
   w.lo += skip ? w.n * kTileCost + kIn : 1;
   if (++w.q == w.s.items) {
@@ -200,11 +207,11 @@ __device__ inline void next_item(const PromptArgs &a, Walk &w, int skip) {
       w.h = 0;
       do {
         w.b++;
-        load_seq(a, w.b, w.s);
+        load_seq<CROSS>(a, w.b, w.s);
       } while (w.s.items == 0);
     }
   }
-  set_item(a, w);
+  set_item<CROSS>(a, w);
 }
 
 // A part of an item: key tiles j0 .. j0 + max(cnt) - 1, of which tile a of the rows
@@ -215,6 +222,7 @@ struct Part {
 };
 
 // The parts of a CTA's run [lo, hi), one after the other.
+template <bool CROSS>
 struct Run {
   Walk w;
   int64_t at, hi;
@@ -230,11 +238,11 @@ struct Run {
       p.first = w.lo + (skip ? kIn : 0), p.last = p.first + (skip ? (w.n - 1) * kTileCost : 0);
       for (int t = 0; t < 2; t++) {
         p.tok[t] = w.q * a.W + t * a.TG;
-        const int n = p.tok[t] < w.s.nq ? key_tiles(w.s, min(w.s.nq, p.tok[t] + a.TG)) : 0;
+        const int n = p.tok[t] < w.s.nq ? key_tiles<CROSS>(w.s, min(w.s.nq, p.tok[t] + a.TG)) : 0;
         p.cnt[t] = max(0, min(j1, n) - j0);
       }
       at = end;
-      if (at < hi) next_item(a, w, skip);
+      if (at < hi) next_item<CROSS>(a, w, skip);
       if (j1 > j0) return true;
     }
     return false;
@@ -352,7 +360,10 @@ __device__ inline uint32_t pack(float lo, float hi) {
 }
 
 // ---- the kernel -----------------------------------------------------------------
-template <int D, bool BF16>
+// CROSS: every query of a sequence sees all of its keys, which others may share
+// and read at the same time.  Beside the lengths, only what a row sees last and
+// what is done about values of V that are not finite differ.
+template <int D, bool BF16, bool CROSS>
 __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ PromptArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Smem<D> &sm = *reinterpret_cast<Smem<D> *>(smem_raw);
@@ -381,11 +392,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
   bool bad = false;
   for (int b = b0; b < b1; b++) {
     Seq s;
-    bad |= !load_seq(a, b, s);
+    bad |= !load_seq<CROSS>(a, b, s);
     if (s.items == 0) continue;
-    cost += cost_before(a, s, s.items) * a.H;
+    cost += cost_before<CROSS>(a, s, s.items) * a.H;
     items += int64_t(s.items) * a.H;
-    most = max(most, key_tiles(s, s.nq));
+    most = max(most, key_tiles<CROSS>(s, s.nq));
   }
   int64_t cost_to = cost, items_to = items;
 #pragma unroll
@@ -419,8 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
     int b = b0;
     for (;; b++) {
       Seq s;
-      load_seq(a, b, s);
-      const int64_t n = s.items == 0 ? 0 : (skip ? cost_before(a, s, s.items) : s.items) * a.H;
+      load_seq<CROSS>(a, b, s);
+      const int64_t n = s.items == 0 ? 0 : (skip ? cost_before<CROSS>(a, s, s.items) : s.items) * a.H;
       if (lo < at + n) break;
       at += n;
     }
@@ -435,33 +446,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
       if (warp == 8) {
       // ---- loads ----
-      Run run;
+      Run<CROSS> run;
       Part p;
       run.at = lo, run.hi = hi, run.skip = skip;
       Walk &w = run.w;
       w.b = sm.b;
-      load_seq(a, w.b, w.s);
-      const int64_t head = skip ? cost_before(a, w.s, w.s.items) : w.s.items;
+      load_seq<CROSS>(a, w.b, w.s);
+      const int64_t head = skip ? cost_before<CROSS>(a, w.s, w.s.items) : w.s.items;
       w.h = int((lo - sm.prefix) / head);
       const int64_t rest = lo - sm.prefix - w.h * head;
       int l = 0, n = w.s.items;  // the last item that begins at or before `rest` is one of l .. l + n - 1
       while (n > 1) {            // 32 of them at a time
         const int step = (n + 31) / 32, at = l + lane * step;
-        const bool behind = lane > 0 && (at >= l + n || (skip ? cost_before(a, w.s, at) : at) > rest);
+        const bool behind = lane > 0 && (at >= l + n || (skip ? cost_before<CROSS>(a, w.s, at) : at) > rest);
         const uint32_t first = __ballot_sync(0xffffffffu, behind);
         const int k = first ? __ffs(first) - 2 : 31;
         n = min(step, l + n - (l + k * step));
         l += k * step;
       }
       w.q = l;
-      w.lo = sm.prefix + w.h * head + (skip ? cost_before(a, w.s, l) : l);
-      set_item(a, w);
+      w.lo = sm.prefix + w.h * head + (skip ? cost_before<CROSS>(a, w.s, l) : l);
+      set_item<CROSS>(a, w);
       if (lane == 0) {
         int stage = 0, turn = 0, seg = 0;
         uint32_t kv_phase = 1, q_phase = 1, todo_phase = 1;  // the first pass over a ring finds it empty
         bool ok = true;
         const uint32_t q_bytes = uint32_t(kChunks) * 128 * a.G * a.TG;
-        const Run begin = run;
+        const Run<CROSS> begin = run;
         int careful = 0;
         for (;;) {
           const bool more = run.next(a, p);
@@ -486,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
           const int64_t c0 = ((p.first + 1) * ctas - 1) / total, c1 = ((p.last + 1) * ctas - 1) / total;
           for (int t = 0; t < 2; t++) todo.cnt[t] = p.cnt[t], todo.tok[t] = p.tok[t];
           todo.nq = p.nq, todo.nk = p.nk, todo.keys = p.nk - p.j0 * kTile, todo.q0 = p.q0, todo.head = p.h * a.G;
-          const int least = min(p.nk - 1, p.nk - p.nq + p.tok[p.cnt[0] > 0 ? 0 : 1]) - p.j0 * kTile;  // the last key of the first row
+          const int least = (CROSS ? p.nk - 1 : min(p.nk - 1, p.nk - p.nq + p.tok[p.cnt[0] > 0 ? 0 : 1])) - p.j0 * kTile;  // the last key of the first row
           todo.cut = max(0, least + 1) / kTile;
           todo.slot = c0 == c1 ? -1 : 2 * int(blockIdx.x) + (seg > 0);  // slot 1: the run's last part
           bar_arrive(&sm.todo_full[turn]);
@@ -628,35 +639,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
                 __syncwarp();
                 if (!careful && lane == 0) bar_arrive(&sm.v_ok[vs]);
               }
-              uint32_t top = 0;
+              if (!CROSS) {  // (no row sees a part of the keys that are left)
+                uint32_t top = 0;
 #pragma unroll 8
-              for (int i = lane; i < kTile * 8 * kChunks; i += 32) {
-                const uint4 w = v[i];
-                top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
-              }
-              const bool odd = __any_sync(0xffffffffu, max(top & 0xffffu, top >> 16) >= kInf);
-              if (odd && !careful) sm.again = 1;
-              if (odd && careful) {
-                any = true;
-                for (int r = 0; r < left; r++)
+                for (int i = lane; i < kTile * 8 * kChunks; i += 32) {
+                  const uint4 w = v[i];
+                  top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+                }
+                const bool odd = __any_sync(0xffffffffu, max(top & 0xffffu, top >> 16) >= kInf);
+                if (odd && !careful) sm.again = 1;
+                if (odd && careful) {
+                  any = true;
+                  for (int r = 0; r < left; r++)
 #pragma unroll
-                  for (int k = 0; k < kMine; k++) {
-                    const int ch = lane * kMine + k;
-                    uint16_t *x = reinterpret_cast<uint16_t *>(sm.kv[vs][ch / 64] + r * 128 + ((ch % 64 / 8 ^ (r & 7)) << 4)) + ch % 8;
-                    const uint32_t w = *x, at = uint32_t(j - cut) * kTile + r;
-                    if ((w & 0x7fffu) < kInf) continue;
-                    if ((w & 0x7fffu) > kInf)
-                      nan[k] = min(nan[k], at);
-                    else if (w >> 15)
-                      down[k] = min(down[k], at);
-                    else
-                      up[k] = min(up[k], at);
-                    *x = 0;
-                  }
-                fence_async();
+                    for (int k = 0; k < kMine; k++) {
+                      const int ch = lane * kMine + k;
+                      uint16_t *x = reinterpret_cast<uint16_t *>(sm.kv[vs][ch / 64] + r * 128 + ((ch % 64 / 8 ^ (r & 7)) << 4)) + ch % 8;
+                      const uint32_t w = *x, at = uint32_t(j - cut) * kTile + r;
+                      if ((w & 0x7fffu) < kInf) continue;
+                      if ((w & 0x7fffu) > kInf)
+                        nan[k] = min(nan[k], at);
+                      else if (w >> 15)
+                        down[k] = min(down[k], at);
+                      else
+                        up[k] = min(up[k], at);
+                      *x = 0;
+                    }
+                  fence_async();
+                }
+                __syncwarp();
+                if (careful && lane == 0) bar_arrive(&sm.v_ok[vs]);
               }
-              __syncwarp();
-              if (careful && lane == 0) bar_arrive(&sm.v_ok[vs]);
             }
             if (lane == 0) bar_arrive(&sm.kv_empty[vs]);
             stage += 2;
@@ -693,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
         const Todo &todo = sm.todo[turn];
         const int cnt = todo.cnt[0] < 0 ? -1 : todo.cnt[t];
         // the last key seen, from the part's first
-        const int last = min(todo.nk - 1, todo.nk - todo.nq + todo.tok[t] + my_tok) - (todo.nk - todo.keys);
+        const int last = CROSS ? todo.keys - 1 : min(todo.nk - 1, todo.nk - todo.nq + todo.tok[t] + my_tok) - (todo.nk - todo.keys);
         if (cnt < 0) break;
         float m = -INFINITY;
         float2 l = make_float2(0.0f, 0.0f);
@@ -908,14 +921,15 @@ __global__ void __launch_bounds__(2 * D, 2048 / (2 * D)) k_prompt_join(const __g
 }
 
 // The status of a call without queries: only its offsets are looked at.
-__global__ void __launch_bounds__(kThreads) k_prompt_none(const int32_t *cu_q, const int32_t *cu_k, int n_seq, int max_q, int max_k, int n_q, int n_k,
+template <bool CROSS>
+__global__ void __launch_bounds__(kThreads) k_prompt_none(const int32_t *cu_q, const int32_t *cu_k, const int32_t *k_len, int n_seq, int max_q, int max_k, int n_q, int n_k,
                                                           uint32_t *status) {
   PromptArgs a{};
-  a.cu_q = cu_q, a.cu_k = cu_k, a.max_q = max_q, a.max_k = max_k, a.n_q = n_q, a.n_k = n_k, a.W = 1;
+  a.cu_q = cu_q, a.cu_k = cu_k, a.k_len = k_len, a.max_q = max_q, a.max_k = max_k, a.n_q = n_q, a.n_k = n_k, a.W = 1;
   bool bad = false;
   for (int b = threadIdx.x; b < n_seq; b += kThreads) {
     Seq s;
-    bad |= !load_seq(a, b, s);
+    bad |= !load_seq<CROSS>(a, b, s);
   }
   bad = __syncthreads_or(bad);
   if (threadIdx.x == 0) *status = bad ? kStBadArg : 0;
@@ -950,47 +964,40 @@ bool make_map(CUtensorMap *map, const void *base, int d, int64_t size1, int64_t 
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool CROSS>
 cudaError_t launch(const PromptArgs &a, unsigned grid, cudaStream_t st) {
   constexpr int kSmem = int(sizeof(Smem<D>));
   static_assert(kSmem <= 227 * 1024, "fits in an SM");
-  const cudaError_t e = cudaFuncSetAttribute(k_prompt<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const cudaError_t e = cudaFuncSetAttribute(k_prompt<D, BF16, CROSS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  k_prompt<D, BF16><<<grid, kThreads, kSmem, st>>>(a);
+  k_prompt<D, BF16, CROSS><<<grid, kThreads, kSmem, st>>>(a);
   const cudaError_t e2 = launch_early(k_prompt_join<D, BF16>, dim3(grid, kRows / 8), dim3(2 * D), 0, st, a);
   return e2 != cudaSuccess ? e2 : cudaGetLastError();
 }
 
-}  // namespace
-}  // namespace cg
+size_t workspace_bytes(const cg_prompt &p) { return size_t(kNotes + 4 * uint64_t(2 * kGrid) * kRows * (padded(p.d) + 2)); }
 
-extern "C" size_t cg_prompt_workspace_bytes(const cg_prompt *prompt) {
-  using namespace cg;
-  if (!prompt_ok(prompt)) return 0;
-  return size_t(kNotes + 4 * uint64_t(2 * kGrid) * kRows * (padded(prompt->d) + 2));
-}
-
-extern "C" cg_status cg_prompt_attend(const cg_prompt *prompt, const void *q_dev, const void *k_dev,
-                                      const void *v_dev, const int32_t *cu_q_dev, const int32_t *cu_k_dev,
-                                      void *out_dev, float *lse_dev, void *ws_dev, size_t ws_bytes, void *stream) {
-  using namespace cg;
+// Both calls: k_first is cu_k, or (CROSS) where each sequence's keys begin.
+template <bool CROSS>
+cg_status attend(const cg_prompt *prompt, const void *q_dev, const void *k_dev, const void *v_dev, const int32_t *cu_q_dev,
+                 const int32_t *k_first_dev, const int32_t *k_len_dev, void *out_dev, float *lse_dev, void *ws_dev, size_t ws_bytes, void *stream) {
   // arrays without rows may be NULL
-  if (!prompt_ok(prompt) || ((!q_dev || !out_dev) && prompt->n_q > 0) || ((!k_dev || !v_dev) && prompt->n_k > 0) || !cu_q_dev || !cu_k_dev ||
-      !ws_dev)
+  if (!prompt_ok(prompt) || ((!q_dev || !out_dev) && prompt->n_q > 0) || ((!k_dev || !v_dev) && prompt->n_k > 0) || !cu_q_dev || !k_first_dev ||
+      (CROSS && !k_len_dev) || !ws_dev)
     return CG_ERR_INVALID_ARG;
   if (!is_aligned(q_dev, 16) || !is_aligned(k_dev, 16) || !is_aligned(v_dev, 16) || !is_aligned(out_dev, 16) ||
-      !is_aligned(cu_q_dev, 4) || !is_aligned(cu_k_dev, 4) || !is_aligned(lse_dev, 4) || !is_aligned(ws_dev, 256) ||
-      ws_bytes < cg_prompt_workspace_bytes(prompt))
+      !is_aligned(cu_q_dev, 4) || !is_aligned(k_first_dev, 4) || !is_aligned(k_len_dev, 4) || !is_aligned(lse_dev, 4) || !is_aligned(ws_dev, 256) ||
+      ws_bytes < workspace_bytes(*prompt))
     return CG_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t *ws = static_cast<uint8_t *>(ws_dev);
   const cg_prompt &p = *prompt;
   if (p.max_q == 0 || p.n_q == 0) {
-    k_prompt_none<<<1, kThreads, 0, st>>>(cu_q_dev, cu_k_dev, p.n_seq, p.max_q, p.max_k, p.n_q, p.n_k, reinterpret_cast<uint32_t *>(ws));
+    k_prompt_none<CROSS><<<1, kThreads, 0, st>>>(cu_q_dev, k_first_dev, k_len_dev, p.n_seq, p.max_q, p.max_k, p.n_q, p.n_k, reinterpret_cast<uint32_t *>(ws));
     return launched();
   }
   PromptArgs a{};
-  a.cu_q = cu_q_dev, a.cu_k = cu_k_dev;
+  a.cu_q = cu_q_dev, a.cu_k = k_first_dev, a.k_len = k_len_dev;
   a.out = static_cast<uint16_t *>(out_dev), a.lse = lse_dev;
   a.status = reinterpret_cast<uint32_t *>(ws);
   a.notes = reinterpret_cast<Note *>(ws + 256);
@@ -1008,7 +1015,28 @@ extern "C" cg_status cg_prompt_attend(const cg_prompt *prompt, const void *q_dev
   }
   if (!ok) return CG_ERR_INVALID_ARG;  // strides that a tensor map cannot have
   const bool bf16 = p.dtype == CG_BF16;
-  const cudaError_t e = p.d <= 64 ? (bf16 ? launch<64, true>(a, kGrid, st) : launch<64, false>(a, kGrid, st))
-                                  : (bf16 ? launch<128, true>(a, kGrid, st) : launch<128, false>(a, kGrid, st));
+  const cudaError_t e = p.d <= 64 ? (bf16 ? launch<64, true, CROSS>(a, kGrid, st) : launch<64, false, CROSS>(a, kGrid, st))
+                                  : (bf16 ? launch<128, true, CROSS>(a, kGrid, st) : launch<128, false, CROSS>(a, kGrid, st));
   return e == cudaSuccess ? CG_OK : CG_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace cg
+
+extern "C" size_t cg_prompt_workspace_bytes(const cg_prompt *prompt) {
+  using namespace cg;
+  if (!prompt_ok(prompt)) return 0;
+  return workspace_bytes(*prompt);
+}
+
+extern "C" cg_status cg_prompt_attend(const cg_prompt *prompt, const void *q_dev, const void *k_dev,
+                                      const void *v_dev, const int32_t *cu_q_dev, const int32_t *cu_k_dev,
+                                      void *out_dev, float *lse_dev, void *ws_dev, size_t ws_bytes, void *stream) {
+  return cg::attend<false>(prompt, q_dev, k_dev, v_dev, cu_q_dev, cu_k_dev, nullptr, out_dev, lse_dev, ws_dev, ws_bytes, stream);
+}
+
+extern "C" cg_status cg_cross_attend(const cg_prompt *prompt, const void *q_dev, const void *k_dev, const void *v_dev,
+                                     const int32_t *cu_q_dev, const int32_t *k_begin_dev, const int32_t *k_len_dev,
+                                     void *out_dev, float *lse_dev, void *ws_dev, size_t ws_bytes, void *stream) {
+  return cg::attend<true>(prompt, q_dev, k_dev, v_dev, cu_q_dev, k_begin_dev, k_len_dev, out_dev, lse_dev, ws_dev, ws_bytes, stream);
 }
