@@ -139,6 +139,40 @@ cg_status cg_cache_attend(const cg_cache *cache, const cg_attend *attend, const 
                           const int32_t *len_dev, void *out_dev, float *lse_dev, void *ws_dev, size_t ws_bytes,
                           void *stream);
 
+/* ---- attention of new tokens whose sequences share a prefix ----------------- */
+typedef struct {
+    int32_t n_groups;            /* groups, empty ones among them            */
+    int32_t n_members;           /* entries of member_dev                    */
+    const int32_t *cu_group_dev; /* [n_groups + 1]                           */
+    const int32_t *member_dev;   /* [n_members]                              */
+    const int32_t *shared_dev;   /* [n_groups]                               */
+} cg_groups;
+
+/* Workspace bytes of cg_shared_attend (0 on bad input). */
+size_t cg_shared_workspace_bytes(const cg_cache *cache, const cg_attend *attend, const cg_groups *groups);
+
+/* cg_cache_attend for sequences of which some share the pages of a prefix, as
+ * they do after cg_pages_fork: a shared prefix is read once for all of its
+ * readers.  Sequences member[cu_group[g]] .. member[cu_group[g+1]-1] are in
+ * group g, and their rows of the table begin with the same shared[g] pages, all
+ * of them full (cg_pages_groups finds groups, and its arrays can be passed as
+ * they are).  Arguments, formulas and outputs are those of cg_cache_attend, with
+ * one difference: of a shared prefix a weight is off by at most 2^-11 of itself
+ * or 2^-36 of the largest probability times the largest V scale, whichever is
+ * more.
+ * Sequences that are in no group, and those of a group whose first new token
+ * does not see its whole prefix, read all of their positions by themselves.  A
+ * group of one is slower than none.  Pages of a shared prefix hold no e4m3 NaN.
+ * Without groups or members it is cg_cache_attend (the arrays may be NULL then).
+ * Device errors: as for cg_cache_attend, and CG_ERR_INVALID_ARG for offsets
+ * that are negative, fall or pass n_members (no group counts), a shared[g] that
+ * is negative or more than a row of the table (that group does not), a member
+ * that is no sequence, or named before (that entry does not). */
+cg_status cg_shared_attend(const cg_cache *cache, const cg_attend *attend, const cg_groups *groups, const void *q_dev,
+                           const void *k_pool, const void *v_pool, const float *k_scale, const float *v_scale,
+                           const int32_t *table_dev, const int32_t *len_dev, void *out_dev, float *lse_dev, void *ws_dev,
+                           size_t ws_bytes, void *stream);
+
 /* ---- attention of whole prompts ------------------------------------------- */
 typedef struct {
     int32_t n_seq;

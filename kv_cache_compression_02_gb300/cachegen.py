@@ -57,6 +57,11 @@ class cg_pages(ctypes.Structure):
                 ("table_dev", ctypes.c_void_p), ("len_dev", ctypes.c_void_p)]
 
 
+class cg_groups(ctypes.Structure):
+    _fields_ = [("n_groups", ctypes.c_int32), ("n_members", ctypes.c_int32), ("cu_group_dev", ctypes.c_void_p),
+                ("member_dev", ctypes.c_void_p), ("shared_dev", ctypes.c_void_p)]
+
+
 class CacheGenError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {cg_status_str(status)}")
@@ -103,6 +108,8 @@ def lib() -> ctypes.CDLL:
             "cg_cache_write": (ctypes.c_int, [P] * 12 + [S, P]),
             "cg_cache_workspace_bytes": (S, [P, P]),
             "cg_cache_attend": (ctypes.c_int, [P] * 12 + [S, P]),
+            "cg_shared_workspace_bytes": (S, [P, P, P]),
+            "cg_shared_attend": (ctypes.c_int, [P] * 13 + [S, P]),
             "cg_prompt_workspace_bytes": (S, [P]),
             "cg_prompt_attend": (ctypes.c_int, [P] * 9 + [S, P]),
             "cg_cross_attend": (ctypes.c_int, [P] * 10 + [S, P]),
@@ -214,6 +221,18 @@ class Pages:
     def __init__(self, refs, table, lens):
         self.tensors = (refs, table, lens)
         self.c = cg_pages(table.shape[0], table.shape[1], _ptr(refs), _ptr(table), _ptr(lens))
+        self.ref = ctypes.addressof(self.c)
+
+
+class Groups:
+    """Sequences that share prefixes, for cg_shared_attend: device int32 tensors cu_group [n_groups + 1], member and shared
+    [n_groups] (as cg_pages_groups writes them), kept for as long as this object."""
+
+    def __init__(self, cu_group, member, shared):
+        if cu_group.numel() != shared.numel() + 1:
+            raise ValueError(f"cu_group has {cu_group.numel()} offsets for {shared.numel()} groups")
+        self.tensors = (cu_group, member, shared)
+        self.c = cg_groups(shared.numel(), member.numel(), _ptr(cu_group), _ptr(member), _ptr(shared))
         self.ref = ctypes.addressof(self.c)
 
 
@@ -381,6 +400,17 @@ def cg_cache_attend(cache: Cache, attend: Attend, q, k_pool, v_pool, k_scale, v_
     return lib().cg_cache_attend(cache.ref, attend.for_cache(cache), _ptr(q), _ptr(k_pool), _ptr(v_pool),
                                  _ptr(k_scale), _ptr(v_scale), _ptr(table), _ptr(lens), _ptr(out), _ptr(lse),
                                  _ptr(ws), _bytes(ws), _stream(stream))
+
+
+def cg_shared_workspace_bytes(cache: Cache, attend: Attend, groups: Groups) -> int:
+    return lib().cg_shared_workspace_bytes(cache.ref, attend.for_cache(cache), groups.ref)
+
+
+def cg_shared_attend(cache: Cache, attend: Attend, groups: Groups, q, k_pool, v_pool, k_scale, v_scale, table, lens, out, lse, ws,
+                     stream=None) -> int:
+    """lse may be None."""
+    return lib().cg_shared_attend(cache.ref, attend.for_cache(cache), groups.ref, _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
+                                  _ptr(table), _ptr(lens), _ptr(out), _ptr(lse), _ptr(ws), _bytes(ws), _stream(stream))
 
 
 def cg_prompt_workspace_bytes(prompt: Prompt) -> int:

@@ -1,0 +1,991 @@
+// cg_shared.cu -- cg_shared_attend: new tokens of sequences that share a prefix.
+//
+// The rows of all readers of a prefix that read the same KV head (members x T x
+// Hq / H of them) are one matrix Q, and the prefix is gone over once for up to
+// 256 of its rows:  S = Q K^T, P = 2^(S - max), O = P V, in tiles of 128 rows and
+// 128 positions on tcgen05.  What a sequence has to itself is left to the
+// kernels of cg_cache_attend, and the two parts, each with its maximum m and sum
+// l, are joined: with M = max m_i, l = sum l_i 2^(m_i - M), out = sum O_i 2^(m_i -
+// M) / l.
+//
+// Codes of either format are exact in f16, which is what the products take.  A
+// bf16 query row is raised to the top of f16's range by a power of two.  K's
+// page scales are applied to the scores, V's to the probabilities, over a power
+// of two above the largest scale so far (O is scaled when that grows).  P is
+// rounded to f16: a weight is off by at most 2^-11 of itself or 2^-36 of the
+// largest times the largest scale, whichever is more (p < 2^15, and the largest
+// has at least 2^12).
+//
+// A CTA has two tiles of rows, a and b, whose softmax warpgroups take turns with
+// the products; where an item has up to 128 rows, a and b are the same rows
+// and take the even and the odd tiles of positions.  Warps: 0-3 and 4-7 the
+// softmax of a and b, one row a thread; 8-11 turn codes into operands in shared
+// memory; 12-14 look up pages and scales, a tile each in turns; 15 issues the
+// products.
+#include "cg_shared.cuh"
+
+#include "cg_cache.cuh"
+#include "cg_tc.cuh"
+#include "cg_tma.cuh"
+
+namespace cg {
+namespace {
+
+constexpr int kThreads = 512;
+// Registers a thread: 512 are launched with 128 each (2 * 176 + 88 + 72 = 4 * 128).
+constexpr int kSoftRegs = 176, kConvRegs = 88, kOtherRegs = 72;
+constexpr int kTile = 128;  // rows of a tile, positions of a tile
+constexpr int kRows = 2 * kTile;
+constexpr int kGrid = kSMs;
+constexpr int kStages = 4;   // operand tiles of K or V
+constexpr int kInfo = 6;     // tiles whose pages and scales are known
+constexpr int kLookers = 3;  // warps that look them up
+constexpr int kPlan = 1024;
+// p = 2^(s - m + kLift) < 2^15, m at most kLag under the maximum: as in the kernels whose parts are joined with these
+constexpr float kLift = 12.0f, kLag = 3.0f;
+// What an item costs: kIn for its way in and out, and for each tile of positions.
+constexpr int kIn = 10, kFull = 4, kSplit = 2;
+
+struct Note {
+  uint32_t errors;
+  int32_t parts;   // of the item that this CTA has the first but not the last part of, or 0
+  int32_t second;  // the first part is in this CTA's second slot
+  int32_t g, h, q;
+};
+
+struct SharedArgs {
+  const uint16_t *q;
+  const uint8_t *kp, *vp;
+  const float *ks, *vs;
+  const int32_t *table, *len;
+  uint16_t *out;
+  float *lse;
+  const int32_t *cu, *member, *shared;  // the caller's groups
+  uint32_t *status, *bad;
+  int32_t *owner, *first;  // of a sequence: its entry in the groups, and the pages that it shares
+  int32_t *seq;            // of an entry: its sequence, or -1
+  int32_t *keys, *lead;    // of a group: its positions (0: nothing to do), and an entry whose row of the table has them
+  float *own, *own_ml;
+  Note *notes;
+  float *parts;  // [2 * kGrid][kRows][D + 2]
+  int64_t q_seq, q_tok, q_head;
+  int n_groups, n_members, B, T, Hq, H, G, TG, d, bt, n_blocks, stride;  // TG: rows of a sequence and KV head
+  float scale_log2;  // scale * log2(e)
+  bool bf16;
+};
+
+// Pages and scales of a tile of positions.
+struct Info {
+  int64_t row[kTile];  // where a position's codes begin, or -1
+  float ks[kTile], vs[kTile];
+  uint32_t valid[4];
+  int v_exp, whole;
+};
+
+// What is to be done for a part of an item.
+struct Todo {
+  int n, split;      // tiles of positions; n < 0: the end
+  int e0, row0, rows;  // the group's first entry; the block's first row, and the group's rows
+  int head, slot;    // KV head; slot of the workspace, or -1: the item is whole
+};
+
+template <int D>
+struct Smem {
+  static constexpr int kChunks = D / 64;  // of 64 channels: 128 bytes, a swizzled row
+  uint8_t q[2][kChunks][kTile * 128];
+  uint8_t kv[kStages][kChunks][kTile * 128];
+  Info info[kInfo];
+  float ml[kTile][2];  // split: b's maximum and sum, for a
+  int ml_exp;
+  uint64_t todo_full[2], todo_empty[2], info_full[kInfo], info_empty[kInfo], q_full, q_empty, kv_full[kStages], kv_empty[kStages], s_full[2],
+      p_full[2][2], o_full[2], ml_full, ml_empty;
+  Todo todo[2];
+  uint32_t tmem, errors, dead;
+  int most[kThreads / 32], g;
+  int64_t sum[kThreads / 32][2], prefix;
+};
+
+// ---- the plan: who takes part -----------------------------------------------------
+// An entry of a group counts where it is the first to name its sequence and every
+// new token of the sequence sees the whole prefix; the others read their
+// positions by themselves.
+__global__ void __launch_bounds__(kPlan) k_shared_plan(const SharedArgs a) {
+  for (int b = threadIdx.x; b < a.B; b += kPlan) a.owner[b] = 0x7fffffff, a.first[b] = 0;
+  bool bad = false, fall = false;
+  for (int g = threadIdx.x; g < a.n_groups; g += kPlan) {
+    a.keys[g] = 0, a.lead[g] = 0x7fffffff;
+    fall |= a.cu[g] < 0 || a.cu[g + 1] < a.cu[g] || a.cu[g + 1] > a.n_members;
+    bad |= a.shared[g] < 0 || a.shared[g] > a.stride;
+  }
+  fall = __syncthreads_or(fall);
+  if (!fall) {
+    const int e0 = a.cu[0], e1 = a.cu[a.n_groups];
+    for (int e = e0 + threadIdx.x; e < e1; e += kPlan) {
+      const int b = a.member[e];
+      if (uint32_t(b) < uint32_t(a.B))
+        atomicMin(&a.owner[b], e);
+      else
+        bad = true;
+    }
+    __syncthreads();
+    for (int e = e0 + threadIdx.x; e < e1; e += kPlan) {
+      const int b = a.member[e];
+      int takes = -1;
+      if (uint32_t(b) < uint32_t(a.B)) {
+        if (__ldcg(&a.owner[b]) != e) {
+          bad = true;
+        } else {
+          int g = 0, hi = a.n_groups;  // the last group that begins at or before e
+          while (hi - g > 1) {
+            const int mid = g + (hi - g) / 2;
+            if (a.cu[mid] <= e)
+              g = mid;
+            else
+              hi = mid;
+          }
+          const int pages = a.shared[g];
+          const int64_t keys = int64_t(pages) * a.bt, len = max(int64_t(0), min(int64_t(a.len[b]), int64_t(a.stride) * a.bt));
+          if (pages > 0 && pages <= a.stride && len - a.T + 1 >= keys) {
+            takes = b;
+            a.first[b] = pages;
+            a.keys[g] = int(keys);
+            atomicMin(&a.lead[g], e);
+          }
+        }
+      }
+      a.seq[e] = takes;
+    }
+  }
+  bad = __syncthreads_or(bad || fall);
+  if (threadIdx.x == 0) *a.bad = bad ? kStBadArg : 0;
+}
+
+// ---- items --------------------------------------------------------------------------
+// Item (g, h, q): rows 256 q ... of group g, KV head h.
+struct Group {
+  int rows, tiles, blocks;
+};
+
+__device__ inline Group load_group(const SharedArgs &a, int g) {
+  Group s;
+  const int keys = a.keys[g];
+  s.rows = keys > 0 ? (a.cu[g + 1] - a.cu[g]) * a.TG : 0;
+  s.blocks = (s.rows + kRows - 1) / kRows, s.tiles = (keys + kTile - 1) / kTile;
+  return s;
+}
+
+__device__ inline bool is_split(const Group &s, int q) { return s.rows - q * kRows <= kTile; }
+
+__device__ inline int tile_cost(const Group &s, int q) { return is_split(s, q) ? kSplit : kFull; }
+
+__device__ inline int64_t item_cost(const Group &s, int q, int skip) { return skip ? kIn + int64_t(s.tiles) * tile_cost(s, q) : 1; }
+
+__device__ inline int64_t head_cost(const Group &s, int skip) {
+  return s.blocks == 0 ? 0 : skip ? (s.blocks - 1) * (kIn + int64_t(s.tiles) * kFull) + item_cost(s, s.blocks - 1, 1) : s.blocks;
+}
+
+struct Part {
+  int g, h, q, j0, n;
+  int64_t first, last;  // where the costs of the item's first and last tile begin
+};
+
+// The parts of a CTA's run [lo, hi), one after the other.
+struct Run {
+  Group s;
+  int g, h, q;
+  int64_t lo;  // where the item's cost begins
+  int64_t at, hi;
+  int skip;  // 1: items have their costs; 0: each is one
+
+  __device__ bool next(const SharedArgs &a, Part &p) {
+    while (at < hi) {
+      // a tile belongs to the run in which its cost begins
+      const int64_t cost = item_cost(s, q, skip), end = min(hi, lo + cost);
+      const int each = tile_cost(s, q);
+      auto tiles_before = [&](int64_t x) { return int(max(int64_t(0), x - lo - kIn + each - 1) / each); };
+      p.j0 = skip ? tiles_before(at) : 0;
+      p.n = (skip ? tiles_before(end) : s.tiles) - p.j0;
+      p.g = g, p.h = h, p.q = q;
+      p.first = lo + (skip ? kIn : 0), p.last = p.first + (skip ? int64_t(s.tiles - 1) * each : 0);
+      at = end;
+      if (at < hi) {
+        lo += cost;
+        if (++q == s.blocks) {
+          q = 0;
+          if (++h == a.H) {
+            h = 0;
+            do s = load_group(a, ++g);
+            while (s.blocks == 0);
+          }
+        }
+      }
+      if (p.n > 0) return true;
+    }
+    return false;
+  }
+};
+
+// Codes in the low (HALF = 0) or high half of w -> two f16.
+template <int FMT, int HALF>
+__device__ inline uint32_t halves_of(uint32_t w) {
+  uint32_t r;
+  if (FMT == CG_CACHE_E4M3) {
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(uint16_t(HALF ? w >> 16 : w)));
+  } else {  // 0x64uu is 1024 + u; w holds code + 128
+    const __half2 x = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    uint32_t p = __byte_perm(w, 0x64646464u, HALF ? 0x4342 : 0x4140);
+    const __half2 y = __hsub2(*reinterpret_cast<__half2 *>(&p), x);
+    r = *reinterpret_cast<const uint32_t *>(&y);
+  }
+  return r;
+}
+
+template <int FMT>
+__device__ inline uint4 operands_of(uint2 w) {  // eight codes
+  if (FMT == CG_CACHE_INT8) w.x ^= 0x80808080u, w.y ^= 0x80808080u;
+  return make_uint4(halves_of<FMT, 0>(w.x), halves_of<FMT, 1>(w.x), halves_of<FMT, 0>(w.y), halves_of<FMT, 1>(w.y));
+}
+
+// PLAIN: pages are a multiple of 16 tokens, so that 16 positions have one scale.
+template <int FMT, int D, bool PLAIN>
+__global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ SharedArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Smem<D> &sm = *reinterpret_cast<Smem<D> *>(smem_raw);
+  constexpr int kChunks = Smem<D>::kChunks;
+  constexpr uint32_t kTileBytes = kChunks * kTile * 128;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (threadIdx.x == 0) {
+    sm.errors = sm.dead = 0;
+    a.notes[blockIdx.x].parts = 0;
+    bar_init(&sm.q_full, 8), bar_init(&sm.q_empty, 1);
+    for (int i = 0; i < 2; i++) bar_init(&sm.todo_full[i], 1), bar_init(&sm.todo_empty[i], 13);  // 13 warps read it
+    for (int i = 0; i < kInfo; i++) bar_init(&sm.info_full[i], 1), bar_init(&sm.info_empty[i], 1);
+    for (int i = 0; i < kStages; i++) bar_init(&sm.kv_full[i], 4), bar_init(&sm.kv_empty[i], 1);
+    for (int t = 0; t < 2; t++) bar_init(&sm.s_full[t], 1), bar_init(&sm.p_full[t][0], 4), bar_init(&sm.p_full[t][1], 4), bar_init(&sm.o_full[t], 1);
+    bar_init(&sm.ml_full, 4), bar_init(&sm.ml_empty, 4);
+    bar_init_fence();
+  }
+  if (warp == 15) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_of(&sm.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  // The items of the call and what they cost.
+  const int per = (a.n_groups + kThreads - 1) / kThreads, g0 = threadIdx.x * per, g1 = min(a.n_groups, g0 + per);
+  int64_t cost = 0, items = 0;
+  int most = 0;
+  for (int g = g0; g < g1; g++) {
+    const Group s = load_group(a, g);
+    cost += head_cost(s, 1) * a.H, items += int64_t(s.blocks) * a.H;
+    if (s.blocks) most = max(most, s.tiles);
+  }
+  int64_t cost_to = cost, items_to = items;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, cost_to, o), z = __shfl_up_sync(0xffffffffu, items_to, o);
+    if (lane >= o) cost_to += y, items_to += z;
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) sm.sum[warp][0] = cost_to, sm.sum[warp][1] = items_to, sm.most[warp] = most;
+  tm_before();
+  __syncthreads();
+  tm_after();
+  int64_t total = 0, n_items = 0;
+  for (int w = 0; w < kThreads / 32; w++) {
+    if (w < warp) cost_to += sm.sum[w][0], items_to += sm.sum[w][1];
+    total += sm.sum[w][0], n_items += sm.sum[w][1];
+    most = max(most, sm.most[w]);
+  }
+  const int skip = most <= 1 && n_items <= gridDim.x ? 0 : 1;  // 0: a CTA per item
+  if (!skip) total = n_items, cost = items, cost_to = items_to;
+  const int64_t before = cost_to - cost;
+  // no run is shorter than a tile: each has one of every item that goes through it
+  const int64_t ctas = min(int64_t(gridDim.x), skip ? (total + kFull - 1) / kFull : total);
+  const int64_t lo = ctas ? total * blockIdx.x / ctas : 0, hi = ctas ? total * (blockIdx.x + 1) / ctas : 0;
+  const bool busy = int64_t(blockIdx.x) < ctas;
+  if (busy && lo >= before && lo < before + cost) {  // one thread's groups hold the first cost
+    int64_t at = before;
+    int g = g0;
+    for (;; g++) {
+      const int64_t n = head_cost(load_group(a, g), skip) * a.H;
+      if (lo < at + n) break;
+      at += n;
+    }
+    sm.g = g;
+    sm.prefix = at;
+  }
+  __syncthreads();
+  const uint32_t tmem = sm.tmem;
+
+  if (busy) {
+    if (warp >= 12) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+      if (warp < 12 + kLookers) {
+        // ---- pages and scales ----
+        Run run;
+        Part p;
+        run.at = lo, run.hi = hi, run.skip = skip, run.g = sm.g;
+        run.s = load_group(a, run.g);
+        const int64_t head = head_cost(run.s, skip), rest0 = lo - sm.prefix;
+        run.h = int(rest0 / head);
+        const int64_t rest = rest0 - run.h * head;
+        run.q = int(min(int64_t(run.s.blocks) - 1, rest / (skip ? kIn + int64_t(run.s.tiles) * kFull : 1)));
+        run.lo = sm.prefix + run.h * head + run.q * (skip ? kIn + int64_t(run.s.tiles) * kFull : 1);
+        int turn = 0, seg = 0, slot = 0, who = 0;
+        uint32_t todo_phase = 1, phase = 1;  // the first pass over a ring finds it empty
+        bool ok = true;
+        while (ok) {
+          const bool more = run.next(a, p);
+          if (warp == 12) {
+            if (!(ok = bar_wait(&sm.todo_empty[turn], todo_phase, &sm.dead))) break;
+            if (lane == 0) {
+              Todo &todo = sm.todo[turn];
+              if (!more) {
+                todo.n = -1;
+              } else {
+                // who has tiles of this item
+                const int64_t c0 = ((p.first + 1) * ctas - 1) / total, c1 = ((p.last + 1) * ctas - 1) / total;
+                todo.n = p.n;
+                todo.e0 = a.cu[p.g], todo.row0 = p.q * kRows, todo.rows = (a.cu[p.g + 1] - a.cu[p.g]) * a.TG;
+                todo.split = todo.rows - todo.row0 <= kTile;
+                todo.head = p.h;
+                todo.slot = c0 == c1 ? -1 : 2 * int(blockIdx.x) + (seg > 0);  // slot 1: the run's last part
+                if (c0 != c1 && int64_t(blockIdx.x) == c0) {
+                  Note &note = a.notes[blockIdx.x];
+                  note.parts = int(c1 - c0 + 1), note.second = seg > 0, note.g = p.g, note.h = p.h, note.q = p.q;
+                }
+              }
+              bar_arrive(&sm.todo_full[turn]);
+            }
+            __syncwarp();
+            seg++;
+            turn ^= 1;
+            if (turn == 0) todo_phase ^= 1;
+          }
+          if (!more) break;
+          const int keys = a.keys[p.g];
+          const int32_t *row = a.table + int64_t(a.seq[a.lead[p.g]]) * a.stride;
+          for (int j = 0; j < p.n; j++) {
+            if (who == warp - 12) {
+              if (!(ok = bar_wait(&sm.info_empty[slot], phase, &sm.dead))) break;
+              Info &in = sm.info[slot];
+              int page[4], at[4];
+#pragma unroll
+              for (int k = 0; k < 4; k++) {
+                const int tok = (p.j0 + j) * kTile + 32 * k + lane, blk = tok / a.bt;
+                at[k] = tok < keys ? tok - blk * a.bt : -1;
+                page[k] = tok < keys ? row[blk] : -1;
+              }
+              float ks[4], vs[4], top = 0.0f;
+              bool good[4];
+#pragma unroll
+              for (int k = 0; k < 4; k++) {
+                good[k] = uint32_t(page[k]) < uint32_t(a.n_blocks);
+                if (at[k] >= 0 && !good[k]) atomicOr(&sm.errors, kStBadArg);
+                const int64_t sc = good[k] ? int64_t(page[k]) * a.H + p.h : 0;
+                ks[k] = good[k] ? a.ks[sc] : 0.0f, vs[k] = good[k] ? a.vs[sc] : 0.0f;
+              }
+              int whole = 1;
+#pragma unroll
+              for (int k = 0; k < 4; k++) {
+                const uint32_t valid = __ballot_sync(0xffffffffu, good[k]);
+                whole &= valid == 0xffffffffu;
+                in.row[32 * k + lane] = good[k] ? page_row(page[k], a.H, p.h, a.bt, at[k], a.d) : -1;
+                in.ks[32 * k + lane] = ks[k], in.vs[32 * k + lane] = vs[k];
+                top = fmaxf(top, fabsf(vs[k]));
+                if (lane == 0) in.valid[k] = valid;
+              }
+              const int e = __reduce_max_sync(0xffffffffu, min(254, int(__float_as_uint(top) >> 23) + 1));
+              if (lane == 0) in.v_exp = e, in.whole = whole;
+              __syncwarp();
+              if (lane == 0) bar_arrive(&sm.info_full[slot]);
+            }
+            if (++who == kLookers) who = 0;
+            if (++slot == kInfo) slot = 0, phase ^= 1;
+          }
+        }
+      } else {
+        // ---- products ----
+        constexpr uint32_t kCommon = 1u << 4 | uint32_t(kTile >> 4) << 24;  // f16 operands, fp32 sums
+        constexpr uint32_t kS = kCommon | uint32_t(kTile >> 3) << 17, kO = kCommon | 1u << 16 | uint32_t(D >> 3) << 17;
+        constexpr uint32_t kChunk = kTile * 128 >> 4, kStage = kTileBytes >> 4;
+        const uint32_t q_lo = operand_lo(sm.q[0], 16), k_lo = operand_lo(sm.kv[0], 16), v_lo = operand_lo(sm.kv[0], kTile * 128);
+        int stage = 0, turn = 0, slot = 0;
+        uint32_t kv_phase = 0, q_phase = 0, todo_phase = 0, p_phase[2] = {0, 0};
+        bool ok = true;
+        auto s_product = [&](int t, int q, int st) {  // S_t = Q_q K^T
+          const uint32_t a0 = q_lo + q * kStage, b0 = k_lo + st * kStage;
+          if (elected()) {
+#pragma unroll
+            for (int k = 0; k < D / 16; k++)
+              mma_ss(tmem + t * kTile, a0 + k / 4 * kChunk + k % 4 * 2, b0 + k / 4 * kChunk + k % 4 * 2, kS, k > 0);
+            mma_commit(&sm.s_full[t]);
+          }
+        };
+        auto take = [&]() {  // the next operand tile
+          const int st = stage;
+          ok = bar_wait(&sm.kv_full[st], kv_phase, &sm.dead);
+          if (++stage == kStages) stage = 0, kv_phase ^= 1;
+          return st;
+        };
+        for (;;) {
+          if (!(ok = bar_wait(&sm.todo_full[turn], todo_phase, &sm.dead))) break;
+          const int n = sm.todo[turn].n, split = sm.todo[turn].split;
+          __syncwarp();
+          if (lane == 0) bar_arrive(&sm.todo_empty[turn]);
+          turn ^= 1;
+          if (turn == 0) todo_phase ^= 1;
+          if (n < 0) break;
+          if (!(ok = bar_wait(&sm.q_full, q_phase, &sm.dead))) break;
+          q_phase ^= 1;
+          const int ahead = split ? 2 : 1;  // how many tiles of K come before the first of V
+          for (int i = 0; i < min(ahead, n) && ok; i++) {
+            const int ks = take();
+            if (!ok) break;
+            tm_after();
+            if (split) {
+              s_product(i, 0, ks);
+            } else {
+              s_product(0, 0, ks);
+              s_product(1, 1, ks);
+            }
+            if (elected()) {
+              mma_commit(&sm.kv_empty[ks]);
+              if (i + 1 == n) mma_commit(&sm.q_empty);
+            }
+          }
+          for (int j = 0; j < n && ok; j++) {
+            const bool more = j + ahead < n;
+            const int vs = take();
+            if (!ok) break;
+            const int ks = more ? take() : 0;
+            if (!ok) break;
+#pragma unroll
+            for (int t = 0; t < 2; t++) {
+              if (split && t != (j & 1)) continue;
+              const uint32_t b0 = v_lo + vs * kStage;
+#pragma unroll
+              for (int half = 0; half < 2; half++) {  // O_t += P_t V
+                if (!(ok = bar_wait(&sm.p_full[t][half], p_phase[t], &sm.dead))) break;
+                tm_after();
+                if (elected())
+#pragma unroll
+                  for (int k = half * 4; k < half * 4 + 4; k++)
+                    mma_ts(tmem + 2 * kTile + t * kTile, tmem + t * kTile + k * 8, b0 + k * (2048 >> 4), kO, j >= ahead || k > 0);
+              }
+              if (!ok) break;
+              p_phase[t] ^= 1;
+              if (more)
+                s_product(t, split ? 0 : t, ks);
+              else if (elected())
+                mma_commit(&sm.o_full[t]);
+            }
+            if (!ok) break;
+            if (elected()) {
+              mma_commit(&sm.kv_empty[vs]);
+              mma_commit(&sm.info_empty[slot]);
+              if (more) mma_commit(&sm.kv_empty[ks]);
+              if (j + ahead + 1 == n) mma_commit(&sm.q_empty);
+            }
+            if (++slot == kInfo) slot = 0;
+          }
+          if (!ok) break;
+        }
+      }
+    } else if (warp >= 8) {
+      // ---- codes into operands ----
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
+      const int ct = threadIdx.x - 256;
+      int stage = 0, turn = 0, k_slot = 0, v_slot = 0;
+      uint32_t kv_phase = 1, todo_phase = 0, k_phase = 0, v_phase = 0;
+      bool ok = true;
+      auto fill = [&](const uint8_t *pool, int slot, uint32_t phase) {
+        if (!(ok = bar_wait(&sm.info_full[slot], phase, &sm.dead))) return;
+        if (!(ok = bar_wait(&sm.kv_empty[stage], kv_phase, &sm.dead))) return;
+        const Info &in = sm.info[slot];
+        constexpr int kUnits = D / 8;  // eight codes each, of a row
+        const int u = ct % kUnits, r0 = ct / kUnits;
+        constexpr int kStep = 128 / kUnits;
+        const bool there = u * 8 < a.d;
+        uint8_t *to = sm.kv[stage][u >> 3];
+        uint2 w[kUnits];
+#pragma unroll
+        for (int i = 0; i < kUnits; i++) {
+          const int64_t at = in.row[r0 + i * kStep];
+          w[i] = there && at >= 0 ? *reinterpret_cast<const uint2 *>(pool + at + u * 8) : make_uint2(0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kUnits; i++) {
+          const int r = r0 + i * kStep;
+          *reinterpret_cast<uint4 *>(to + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = operands_of<FMT>(w[i]);
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&sm.kv_full[stage]);
+        if (++stage == kStages) stage = 0, kv_phase ^= 1;
+      };
+      for (;;) {
+        if (!(ok = bar_wait(&sm.todo_full[turn], todo_phase, &sm.dead))) break;
+        const int n = sm.todo[turn].n, ahead = sm.todo[turn].split ? 2 : 1;
+        __syncwarp();
+        if (lane == 0) bar_arrive(&sm.todo_empty[turn]);
+        turn ^= 1;
+        if (turn == 0) todo_phase ^= 1;
+        if (n < 0) break;
+        for (int i = 0; i < n + ahead && ok; i++) {
+          if (i >= ahead) {
+            fill(a.vp, v_slot, v_phase);
+            if (++v_slot == kInfo) v_slot = 0, v_phase ^= 1;
+          }
+          if (ok && i < n) {
+            fill(a.kp, k_slot, k_phase);
+            if (++k_slot == kInfo) k_slot = 0, k_phase ^= 1;
+          }
+        }
+        if (!ok) break;
+      }
+    } else {
+      // ---- softmax: a row a thread ----
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+      const int t = warp >> 2, r = threadIdx.x & (kTile - 1);
+      const uint32_t lanes = uint32_t(warp & 3) << 21;  // the warp's lanes of TMEM
+      const uint32_t s_at = tmem + lanes + t * kTile, o_at = tmem + lanes + 2 * kTile + t * kTile;
+      uint32_t s_phase = 0, o_phase = 0, todo_phase = 0, q_phase = 1, info_phase = 0, ml_phase = 0;
+      int turn = 0, slot = 0;
+      bool ok = true;
+      for (;;) {
+        if (!(ok = bar_wait(&sm.todo_full[turn], todo_phase, &sm.dead))) break;
+        const Todo &todo = sm.todo[turn];
+        const int n = todo.n;
+        const bool split = todo.split;
+        if (n < 0) break;
+        // the query row
+        const int row = todo.row0 + (split ? 0 : t * kTile) + r;
+        const int b = row < todo.rows ? a.seq[todo.e0 + row / a.TG] : -1;
+        const int tok = row % a.TG / a.G, head = todo.head * a.G + row % a.G;  // TG is a multiple of G
+        float sc = a.scale_log2;
+        {
+          const uint16_t *src = a.q + b * a.q_seq + tok * a.q_tok + head * a.q_head;
+          uint4 w[D / 8];
+#pragma unroll
+          for (int c = 0; c < D / 8; c++) w[c] = b >= 0 && c * 8 < a.d ? *reinterpret_cast<const uint4 *>(src + c * 8) : make_uint4(0, 0, 0, 0);
+          if (a.bf16) {  // to f16, raised to its top: off by at most 2^-39 of the row's largest
+            uint32_t top = 0;
+#pragma unroll
+            for (int c = 0; c < D / 8; c++) {
+              const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+              for (int k = 0; k < 4; k++) top = max(top, max(x[k] << 16 & 0x7fff0000u, x[k] & 0x7fff0000u));
+            }
+            const int f = min(253, max(1, 268 - int(top >> 23)));
+            const float up = __int_as_float(f << 23);
+            sc *= __int_as_float((254 - f) << 23);
+#pragma unroll
+            for (int c = 0; c < D / 8; c++) {
+              uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+              for (int k = 0; k < 4; k++)
+                x[k] = pack<false>(__uint_as_float(x[k] << 16) * up, __uint_as_float(x[k] & 0xffff0000u) * up);
+              w[c] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          }
+          if (!(ok = bar_wait(&sm.q_empty, q_phase, &sm.dead))) break;
+          q_phase ^= 1;
+          if (!split || t == 0) {
+#pragma unroll
+            for (int c = 0; c < D / 8; c++) *reinterpret_cast<uint4 *>(sm.q[t][c >> 3] + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = w[c];
+            fence_async();
+          }
+          __syncwarp();
+          if (lane == 0) bar_arrive(&sm.q_full);
+        }
+        float m = -INFINITY;
+        float2 l = make_float2(0.0f, 0.0f);
+        int v_exp = 1;  // O is in units of 2^(v_exp - 127), the largest V scale so far
+        int done = 0;   // tiles of this thread's
+        for (int j = 0; j < n; j++) {
+          const Info &in = sm.info[slot];
+          const uint32_t full = info_phase;
+          uint64_t *const info_full = &sm.info_full[slot];
+          if (++slot == kInfo) slot = 0, info_phase ^= 1;
+          if (split && t != (j & 1)) continue;
+          if (!(ok = bar_wait(info_full, full, &sm.dead))) break;
+          if (!(ok = bar_wait(&sm.s_full[t], s_phase, &sm.dead))) break;
+          s_phase ^= 1;
+          tm_after();
+          uint32_t x[kTile];
+#pragma unroll
+          for (int i = 0; i < 4; i++) tm_load(s_at + 32 * i, x + 32 * i);
+          tm_wait_ld();
+          // What turns a product into a score: a page's scale times the row's.  It is
+          // not 0, so that what is masked stays at -inf (a page's codes are 0 where its scale is).
+          float f[PLAIN ? kTile / 16 : 1];
+          if (PLAIN) {
+#pragma unroll
+            for (int i = 0; i < kTile / 16; i++) f[i] = fmaxf(in.ks[16 * i] * sc, 0x1p-126f);
+          } else {
+            f[0] = 1.0f;
+#pragma unroll
+            for (int i = 0; i < kTile; i += 2) {
+              const float2 k2 = *reinterpret_cast<const float2 *>(&in.ks[i]);
+              const float2 y = mul2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), make_float2(k2.x * sc, k2.y * sc));
+              x[i] = __float_as_uint(y.x), x[i + 1] = __float_as_uint(y.y);
+            }
+          }
+          if (!in.whole) {
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+              const uint32_t valid = in.valid[k];
+#pragma unroll
+              for (int i = 0; i < 32; i++)
+                if (!(valid >> i & 1)) x[32 * k + i] = 0xff800000u;
+            }
+          }
+          float now = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < kTile / 16; i++) {
+            float top[2] = {fmaxf(__uint_as_float(x[16 * i]), __uint_as_float(x[16 * i + 1])), fmaxf(__uint_as_float(x[16 * i + 2]), __uint_as_float(x[16 * i + 3]))};
+#pragma unroll
+            for (int k = 4; k < 16; k += 4) {
+              top[0] = max3(top[0], __uint_as_float(x[16 * i + k]), __uint_as_float(x[16 * i + k + 1]));
+              top[1] = max3(top[1], __uint_as_float(x[16 * i + k + 2]), __uint_as_float(x[16 * i + k + 3]));
+            }
+            now = fmaxf(now, fmaxf(top[0], top[1]) * f[PLAIN ? i : 0]);
+          }
+          const bool moved = now > m + kLag;
+          const float keep = moved ? ex2(m - now) : 1.0f;
+          if (moved) m = now;
+          float scale_o = keep;
+          const int e = in.v_exp;
+          if (e > v_exp) {  // the same in every thread
+            scale_o *= e - v_exp > 126 ? 0.0f : __int_as_float((127 + v_exp - e) << 23);
+            v_exp = e;
+          }
+          if (done > 0 && __any_sync(0xffffffffu, scale_o != 1.0f)) {
+            l = mul2(l, make_float2(keep, keep));
+#pragma unroll
+            for (int c = 0; c < D / 32; c++) {
+              uint32_t y[32];
+              tm_load(o_at + 32 * c, y);
+              tm_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; i++) y[i] = __float_as_uint(__uint_as_float(y[i]) * scale_o);
+              tm_store32(o_at + 32 * c, y);
+            }
+          }
+          done++;
+          const float base = kLift - (m == -INFINITY ? 0.0f : m), unit = __int_as_float((254 - v_exp) << 23);
+          float2 sums[4] = {};
+#pragma unroll
+          for (int c = 0; c < 4; c++) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+              const int at = 32 * c + 2 * i;
+              float2 y = make_float2(__uint_as_float(x[at]), __uint_as_float(x[at + 1]));
+              if (PLAIN)
+                y = fma2(y, make_float2(f[PLAIN ? at / 16 : 0], f[PLAIN ? at / 16 : 0]), make_float2(base, base));
+              else
+                y = add2(y, make_float2(base, base));
+              y = make_float2(ex2(y.x), ex2(y.y));
+              sums[i & 3] = add2(sums[i & 3], y);
+              if (PLAIN) {
+                const float v = in.vs[at & ~15] * unit;
+                y = mul2(y, make_float2(v, v));
+              } else {
+                const float2 v2 = *reinterpret_cast<const float2 *>(&in.vs[at]);
+                y = mul2(y, make_float2(v2.x * unit, v2.y * unit));
+              }
+              pk[i] = pack<false>(y.x, y.y);
+            }
+            tm_store16(s_at + 16 * c, pk);
+            if (c & 1) {  // half of P is there
+              tm_wait_st();
+              tm_before();
+              __syncwarp();
+              if (lane == 0) bar_arrive(&sm.p_full[t][c >> 1]);
+            }
+          }
+          l = add2(l, add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
+        }
+        if (!ok) break;
+        float sum = l.x + l.y;
+        if (done > 0) {
+          if (!(ok = bar_wait(&sm.o_full[t], o_phase, &sm.dead))) break;
+          o_phase ^= 1;
+          tm_after();
+        }
+        const int slot_out = todo.slot;
+        const bool whole = slot_out < 0;
+        float f_mine = __int_as_float(v_exp << 23), f_other = 0.0f;
+        if (split && t == 1) {  // hands over to a
+          sm.ml[r][0] = m, sm.ml[r][1] = sum;
+          if (r == 0) sm.ml_exp = v_exp;
+          tm_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&sm.ml_full), bar_arrive(&sm.todo_empty[turn]);
+          if (!(ok = bar_wait(&sm.ml_empty, ml_phase, &sm.dead))) break;
+          ml_phase ^= 1;
+        } else {
+          bool both = false;
+          if (split) {
+            if (!(ok = bar_wait(&sm.ml_full, ml_phase, &sm.dead))) break;
+            ml_phase ^= 1;
+            tm_after();
+            const float mb = sm.ml[r][0], lb = sm.ml[r][1], top = fmaxf(m, mb);
+            both = n > 1;
+            const float ka = m == -INFINITY ? 0.0f : ex2(m - top), kb = mb == -INFINITY ? 0.0f : ex2(mb - top);
+            f_mine *= ka;
+            f_other = kb * __int_as_float(sm.ml_exp << 23);
+            sum = sum * ka + lb * kb;
+            m = top;
+          }
+          const int64_t at = (int64_t(b) * a.T + tok) * a.Hq + head;
+          float f_own = 0.0f, total_l = sum, top = m;
+          if (whole) {  // with what the sequence has to itself
+            status_cleared();
+            if (b >= 0) {
+              const float mo = __ldcg(&a.own_ml[2 * at]), lo_ = __ldcg(&a.own_ml[2 * at + 1]);
+              top = fmaxf(m, mo);
+              const float kp = m == -INFINITY ? 0.0f : ex2(m - top);
+              f_own = mo == -INFINITY ? 0.0f : ex2(mo - top);
+              f_mine *= kp, f_other *= kp;
+              total_l = sum * kp + lo_ * f_own;
+            }
+          }
+          const float turn_l = total_l == 0.0f ? 0.0f : 1.0f / total_l;
+          float *part = a.parts + int64_t(slot_out) * kRows * (D + 2);
+#pragma unroll
+          for (int c = 0; c < D / 32; c++) {
+            uint32_t y[32];
+            tm_load(o_at + 32 * c, y);
+            tm_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; i++) y[i] = __float_as_uint(__uint_as_float(y[i]) * f_mine);
+            if (both) {
+              uint32_t z[32];
+              tm_load(o_at + kTile + 32 * c, z);
+              tm_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; i++) y[i] = __float_as_uint(__uint_as_float(y[i]) + __uint_as_float(z[i]) * f_other);
+            }
+            if (whole) {
+              if (b >= 0) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                  if (32 * c + i >= a.d) continue;
+                  float o[8];
+#pragma unroll
+                  for (int k = 0; k < 8; k++) o[k] = __uint_as_float(y[i + k]);
+                  if (f_own != 0.0f) {
+                    const float4 u0 = __ldcg(reinterpret_cast<const float4 *>(a.own + at * a.d + 32 * c + i));
+                    const float4 u1 = __ldcg(reinterpret_cast<const float4 *>(a.own + at * a.d + 32 * c + i + 4));
+                    o[0] += f_own * u0.x, o[1] += f_own * u0.y, o[2] += f_own * u0.z, o[3] += f_own * u0.w;
+                    o[4] += f_own * u1.x, o[5] += f_own * u1.y, o[6] += f_own * u1.z, o[7] += f_own * u1.w;
+                  }
+                  uint32_t w4[4];
+#pragma unroll
+                  for (int k = 0; k < 4; k++)
+                    w4[k] = a.bf16 ? pack<true>(o[2 * k] * turn_l, o[2 * k + 1] * turn_l) : pack<false>(o[2 * k] * turn_l, o[2 * k + 1] * turn_l);
+                  *reinterpret_cast<uint4 *>(a.out + at * a.d + 32 * c + i) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                }
+              }
+            } else if (b >= 0) {  // four channels of 32 rows lie together
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<uint4 *>(part + ((8 * c + i / 4) * kRows + t * kTile + r) * 4) = make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+            }
+          }
+          tm_before();
+          if (b >= 0) {
+            if (!whole)
+              part[kRows * D + t * kTile + r] = m, part[kRows * (D + 1) + t * kTile + r] = sum;
+            else if (a.lse)
+              a.lse[at] = total_l == 0.0f ? -INFINITY : (top - kLift + log2f(total_l)) * 0.6931471805599453f;
+          }
+          __syncwarp();
+          if (lane == 0) {
+            if (split) bar_arrive(&sm.ml_empty);
+            bar_arrive(&sm.todo_empty[turn]);
+          }
+        }
+        turn ^= 1;
+        if (turn == 0) todo_phase ^= 1;
+      }
+    }
+  }
+  __syncwarp();
+  tm_before();
+  __syncthreads();
+  tm_after();
+  if (sm.dead)  // what is in flight gets a moment to land
+    for (int i = 0; i < 1000; i++) __nanosleep(1000);
+  if (warp == 15) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  if (threadIdx.x == 0) a.notes[blockIdx.x].errors = sm.errors | (sm.dead ? kStTimeout : 0);
+  status_cleared();  // the join that waits for this kernel reads what the ones before it have written
+}
+
+// Joins the parts of items that several CTAs had, with what each sequence has
+// to itself: eight rows a CTA, four channels a thread.
+template <int D>
+__global__ void __launch_bounds__(2 * D, 2048 / (2 * D)) k_shared_join(const __grid_constant__ SharedArgs a) {
+  status_cleared();
+  if (blockIdx.x == 0 && blockIdx.y == 0) {  // the status of the call, with that of the kernels before
+    __shared__ uint32_t s_errors;
+    if (threadIdx.x == 0) s_errors = *a.bad;
+    __syncthreads();
+    uint32_t e = 0;
+    for (int i = threadIdx.x; i < int(gridDim.x); i += 2 * D) e |= __ldcg(&a.notes[i].errors);
+    if (e) atomicOr(&s_errors, e);
+    __syncthreads();
+    if (threadIdx.x == 0 && s_errors) atomicOr(a.status, s_errors);
+  }
+  const Note note = a.notes[blockIdx.x];
+  if (note.parts == 0) return;
+  const int r = blockIdx.y * 8 + threadIdx.x % 8, c = threadIdx.x / 8, e0 = a.cu[note.g], row = note.q * kRows + r;
+  if (row >= (a.cu[note.g + 1] - e0) * a.TG) return;
+  const int b = a.seq[e0 + row / a.TG];
+  if (b < 0) return;
+  const int64_t at = (int64_t(b) * a.T + row % a.TG / a.G) * a.Hq + note.h * a.G + row % a.G;
+  auto part = [&](int i) { return a.parts + (2 * (int64_t(blockIdx.x) + i) + (i == 0 ? note.second : 0)) * kRows * (D + 2); };
+  float top = __ldcg(&a.own_ml[2 * at]), sum = __ldcg(&a.own_ml[2 * at + 1]), y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (top != -INFINITY && c * 4 < a.d) {
+    const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.own + at * a.d + c * 4));
+    y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
+  }
+  for (int base = 0; base < note.parts; base += 2) {
+    float m[2], l[2], now = top;
+    float4 v[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+      if (base + i < note.parts) {
+        const float *p = part(base + i);
+        m[i] = __ldcg(p + kRows * D + r), l[i] = __ldcg(p + kRows * (D + 1) + r);
+        v[i] = __ldcg(reinterpret_cast<const float4 *>(p) + c * kRows + r);
+        now = fmaxf(now, m[i]);
+      }
+    const float keep = top == -INFINITY ? 0.0f : ex2(top - now);
+    top = now;
+    sum *= keep;
+#pragma unroll
+    for (int k = 0; k < 4; k++) y[k] *= keep;
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+      if (base + i < note.parts) {
+        const float w = m[i] == -INFINITY ? 0.0f : ex2(m[i] - now);
+        sum += w * l[i];
+        y[0] += w * v[i].x, y[1] += w * v[i].y, y[2] += w * v[i].z, y[3] += w * v[i].w;
+      }
+  }
+  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+  if (c * 4 < a.d) {
+    const uint2 w = a.bf16 ? make_uint2(pack<true>(y[0] * f, y[1] * f), pack<true>(y[2] * f, y[3] * f))
+                           : make_uint2(pack<false>(y[0] * f, y[1] * f), pack<false>(y[2] * f, y[3] * f));
+    *reinterpret_cast<uint2 *>(a.out + at * a.d + c * 4) = w;
+  }
+  if (c == 0 && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (top - kLift + log2f(sum)) * 0.6931471805599453f;
+}
+
+bool groups_ok(const cg_cache *c, const cg_attend *t, const cg_groups *g) {
+  return attend_args_ok(c, t) && g && g->n_groups >= 0 && g->n_groups <= (1 << 20) && g->n_members >= 0 && g->n_members <= (1 << 20) &&
+         int64_t(g->n_members) * t->q_tokens * (t->Hq / c->H) <= (1 << 30);
+}
+
+int padded(int d) { return d <= 64 ? 64 : 128; }
+
+struct Places {
+  uint64_t bad, owner, first, seq, keys, lead, own, own_ml, notes, parts, bytes;
+};
+
+Places places(const cg_cache *c, const cg_attend *t, const cg_groups *g) {
+  Places w{};
+  const uint64_t rows = uint64_t(t->n_seq) * t->q_tokens * t->Hq;
+  w.bad = attend_own_bytes(c, t);
+  w.bad = pad256(w.bad);
+  w.owner = w.bad + 256;
+  w.first = w.owner + pad256(4 * uint64_t(t->n_seq));
+  w.seq = w.first + pad256(4 * uint64_t(t->n_seq));
+  w.keys = w.seq + pad256(4 * uint64_t(g->n_members));
+  w.lead = w.keys + pad256(4 * uint64_t(g->n_groups));
+  w.own = w.lead + pad256(4 * uint64_t(g->n_groups));
+  w.own_ml = w.own + pad256(4 * rows * c->d);
+  w.notes = w.own_ml + pad256(8 * rows);
+  w.parts = w.notes + pad256(sizeof(Note) * kGrid);
+  w.bytes = w.parts + 4 * uint64_t(2 * kGrid) * kRows * (padded(c->d) + 2);
+  return w;
+}
+
+template <int FMT, int D, bool PLAIN>
+cudaError_t launch(const SharedArgs &a, cudaStream_t st) {
+  constexpr int kSmem = int(sizeof(Smem<D>));
+  static_assert(kSmem <= 227 * 1024, "fits in an SM");
+  const cudaError_t e = cudaFuncSetAttribute(k_shared<FMT, D, PLAIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  const cudaError_t e2 = launch_early(k_shared<FMT, D, PLAIN>, dim3(kGrid), dim3(kThreads), kSmem, st, a);
+  if (e2 != cudaSuccess) return e2;
+  const cudaError_t e3 = launch_early(k_shared_join<D>, dim3(kGrid, kRows / 8), dim3(2 * D), 0, st, a);
+  return e3 != cudaSuccess ? e3 : cudaGetLastError();
+}
+
+template <int FMT>
+cudaError_t launch_format(const SharedArgs &a, cudaStream_t st) {
+  const bool plain = a.bt % 16 == 0;
+  if (a.d <= 64) return plain ? launch<FMT, 64, true>(a, st) : launch<FMT, 64, false>(a, st);
+  return plain ? launch<FMT, 128, true>(a, st) : launch<FMT, 128, false>(a, st);
+}
+
+}  // namespace
+}  // namespace cg
+
+extern "C" size_t cg_shared_workspace_bytes(const cg_cache *cache, const cg_attend *attend, const cg_groups *groups) {
+  using namespace cg;
+  if (!groups_ok(cache, attend, groups)) return 0;
+  return size_t(places(cache, attend, groups).bytes);
+}
+
+extern "C" cg_status cg_shared_attend(const cg_cache *cache, const cg_attend *attend, const cg_groups *groups, const void *q_dev,
+                                      const void *k_pool, const void *v_pool, const float *k_scale, const float *v_scale,
+                                      const int32_t *table_dev, const int32_t *len_dev, void *out_dev, float *lse_dev,
+                                      void *ws_dev, size_t ws_bytes, void *stream) {
+  using namespace cg;
+  if (!groups_ok(cache, attend, groups) || !q_dev || !k_pool || !v_pool || !k_scale || !v_scale || !table_dev || !len_dev || !out_dev || !ws_dev)
+    return CG_ERR_INVALID_ARG;
+  // groups without entries may be NULL
+  if ((groups->n_groups > 0 && (!groups->cu_group_dev || !groups->shared_dev)) || (groups->n_members > 0 && !groups->member_dev))
+    return CG_ERR_INVALID_ARG;
+  if (!is_aligned(q_dev, 16) || !is_aligned(k_pool, 16) || !is_aligned(v_pool, 16) || !is_aligned(out_dev, 16) || !is_aligned(k_scale, 4) ||
+      !is_aligned(v_scale, 4) || !is_aligned(table_dev, 4) || !is_aligned(len_dev, 4) || !is_aligned(lse_dev, 4) || !is_aligned(ws_dev, 256) ||
+      !is_aligned(groups->cu_group_dev, 4) || !is_aligned(groups->member_dev, 4) || !is_aligned(groups->shared_dev, 4))
+    return CG_ERR_INVALID_ARG;
+  const Places w = places(cache, attend, groups);
+  if (ws_bytes < w.bytes) return CG_ERR_INVALID_ARG;
+  if (groups->n_groups == 0 || groups->n_members == 0)
+    return cg_cache_attend(cache, attend, q_dev, k_pool, v_pool, k_scale, v_scale, table_dev, len_dev, out_dev, lse_dev, ws_dev, ws_bytes, stream);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t *ws = static_cast<uint8_t *>(ws_dev);
+  SharedArgs a{};
+  a.q = static_cast<const uint16_t *>(q_dev);
+  a.kp = static_cast<const uint8_t *>(k_pool), a.vp = static_cast<const uint8_t *>(v_pool);
+  a.ks = k_scale, a.vs = v_scale, a.table = table_dev, a.len = len_dev;
+  a.out = static_cast<uint16_t *>(out_dev), a.lse = lse_dev;
+  a.cu = groups->cu_group_dev, a.member = groups->member_dev, a.shared = groups->shared_dev;
+  a.status = reinterpret_cast<uint32_t *>(ws), a.bad = reinterpret_cast<uint32_t *>(ws + w.bad);
+  a.owner = reinterpret_cast<int32_t *>(ws + w.owner), a.first = reinterpret_cast<int32_t *>(ws + w.first);
+  a.seq = reinterpret_cast<int32_t *>(ws + w.seq), a.keys = reinterpret_cast<int32_t *>(ws + w.keys);
+  a.lead = reinterpret_cast<int32_t *>(ws + w.lead);
+  a.own = reinterpret_cast<float *>(ws + w.own), a.own_ml = reinterpret_cast<float *>(ws + w.own_ml);
+  a.notes = reinterpret_cast<Note *>(ws + w.notes), a.parts = reinterpret_cast<float *>(ws + w.parts);
+  a.q_seq = attend->q_stride[0], a.q_tok = attend->q_stride[1], a.q_head = attend->q_stride[2];
+  a.n_groups = groups->n_groups, a.n_members = groups->n_members;
+  a.B = attend->n_seq, a.T = attend->q_tokens, a.Hq = attend->Hq, a.H = cache->H, a.G = a.Hq / a.H, a.TG = a.T * a.G, a.d = cache->d;
+  a.bt = cache->block_tokens, a.n_blocks = cache->n_blocks, a.stride = attend->table_stride;
+  a.scale_log2 = attend->scale * 1.4426950408889634f;
+  a.bf16 = attend->dtype == CG_BF16;
+  k_shared_plan<<<1, kPlan, 0, st>>>(a);
+  const cg_status rc = attend_own(cache, attend, a.first, a.own, a.own_ml, q_dev, k_pool, v_pool, k_scale, v_scale, table_dev, len_dev, out_dev,
+                                  lse_dev, ws, st);
+  if (rc != CG_OK) return rc;
+  const cudaError_t e = cache->format == CG_CACHE_E4M3 ? launch_format<CG_CACHE_E4M3>(a, st) : launch_format<CG_CACHE_INT8>(a, st);
+  return e == cudaSuccess ? CG_OK : CG_ERR_CUDA;
+}

@@ -1,4 +1,4 @@
-"""Slots, groups and cross attention refuse bad arguments at once, before any CUDA call (no GPU)."""
+"""Slots, groups, shared prefixes and cross attention refuse bad arguments at once, before any CUDA call (no GPU)."""
 import ctypes
 
 import pytest
@@ -88,3 +88,47 @@ def test_cross_refuses(lib):
         assert refused(call(prompt(), **{name: FAKE + 2})), name
     assert refused(call(prompt(), lse=FAKE + 1))
     assert refused(call(prompt(), nb=cg.cg_prompt_workspace_bytes(prompt()) - 1))
+
+
+def test_shared_refuses(lib):
+    att = lambda **kw: cg.Attend(**{**dict(n_seq=6, q_tokens=1, Hq=8, dtype=0, table_stride=4, scale=0.1), **kw})  # noqa: E731
+    ok = cg.cg_groups(2, 6, FAKE, FAKE, FAKE)
+
+    def call(c=cache(), t=None, g=ok, **kw):
+        t = att() if t is None else t
+        a = {**dict(q=FAKE, kp=FAKE, vp=FAKE, ks=FAKE, vs=FAKE, table=FAKE, len=FAKE, out=FAKE, lse=FAKE, ws=FAKE, nb=BIG), **kw}
+        return lib.cg_shared_attend(c.ref, t.for_cache(c), ref(g), a["q"], a["kp"], a["vp"], a["ks"], a["vs"], a["table"], a["len"], a["out"], a["lse"],
+                                    a["ws"], a["nb"], None)
+
+    size = lambda c, t, g: lib.cg_shared_workspace_bytes(c.ref, t.for_cache(c), ref(g))  # noqa: E731
+    nan, inf = float("nan"), float("inf")
+    assert lib.cg_shared_workspace_bytes(None, None, None) == 0
+    for kw in BAD_CACHES + [dict(format=cg.CG_CACHE_F16)]:
+        assert refused(call(c=cache(**kw))) and size(cache(**kw), att(), ok) == 0, kw
+    for kw in (dict(n_seq=0), dict(q_tokens=0), dict(Hq=0), dict(Hq=6), dict(dtype=-1), dict(table_stride=0), dict(scale=0.0), dict(scale=-1.0),
+               dict(scale=nan), dict(scale=inf), dict(q_stride=(1024, 1024, 100)), dict(q_stride=(1, 1024, 128)), dict(table_stride=(1 << 26) + 1)):
+        assert refused(call(t=att(**kw))) and size(cache(), att(**kw), ok) == 0, kw
+    for g in (None, cg.cg_groups(-1, 6, FAKE, FAKE, FAKE), cg.cg_groups(2, -1, FAKE, FAKE, FAKE), cg.cg_groups((1 << 20) + 1, 6, FAKE, FAKE, FAKE),
+              cg.cg_groups(2, (1 << 20) + 1, FAKE, FAKE, FAKE)):
+        assert refused(call(g=g)) and size(cache(), att(), g) == 0
+    assert refused(call(t=att(n_seq=1, q_tokens=1 << 14), g=cg.cg_groups(1, 1 << 17, FAKE, FAKE, FAKE))), "more rows than are counted"
+    for bad in (None, FAKE + 2):
+        for i in range(3):
+            p = [FAKE] * 3
+            p[i] = bad
+            assert refused(call(g=cg.cg_groups(2, 6, *p)))
+    for name in ("q", "kp", "vp", "ks", "vs", "table", "len", "out", "ws"):
+        assert refused(call(**{name: None})) and refused(call(**{name: FAKE + 2})), name
+    assert refused(call(lse=FAKE + 1))
+    some, t = cache(), att()
+    need = size(some, t, ok)
+    assert lib.cg_cache_workspace_bytes(some.ref, t.for_cache(some)) < need < 1 << 28
+    assert refused(call(c=some, t=t, nb=need - 1)) and refused(call(c=some, t=t, ws=FAKE + 128))
+
+
+def test_offsets_and_groups_have_their_lengths():
+    import torch
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32)  # noqa: E731
+    for n, m in ((3, 3), (3, 1), (1, 1), (2, 0)):
+        with pytest.raises(ValueError, match="offsets"):
+            cg.Groups(i32(n), i32(4), i32(m))
