@@ -20,8 +20,12 @@
 // the products; where an item has up to 128 rows, a and b are the same rows
 // and take the even and the odd tiles of positions.  Warps: 0-3 and 4-7 the
 // softmax of a and b, one row a thread; 8-11 turn codes into operands in shared
-// memory; 12-14 look up pages and scales, a tile each in turns; 15 issues the
-// products.
+// memory; 12 and 13 look up pages and scales, a tile each in turns; 14 has the
+// codes copied; 15 issues the products.
+//
+//   operands:  K(0) | K(1) V(0) | K(2) V(1) | ...
+//   products:  S_a(0) S_b(0) | PV_a(j) S_a(j+1) PV_b(j) S_b(j+1) | ...
+//   a = b:     S_a(0) | S_b(1) PV_a(0) | S_a(2) PV_b(1) | ...
 #include "cg_shared.cuh"
 
 #include "cg_cache.cuh"
@@ -37,9 +41,10 @@ constexpr int kSoftRegs = 176, kConvRegs = 88, kOtherRegs = 72;
 constexpr int kTile = 128;  // rows of a tile, positions of a tile
 constexpr int kRows = 2 * kTile;
 constexpr int kGrid = kSMs;
-constexpr int kStages = 4;   // operand tiles of K or V
+constexpr int kStages = 3;   // operand tiles of K or V
+constexpr int kRaw = 4;      // tiles of codes
 constexpr int kInfo = 6;     // tiles whose pages and scales are known
-constexpr int kLookers = 3;  // warps that look them up
+constexpr int kLookers = 2;  // warps that look them up
 constexpr int kPlan = 1024;
 // p = 2^(s - m + kLift) < 2^15, m at most kLag under the maximum: as in the kernels whose parts are joined with these
 constexpr float kLift = 12.0f, kLag = 3.0f;
@@ -69,15 +74,17 @@ struct SharedArgs {
   Note *notes;
   float *parts;  // [2 * kGrid][kRows][D + 2]
   int64_t q_seq, q_tok, q_head;
-  int n_groups, n_members, B, T, Hq, H, G, TG, d, bt, n_blocks, stride;  // TG: rows of a sequence and KV head
+  int n_groups, n_members, B, T, Hq, H, G, TG, d, bt, n_blocks, stride, chunk;  // TG: rows of a sequence and KV head; chunk: positions copied at a time
   float scale_log2;  // scale * log2(e)
   bool bf16;
 };
 
-// Pages and scales of a tile of positions.
+// Pages and scales of a tile of positions, for each 16 of them (RAW) or each one.
+template <bool RAW>
 struct Info {
-  int64_t row[kTile];  // where a position's codes begin, or -1
-  float ks[kTile], vs[kTile];
+  static constexpr int kEach = RAW ? 16 : 1, kCount = kTile / kEach;
+  int64_t row[kCount];  // where a position's codes begin, or -1
+  float ks[kCount], vs[kCount];
   uint32_t valid[4];
   int v_exp, whole;
 };
@@ -89,15 +96,16 @@ struct Todo {
   int head, slot;    // KV head; slot of the workspace, or -1: the item is whole
 };
 
-template <int D>
+template <int D, bool RAW>
 struct Smem {
   static constexpr int kChunks = D / 64;  // of 64 channels: 128 bytes, a swizzled row
   uint8_t q[2][kChunks][kTile * 128];
   uint8_t kv[kStages][kChunks][kTile * 128];
-  Info info[kInfo];
+  uint8_t raw[RAW ? kRaw : 1][RAW ? kTile * D : 16];
+  Info<RAW> info[kInfo];
   float ml[kTile][2];  // split: b's maximum and sum, for a
   int ml_exp;
-  uint64_t todo_full[2], todo_empty[2], info_full[kInfo], info_empty[kInfo], q_full, q_empty, kv_full[kStages], kv_empty[kStages], s_full[2],
+  uint64_t todo_full[2], todo_empty[2], info_full[kInfo], info_empty[kInfo], q_full, q_empty, kv_full[kStages], kv_empty[kStages], raw_full[kRaw], raw_empty[kRaw], s_full[2],
       p_full[2][2], o_full[2], ml_full, ml_empty;
   Todo todo[2];
   uint32_t tmem, errors, dead;
@@ -246,12 +254,22 @@ __device__ inline uint4 operands_of(uint2 w) {  // eight codes
   return make_uint4(halves_of<FMT, 0>(w.x), halves_of<FMT, 1>(w.x), halves_of<FMT, 0>(w.y), halves_of<FMT, 1>(w.y));
 }
 
-// PLAIN: pages are a multiple of 16 tokens, so that 16 positions have one scale.
-template <int FMT, int D, bool PLAIN>
+// Copies `bytes`, a multiple of 16, to shared memory.
+__device__ inline void copy_bulk(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
+               "r"(smem_of(bar))
+               : "memory");
+}
+
+// RAW: pages are a multiple of 16 tokens, so that 16 positions have one scale,
+// and rows have D channels: codes are copied, `chunk` positions (a power of two
+// up to 128 that divides a page) at a time.  Other shapes load them a position
+// and eight channels at a time.
+template <int FMT, int D, bool RAW>
 __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ SharedArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  Smem<D> &sm = *reinterpret_cast<Smem<D> *>(smem_raw);
-  constexpr int kChunks = Smem<D>::kChunks;
+  Smem<D, RAW> &sm = *reinterpret_cast<Smem<D, RAW> *>(smem_raw);
+  constexpr int kChunks = Smem<D, RAW>::kChunks;
   constexpr uint32_t kTileBytes = kChunks * kTile * 128;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -260,9 +278,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
     sm.errors = sm.dead = 0;
     a.notes[blockIdx.x].parts = 0;
     bar_init(&sm.q_full, 8), bar_init(&sm.q_empty, 1);
-    for (int i = 0; i < 2; i++) bar_init(&sm.todo_full[i], 1), bar_init(&sm.todo_empty[i], 13);  // 13 warps read it
+    for (int i = 0; i < 2; i++) bar_init(&sm.todo_full[i], 1), bar_init(&sm.todo_empty[i], 14);  // 14 warps read it
     for (int i = 0; i < kInfo; i++) bar_init(&sm.info_full[i], 1), bar_init(&sm.info_empty[i], 1);
     for (int i = 0; i < kStages; i++) bar_init(&sm.kv_full[i], 4), bar_init(&sm.kv_empty[i], 1);
+    for (int i = 0; i < kRaw; i++) bar_init(&sm.raw_full[i], 1), bar_init(&sm.raw_empty[i], 4);
     for (int t = 0; t < 2; t++) bar_init(&sm.s_full[t], 1), bar_init(&sm.p_full[t][0], 4), bar_init(&sm.p_full[t][1], 4), bar_init(&sm.o_full[t], 1);
     bar_init(&sm.ml_full, 4), bar_init(&sm.ml_empty, 4);
     bar_init_fence();
@@ -366,35 +385,50 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
           if (!more) break;
           const int keys = a.keys[p.g];
           const int32_t *row = a.table + int64_t(a.seq[a.lead[p.g]]) * a.stride;
+          constexpr int kEach = Info<RAW>::kEach, kCount = Info<RAW>::kCount, kMine = (kCount + 31) / 32;
+          int page[kMine], at[kMine];  // of the warp's next tile
+          auto look = [&](int j) {
+#pragma unroll
+            for (int k = 0; k < kMine; k++) {
+              const int i = 32 * k + lane, tok = (p.j0 + j) * kTile + i * kEach, blk = tok / a.bt;
+              const bool there = i < kCount && tok < keys;
+              at[k] = there ? tok - blk * a.bt : -1;
+              page[k] = there ? row[blk] : -1;
+            }
+          };
+          int mine = warp - 12 - who;
+          if (mine < 0) mine += kLookers;
+          if (mine < p.n) look(mine);
           for (int j = 0; j < p.n; j++) {
-            if (who == warp - 12) {
-              if (!(ok = bar_wait(&sm.info_empty[slot], phase, &sm.dead))) break;
-              Info &in = sm.info[slot];
-              int page[4], at[4];
+            if (j == mine) {
+              float ks[kMine], vs[kMine], top = 0.0f;
+              int64_t begin[kMine];
+              bool good[kMine];
 #pragma unroll
-              for (int k = 0; k < 4; k++) {
-                const int tok = (p.j0 + j) * kTile + 32 * k + lane, blk = tok / a.bt;
-                at[k] = tok < keys ? tok - blk * a.bt : -1;
-                page[k] = tok < keys ? row[blk] : -1;
-              }
-              float ks[4], vs[4], top = 0.0f;
-              bool good[4];
-#pragma unroll
-              for (int k = 0; k < 4; k++) {
+              for (int k = 0; k < kMine; k++) {
                 good[k] = uint32_t(page[k]) < uint32_t(a.n_blocks);
                 if (at[k] >= 0 && !good[k]) atomicOr(&sm.errors, kStBadArg);
                 const int64_t sc = good[k] ? int64_t(page[k]) * a.H + p.h : 0;
                 ks[k] = good[k] ? a.ks[sc] : 0.0f, vs[k] = good[k] ? a.vs[sc] : 0.0f;
+                begin[k] = good[k] ? page_row(page[k], a.H, p.h, a.bt, at[k], a.d) : -1;
               }
+              mine += kLookers;
+              if (mine < p.n) look(mine);
+              if (!(ok = bar_wait(&sm.info_empty[slot], phase, &sm.dead))) break;
+              Info<RAW> &in = sm.info[slot];
               int whole = 1;
 #pragma unroll
-              for (int k = 0; k < 4; k++) {
+              for (int k = 0; k < kMine; k++) {
+                const int i = 32 * k + lane;
                 const uint32_t valid = __ballot_sync(0xffffffffu, good[k]);
-                whole &= valid == 0xffffffffu;
-                in.row[32 * k + lane] = good[k] ? page_row(page[k], a.H, p.h, a.bt, at[k], a.d) : -1;
-                in.ks[32 * k + lane] = ks[k], in.vs[32 * k + lane] = vs[k];
+                whole &= valid == (RAW ? 0xffu : 0xffffffffu);
+                if (i < kCount) in.row[i] = begin[k], in.ks[i] = ks[k], in.vs[i] = vs[k];
                 top = fmaxf(top, fabsf(vs[k]));
-                if (lane == 0) in.valid[k] = valid;
+                if (RAW) {
+                  if (lane < 4) in.valid[lane] = (valid >> (2 * lane) & 1 ? 0xffffu : 0) | (valid >> (2 * lane + 1) & 1 ? 0xffff0000u : 0);
+                } else if (lane == 0) {
+                  in.valid[k] = valid;
+                }
               }
               const int e = __reduce_max_sync(0xffffffffu, min(254, int(__float_as_uint(top) >> 23) + 1));
               if (lane == 0) in.v_exp = e, in.whole = whole;
@@ -404,6 +438,43 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
             if (++who == kLookers) who = 0;
             if (++slot == kInfo) slot = 0, phase ^= 1;
           }
+        }
+      } else if (warp == 14) {
+        // ---- copies of codes ----
+        int turn = 0, k_slot = 0, v_slot = 0, at = 0;
+        uint32_t todo_phase = 0, k_phase = 0, v_phase = 0, raw_phase = 1;
+        bool ok = true;
+        const int chunk = a.chunk;  // lane l has the l-th
+        const uint32_t bytes = uint32_t(chunk) * D;
+        auto copy = [&](const uint8_t *pool, int slot, uint32_t phase) {
+          if (!(ok = bar_wait(&sm.info_full[slot], phase, &sm.dead))) return;
+          if (!(ok = bar_wait(&sm.raw_empty[at], raw_phase, &sm.dead))) return;
+          const int64_t begin = lane < kTile / chunk ? sm.info[slot].row[RAW ? lane * (chunk / 16) : 0] : -1;
+          const uint32_t there = __ballot_sync(0xffffffffu, begin >= 0);
+          if (lane == 0) bar_expect(&sm.raw_full[at], __popc(there) * bytes);
+          __syncwarp();
+          if (begin >= 0) copy_bulk(smem_of(sm.raw[RAW ? at : 0] + lane * bytes), pool + begin, bytes, &sm.raw_full[at]);
+          if (++at == kRaw) at = 0, raw_phase ^= 1;
+        };
+        for (;;) {
+          if (!(ok = bar_wait(&sm.todo_full[turn], todo_phase, &sm.dead))) break;
+          const int n = sm.todo[turn].n;
+          __syncwarp();
+          if (lane == 0) bar_arrive(&sm.todo_empty[turn]);
+          turn ^= 1;
+          if (turn == 0) todo_phase ^= 1;
+          if (n < 0) break;
+          for (int j = 0; RAW && j <= n && ok; j++) {
+            if (j < n) {
+              copy(a.kp, k_slot, k_phase);
+              if (++k_slot == kInfo) k_slot = 0, k_phase ^= 1;
+            }
+            if (ok && j > 0) {
+              copy(a.vp, v_slot, v_phase);
+              if (++v_slot == kInfo) v_slot = 0, v_phase ^= 1;
+            }
+          }
+          if (!ok) break;
         }
       } else {
         // ---- products ----
@@ -439,27 +510,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
           if (n < 0) break;
           if (!(ok = bar_wait(&sm.q_full, q_phase, &sm.dead))) break;
           q_phase ^= 1;
-          const int ahead = split ? 2 : 1;  // how many tiles of K come before the first of V
-          for (int i = 0; i < min(ahead, n) && ok; i++) {
+          {
             const int ks = take();
             if (!ok) break;
             tm_after();
-            if (split) {
-              s_product(i, 0, ks);
-            } else {
-              s_product(0, 0, ks);
-              s_product(1, 1, ks);
-            }
+            s_product(0, 0, ks);
+            if (!split) s_product(1, 1, ks);
             if (elected()) {
               mma_commit(&sm.kv_empty[ks]);
-              if (i + 1 == n) mma_commit(&sm.q_empty);
+              if (n == 1) mma_commit(&sm.q_empty);
             }
           }
           for (int j = 0; j < n && ok; j++) {
-            const bool more = j + ahead < n;
+            const bool more = j + 1 < n;
+            int ks = 0;
+            if (more) {
+              ks = take();
+              if (!ok) break;
+              if (split) {  // the other tile's: P(j-1), which it overwrites, is behind PV(j-1)
+                tm_after();
+                s_product(j + 1 & 1, 0, ks);
+              }
+            }
             const int vs = take();
-            if (!ok) break;
-            const int ks = more ? take() : 0;
             if (!ok) break;
 #pragma unroll
             for (int t = 0; t < 2; t++) {
@@ -472,13 +545,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
                 if (elected())
 #pragma unroll
                   for (int k = half * 4; k < half * 4 + 4; k++)
-                    mma_ts(tmem + 2 * kTile + t * kTile, tmem + t * kTile + k * 8, b0 + k * (2048 >> 4), kO, j >= ahead || k > 0);
+                    mma_ts(tmem + 2 * kTile + t * kTile, tmem + t * kTile + k * 8, b0 + k * (2048 >> 4), kO, j > split || k > 0);
               }
               if (!ok) break;
               p_phase[t] ^= 1;
-              if (more)
-                s_product(t, split ? 0 : t, ks);
-              else if (elected())
+              if (more && !split)
+                s_product(t, t, ks);
+              else if ((!more || (split && j + 2 == n)) && elected())
                 mma_commit(&sm.o_full[t]);
             }
             if (!ok) break;
@@ -486,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
               mma_commit(&sm.kv_empty[vs]);
               mma_commit(&sm.info_empty[slot]);
               if (more) mma_commit(&sm.kv_empty[ks]);
-              if (j + ahead + 1 == n) mma_commit(&sm.q_empty);
+              if (j + 2 == n) mma_commit(&sm.q_empty);
             }
             if (++slot == kInfo) slot = 0;
           }
@@ -497,24 +570,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
       // ---- codes into operands ----
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
       const int ct = threadIdx.x - 256;
-      int stage = 0, turn = 0, k_slot = 0, v_slot = 0;
-      uint32_t kv_phase = 1, todo_phase = 0, k_phase = 0, v_phase = 0;
+      int stage = 0, turn = 0, k_slot = 0, v_slot = 0, at = 0;
+      uint32_t kv_phase = 1, todo_phase = 0, k_phase = 0, v_phase = 0, raw_phase = 0;
       bool ok = true;
+      constexpr int kUnits = D / 8, kStep = 128 / kUnits;  // eight codes each, of a row
+      const int u = ct % kUnits, r0 = ct / kUnits;
       auto fill = [&](const uint8_t *pool, int slot, uint32_t phase) {
         if (!(ok = bar_wait(&sm.info_full[slot], phase, &sm.dead))) return;
-        if (!(ok = bar_wait(&sm.kv_empty[stage], kv_phase, &sm.dead))) return;
-        const Info &in = sm.info[slot];
-        constexpr int kUnits = D / 8;  // eight codes each, of a row
-        const int u = ct % kUnits, r0 = ct / kUnits;
-        constexpr int kStep = 128 / kUnits;
-        const bool there = u * 8 < a.d;
-        uint8_t *to = sm.kv[stage][u >> 3];
+        const Info<RAW> &in = sm.info[slot];
         uint2 w[kUnits];
+        if (RAW) {
+          if (!(ok = bar_wait(&sm.raw_full[at], raw_phase, &sm.dead))) return;
 #pragma unroll
-        for (int i = 0; i < kUnits; i++) {
-          const int64_t at = in.row[r0 + i * kStep];
-          w[i] = there && at >= 0 ? *reinterpret_cast<const uint2 *>(pool + at + u * 8) : make_uint2(0, 0);
+          for (int i = 0; i < kUnits; i++) w[i] = *reinterpret_cast<const uint2 *>(sm.raw[RAW ? at : 0] + (r0 + i * kStep) * D + u * 8);
+          if (!in.whole) {  // nothing was copied there
+#pragma unroll
+            for (int i = 0; i < kUnits; i++) {
+              const int r = r0 + i * kStep;
+              if (!(in.valid[r / 32] >> (r & 31) & 1)) w[i] = make_uint2(0, 0);
+            }
+          }
+        } else {
+          const bool there = u * 8 < a.d;
+#pragma unroll
+          for (int i = 0; i < kUnits; i++) {
+            const int64_t begin = in.row[RAW ? 0 : r0 + i * kStep];
+            w[i] = there && begin >= 0 ? *reinterpret_cast<const uint2 *>(pool + begin + u * 8) : make_uint2(0, 0);
+          }
         }
+        if (!(ok = bar_wait(&sm.kv_empty[stage], kv_phase, &sm.dead))) return;
+        uint8_t *to = sm.kv[stage][u >> 3];
 #pragma unroll
         for (int i = 0; i < kUnits; i++) {
           const int r = r0 + i * kStep;
@@ -522,25 +607,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
         }
         fence_async();
         __syncwarp();
-        if (lane == 0) bar_arrive(&sm.kv_full[stage]);
+        if (lane == 0) {
+          bar_arrive(&sm.kv_full[stage]);
+          if (RAW) bar_arrive(&sm.raw_empty[at]);
+        }
         if (++stage == kStages) stage = 0, kv_phase ^= 1;
+        if (++at == kRaw) at = 0, raw_phase ^= 1;
       };
       for (;;) {
         if (!(ok = bar_wait(&sm.todo_full[turn], todo_phase, &sm.dead))) break;
-        const int n = sm.todo[turn].n, ahead = sm.todo[turn].split ? 2 : 1;
+        const int n = sm.todo[turn].n;
         __syncwarp();
         if (lane == 0) bar_arrive(&sm.todo_empty[turn]);
         turn ^= 1;
         if (turn == 0) todo_phase ^= 1;
         if (n < 0) break;
-        for (int i = 0; i < n + ahead && ok; i++) {
-          if (i >= ahead) {
-            fill(a.vp, v_slot, v_phase);
-            if (++v_slot == kInfo) v_slot = 0, v_phase ^= 1;
-          }
-          if (ok && i < n) {
+        for (int j = 0; j <= n && ok; j++) {
+          if (j < n) {
             fill(a.kp, k_slot, k_phase);
             if (++k_slot == kInfo) k_slot = 0, k_phase ^= 1;
+          }
+          if (ok && j > 0) {
+            fill(a.vp, v_slot, v_phase);
+            if (++v_slot == kInfo) v_slot = 0, v_phase ^= 1;
           }
         }
         if (!ok) break;
@@ -605,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
         int v_exp = 1;  // O is in units of 2^(v_exp - 127), the largest V scale so far
         int done = 0;   // tiles of this thread's
         for (int j = 0; j < n; j++) {
-          const Info &in = sm.info[slot];
+          const Info<RAW> &in = sm.info[slot];
           const uint32_t full = info_phase;
           uint64_t *const info_full = &sm.info_full[slot];
           if (++slot == kInfo) slot = 0, info_phase ^= 1;
@@ -620,15 +709,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
           tm_wait_ld();
           // What turns a product into a score: a page's scale times the row's.  It is
           // not 0, so that what is masked stays at -inf (a page's codes are 0 where its scale is).
-          float f[PLAIN ? kTile / 16 : 1];
-          if (PLAIN) {
+          float f[RAW ? kTile / 16 : 1];
+          if (RAW) {
 #pragma unroll
-            for (int i = 0; i < kTile / 16; i++) f[i] = fmaxf(in.ks[16 * i] * sc, 0x1p-126f);
+            for (int i = 0; i < kTile / 16; i++) f[i] = fmaxf(in.ks[RAW ? i : 0] * sc, 0x1p-126f);
           } else {
             f[0] = 1.0f;
 #pragma unroll
             for (int i = 0; i < kTile; i += 2) {
-              const float2 k2 = *reinterpret_cast<const float2 *>(&in.ks[i]);
+              const float2 k2 = *reinterpret_cast<const float2 *>(&in.ks[RAW ? 0 : i]);
               const float2 y = mul2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), make_float2(k2.x * sc, k2.y * sc));
               x[i] = __float_as_uint(y.x), x[i + 1] = __float_as_uint(y.y);
             }
@@ -651,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
               top[0] = max3(top[0], __uint_as_float(x[16 * i + k]), __uint_as_float(x[16 * i + k + 1]));
               top[1] = max3(top[1], __uint_as_float(x[16 * i + k + 2]), __uint_as_float(x[16 * i + k + 3]));
             }
-            now = fmaxf(now, fmaxf(top[0], top[1]) * f[PLAIN ? i : 0]);
+            now = fmaxf(now, fmaxf(top[0], top[1]) * f[RAW ? i : 0]);
           }
           const bool moved = now > m + kLag;
           const float keep = moved ? ex2(m - now) : 1.0f;
@@ -684,17 +773,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
             for (int i = 0; i < 16; i++) {
               const int at = 32 * c + 2 * i;
               float2 y = make_float2(__uint_as_float(x[at]), __uint_as_float(x[at + 1]));
-              if (PLAIN)
-                y = fma2(y, make_float2(f[PLAIN ? at / 16 : 0], f[PLAIN ? at / 16 : 0]), make_float2(base, base));
+              if (RAW)
+                y = fma2(y, make_float2(f[RAW ? at / 16 : 0], f[RAW ? at / 16 : 0]), make_float2(base, base));
               else
                 y = add2(y, make_float2(base, base));
               y = make_float2(ex2(y.x), ex2(y.y));
               sums[i & 3] = add2(sums[i & 3], y);
-              if (PLAIN) {
-                const float v = in.vs[at & ~15] * unit;
+              if (RAW) {
+                const float v = in.vs[RAW ? at / 16 : 0] * unit;
                 y = mul2(y, make_float2(v, v));
               } else {
-                const float2 v2 = *reinterpret_cast<const float2 *>(&in.vs[at]);
+                const float2 v2 = *reinterpret_cast<const float2 *>(&in.vs[RAW ? 0 : at]);
                 y = mul2(y, make_float2(v2.x * unit, v2.y * unit));
               }
               pk[i] = pack<false>(y.x, y.y);
@@ -916,13 +1005,13 @@ Places places(const cg_cache *c, const cg_attend *t, const cg_groups *g) {
   return w;
 }
 
-template <int FMT, int D, bool PLAIN>
+template <int FMT, int D, bool RAW>
 cudaError_t launch(const SharedArgs &a, cudaStream_t st) {
-  constexpr int kSmem = int(sizeof(Smem<D>));
+  constexpr int kSmem = int(sizeof(Smem<D, RAW>));
   static_assert(kSmem <= 227 * 1024, "fits in an SM");
-  const cudaError_t e = cudaFuncSetAttribute(k_shared<FMT, D, PLAIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const cudaError_t e = cudaFuncSetAttribute(k_shared<FMT, D, RAW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  const cudaError_t e2 = launch_early(k_shared<FMT, D, PLAIN>, dim3(kGrid), dim3(kThreads), kSmem, st, a);
+  const cudaError_t e2 = launch_early(k_shared<FMT, D, RAW>, dim3(kGrid), dim3(kThreads), kSmem, st, a);
   if (e2 != cudaSuccess) return e2;
   const cudaError_t e3 = launch_early(k_shared_join<D>, dim3(kGrid, kRows / 8), dim3(2 * D), 0, st, a);
   return e3 != cudaSuccess ? e3 : cudaGetLastError();
@@ -930,9 +1019,9 @@ cudaError_t launch(const SharedArgs &a, cudaStream_t st) {
 
 template <int FMT>
 cudaError_t launch_format(const SharedArgs &a, cudaStream_t st) {
-  const bool plain = a.bt % 16 == 0;
-  if (a.d <= 64) return plain ? launch<FMT, 64, true>(a, st) : launch<FMT, 64, false>(a, st);
-  return plain ? launch<FMT, 128, true>(a, st) : launch<FMT, 128, false>(a, st);
+  const bool raw = a.bt % 16 == 0 && (a.d == 64 || a.d == 128);
+  if (a.d <= 64) return raw ? launch<FMT, 64, true>(a, st) : launch<FMT, 64, false>(a, st);
+  return raw ? launch<FMT, 128, true>(a, st) : launch<FMT, 128, false>(a, st);
 }
 
 }  // namespace
@@ -982,6 +1071,8 @@ extern "C" cg_status cg_shared_attend(const cg_cache *cache, const cg_attend *at
   a.bt = cache->block_tokens, a.n_blocks = cache->n_blocks, a.stride = attend->table_stride;
   a.scale_log2 = attend->scale * 1.4426950408889634f;
   a.bf16 = attend->dtype == CG_BF16;
+  a.chunk = kTile;
+  while (a.bt % a.chunk) a.chunk /= 2;
   k_shared_plan<<<1, kPlan, 0, st>>>(a);
   const cg_status rc = attend_own(cache, attend, a.first, a.own, a.own_ml, q_dev, k_pool, v_pool, k_scale, v_scale, table_dev, len_dev, out_dev,
                                   lse_dev, ws, st);
