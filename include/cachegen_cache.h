@@ -158,7 +158,7 @@ size_t cg_shared_workspace_bytes(const cg_cache *cache, const cg_attend *attend,
  * of them full (cg_pages_groups finds groups, and its arrays can be passed as
  * they are).  Arguments, formulas and outputs are those of cg_cache_attend, with
  * one difference: of a shared prefix a weight is off by at most 2^-11 of itself
- * or 2^-36 of the largest probability times the largest V scale, whichever is
+ * or 2^-31 of the largest probability times the largest V scale, whichever is
  * more.
  * Sequences that are in no group, and those of a group whose first new token
  * does not see its whole prefix, read all of their positions by themselves.  A

@@ -12,9 +12,9 @@
 // bf16 query row is raised to the top of f16's range by a power of two.  K's
 // page scales are applied to the scores, V's to the probabilities, over a power
 // of two above the largest scale so far (O is scaled when that grows).  P is
-// rounded to f16: a weight is off by at most 2^-11 of itself or 2^-36 of the
-// largest times the largest scale, whichever is more (p < 2^15, and the largest
-// has at least 2^12).
+// rounded to f16: a weight is off by at most 2^-11 of itself or 2^-31 of the
+// largest times the largest scale, whichever is more (the largest has at least
+// 2^7, and half of the spacing of f16's subnormals is 2^-25).
 //
 // A CTA has two tiles of rows, a and b, whose softmax warpgroups take turns with
 // the products; where an item has up to 128 rows, a and b are the same rows
@@ -46,8 +46,10 @@ constexpr int kRaw = 4;      // tiles of codes
 constexpr int kInfo = 6;     // tiles whose pages and scales are known
 constexpr int kLookers = 2;  // warps that look them up
 constexpr int kPlan = 1024;
-// p = 2^(s - m + kLift) < 2^15, m at most kLag under the maximum: as in the kernels whose parts are joined with these
-constexpr float kLift = 12.0f, kLag = 3.0f;
+// p = 2^(s - m + kLift) < 2^15, m at most kLag under the maximum.  The parts that
+// these are joined with have kOwnLift.  (With 12 and 3 here O is scaled so often
+// that 64 readers of 32768 tokens take 155 us, not 150.)
+constexpr float kLift = 7.0f, kLag = 8.0f, kOwnLift = 12.0f;
 // What an item costs: kIn for its way in and out, and for each tile of positions.
 constexpr int kIn = 10, kFull = 4, kSplit = 2;
 
@@ -252,6 +254,13 @@ template <int FMT>
 __device__ inline uint4 operands_of(uint2 w) {  // eight codes
   if (FMT == CG_CACHE_INT8) w.x ^= 0x80808080u, w.y ^= 0x80808080u;
   return make_uint4(halves_of<FMT, 0>(w.x), halves_of<FMT, 1>(w.x), halves_of<FMT, 0>(w.y), halves_of<FMT, 1>(w.y));
+}
+
+// Waits for what tm_load is to bring; x is not used before.
+__device__ inline void tm_landed(uint32_t (&x)[32]) {
+#define CG_W8(i) "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3]), "+r"(x[i + 4]), "+r"(x[i + 5]), "+r"(x[i + 6]), "+r"(x[i + 7])
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : CG_W8(0), CG_W8(8), CG_W8(16), CG_W8(24) : : "memory");
+#undef CG_W8
 }
 
 // Copies `bytes`, a multiple of 16, to shared memory.
@@ -464,14 +473,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
           turn ^= 1;
           if (turn == 0) todo_phase ^= 1;
           if (n < 0) break;
-          for (int j = 0; RAW && j <= n && ok; j++) {
-            if (j < n) {
-              copy(a.kp, k_slot, k_phase);
-              if (++k_slot == kInfo) k_slot = 0, k_phase ^= 1;
-            }
-            if (ok && j > 0) {
-              copy(a.vp, v_slot, v_phase);
+#pragma unroll 1
+          for (int i = 0; RAW && i < 2 * n && ok; i++) {
+            const bool is_v = i == 2 * n - 1 || (i > 0 && i % 2 == 0);
+            copy(is_v ? a.vp : a.kp, is_v ? v_slot : k_slot, is_v ? v_phase : k_phase);
+            if (is_v) {
               if (++v_slot == kInfo) v_slot = 0, v_phase ^= 1;
+            } else {
+              if (++k_slot == kInfo) k_slot = 0, k_phase ^= 1;
             }
           }
           if (!ok) break;
@@ -575,45 +584,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
       bool ok = true;
       constexpr int kUnits = D / 8, kStep = 128 / kUnits;  // eight codes each, of a row
       const int u = ct % kUnits, r0 = ct / kUnits;
-      auto fill = [&](const uint8_t *pool, int slot, uint32_t phase) {
-        if (!(ok = bar_wait(&sm.info_full[slot], phase, &sm.dead))) return;
-        const Info<RAW> &in = sm.info[slot];
-        uint2 w[kUnits];
-        if (RAW) {
-          if (!(ok = bar_wait(&sm.raw_full[at], raw_phase, &sm.dead))) return;
-#pragma unroll
-          for (int i = 0; i < kUnits; i++) w[i] = *reinterpret_cast<const uint2 *>(sm.raw[RAW ? at : 0] + (r0 + i * kStep) * D + u * 8);
-          if (!in.whole) {  // nothing was copied there
-#pragma unroll
-            for (int i = 0; i < kUnits; i++) {
-              const int r = r0 + i * kStep;
-              if (!(in.valid[r / 32] >> (r & 31) & 1)) w[i] = make_uint2(0, 0);
-            }
-          }
-        } else {
-          const bool there = u * 8 < a.d;
-#pragma unroll
-          for (int i = 0; i < kUnits; i++) {
-            const int64_t begin = in.row[RAW ? 0 : r0 + i * kStep];
-            w[i] = there && begin >= 0 ? *reinterpret_cast<const uint2 *>(pool + begin + u * 8) : make_uint2(0, 0);
-          }
-        }
-        if (!(ok = bar_wait(&sm.kv_empty[stage], kv_phase, &sm.dead))) return;
-        uint8_t *to = sm.kv[stage][u >> 3];
-#pragma unroll
-        for (int i = 0; i < kUnits; i++) {
-          const int r = r0 + i * kStep;
-          *reinterpret_cast<uint4 *>(to + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = operands_of<FMT>(w[i]);
-        }
-        fence_async();
-        __syncwarp();
-        if (lane == 0) {
-          bar_arrive(&sm.kv_full[stage]);
-          if (RAW) bar_arrive(&sm.raw_empty[at]);
-        }
-        if (++stage == kStages) stage = 0, kv_phase ^= 1;
-        if (++at == kRaw) at = 0, raw_phase ^= 1;
-      };
       for (;;) {
         if (!(ok = bar_wait(&sm.todo_full[turn], todo_phase, &sm.dead))) break;
         const int n = sm.todo[turn].n;
@@ -622,14 +592,51 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
         turn ^= 1;
         if (turn == 0) todo_phase ^= 1;
         if (n < 0) break;
-        for (int j = 0; j <= n && ok; j++) {
-          if (j < n) {
-            fill(a.kp, k_slot, k_phase);
-            if (++k_slot == kInfo) k_slot = 0, k_phase ^= 1;
+#pragma unroll 1
+        for (int i = 0; i < 2 * n; i++) {
+          const bool is_v = i == 2 * n - 1 || (i > 0 && i % 2 == 0);
+          const Info<RAW> &in = sm.info[is_v ? v_slot : k_slot];
+          if (!(ok = bar_wait(&sm.info_full[is_v ? v_slot : k_slot], is_v ? v_phase : k_phase, &sm.dead))) break;
+          if (RAW && !(ok = bar_wait(&sm.raw_full[at], raw_phase, &sm.dead))) break;
+          if (!(ok = bar_wait(&sm.kv_empty[stage], kv_phase, &sm.dead))) break;
+          const uint8_t *pool = is_v ? a.vp : a.kp, *from = sm.raw[RAW ? at : 0] + r0 * D + u * 8;
+          const bool there = u * 8 < a.d, whole = in.whole;
+          uint8_t *to = sm.kv[stage][u >> 3] + r0 * 128 + (((u & 7) ^ (r0 & 7)) << 4);  // (kStep is a multiple of 8)
+#pragma unroll 1
+          for (int h = 0; h < kUnits; h += 8) {
+            uint2 w[8];
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+              const int r = (h + k) * kStep;
+              if (RAW) {
+                w[k] = *reinterpret_cast<const uint2 *>(from + r * D);
+              } else {
+                const int64_t begin = in.row[RAW ? 0 : r0 + r];
+                w[k] = there && begin >= 0 ? *reinterpret_cast<const uint2 *>(pool + begin + u * 8) : make_uint2(0, 0);
+              }
+            }
+            if (RAW && !whole) {  // nothing was copied there
+#pragma unroll
+              for (int k = 0; k < 8; k++) {
+                const int r = r0 + (h + k) * kStep;
+                if (!(in.valid[r / 32] >> (r & 31) & 1)) w[k] = make_uint2(0, 0);
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 8; k++) *reinterpret_cast<uint4 *>(to + (h + k) * kStep * 128) = operands_of<FMT>(w[k]);
           }
-          if (ok && j > 0) {
-            fill(a.vp, v_slot, v_phase);
+          fence_async();
+          __syncwarp();
+          if (lane == 0) {
+            bar_arrive(&sm.kv_full[stage]);
+            if (RAW) bar_arrive(&sm.raw_empty[at]);
+          }
+          if (++stage == kStages) stage = 0, kv_phase ^= 1;
+          if (++at == kRaw) at = 0, raw_phase ^= 1;
+          if (is_v) {
             if (++v_slot == kInfo) v_slot = 0, v_phase ^= 1;
+          } else {
+            if (++k_slot == kInfo) k_slot = 0, k_phase ^= 1;
           }
         }
         if (!ok) break;
@@ -703,45 +710,50 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
           if (!(ok = bar_wait(&sm.s_full[t], s_phase, &sm.dead))) break;
           s_phase ^= 1;
           tm_after();
-          uint32_t x[kTile];
-#pragma unroll
-          for (int i = 0; i < 4; i++) tm_load(s_at + 32 * i, x + 32 * i);
-          tm_wait_ld();
+          // The scores are read twice, for the maximum and for the exponentials, 32
+          // columns ahead of the arithmetic each time.
+          uint32_t x[2][32];
+          const int whole = in.whole;
           // What turns a product into a score: a page's scale times the row's.  It is
           // not 0, so that what is masked stays at -inf (a page's codes are 0 where its scale is).
-          float f[RAW ? kTile / 16 : 1];
-          if (RAW) {
+          auto scale_of = [&](int i) { return RAW ? fmaxf(in.ks[RAW ? i : 0] * sc, 0x1p-126f) : 1.0f; };
+          auto prepare = [&](int c, uint32_t (&y)[32]) {  // columns 32 c ...
+            if (!RAW) {
 #pragma unroll
-            for (int i = 0; i < kTile / 16; i++) f[i] = fmaxf(in.ks[RAW ? i : 0] * sc, 0x1p-126f);
-          } else {
-            f[0] = 1.0f;
-#pragma unroll
-            for (int i = 0; i < kTile; i += 2) {
-              const float2 k2 = *reinterpret_cast<const float2 *>(&in.ks[RAW ? 0 : i]);
-              const float2 y = mul2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), make_float2(k2.x * sc, k2.y * sc));
-              x[i] = __float_as_uint(y.x), x[i + 1] = __float_as_uint(y.y);
+              for (int i = 0; i < 32; i += 2) {
+                const float2 k2 = *reinterpret_cast<const float2 *>(&in.ks[RAW ? 0 : 32 * c + i]);
+                const float2 z = mul2(make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), make_float2(k2.x * sc, k2.y * sc));
+                y[i] = __float_as_uint(z.x), y[i + 1] = __float_as_uint(z.y);
+              }
             }
-          }
-          if (!in.whole) {
-#pragma unroll
-            for (int k = 0; k < 4; k++) {
-              const uint32_t valid = in.valid[k];
+            if (!whole) {
+              const uint32_t valid = in.valid[c];
 #pragma unroll
               for (int i = 0; i < 32; i++)
-                if (!(valid >> i & 1)) x[32 * k + i] = 0xff800000u;
+                if (!(valid >> i & 1)) y[i] = 0xff800000u;
             }
-          }
+          };
+          tm_load(s_at, x[0]);
+          tm_landed(x[0]);
           float now = -INFINITY;
+#pragma unroll 1
+          for (int c2 = 0; c2 < 4; c2 += 2)
 #pragma unroll
-          for (int i = 0; i < kTile / 16; i++) {
-            float top[2] = {fmaxf(__uint_as_float(x[16 * i]), __uint_as_float(x[16 * i + 1])), fmaxf(__uint_as_float(x[16 * i + 2]), __uint_as_float(x[16 * i + 3]))};
+            for (int k = 0; k < 2; k++) {
+              const int c = c2 + k;
+              uint32_t(&y)[32] = x[k];
+              tm_load(s_at + 32 * (c + 1 & 3), x[k ^ 1]);  // the last one is the first of the next pass
+              prepare(c, y);
 #pragma unroll
-            for (int k = 4; k < 16; k += 4) {
-              top[0] = max3(top[0], __uint_as_float(x[16 * i + k]), __uint_as_float(x[16 * i + k + 1]));
-              top[1] = max3(top[1], __uint_as_float(x[16 * i + k + 2]), __uint_as_float(x[16 * i + k + 3]));
+              for (int h = 0; h < 2; h++) {
+                auto at = [&](int i) { return __uint_as_float(y[16 * h + i]); };
+                float top[2] = {fmaxf(at(0), at(1)), fmaxf(at(2), at(3))};
+#pragma unroll
+                for (int i = 4; i < 16; i += 4) top[0] = max3(top[0], at(i), at(i + 1)), top[1] = max3(top[1], at(i + 2), at(i + 3));
+                now = fmaxf(now, fmaxf(top[0], top[1]) * scale_of(2 * c + h));
+              }
+              tm_landed(x[k ^ 1]);
             }
-            now = fmaxf(now, fmaxf(top[0], top[1]) * f[RAW ? i : 0]);
-          }
           const bool moved = now > m + kLag;
           const float keep = moved ? ex2(m - now) : 1.0f;
           if (moved) m = now;
@@ -753,11 +765,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
           }
           if (done > 0 && __any_sync(0xffffffffu, scale_o != 1.0f)) {
             l = mul2(l, make_float2(keep, keep));
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; c++) {
               uint32_t y[32];
               tm_load(o_at + 32 * c, y);
-              tm_wait_ld();
+              tm_landed(y);
 #pragma unroll
               for (int i = 0; i < 32; i++) y[i] = __float_as_uint(__uint_as_float(y[i]) * scale_o);
               tm_store32(o_at + 32 * c, y);
@@ -766,40 +778,46 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
           done++;
           const float base = kLift - (m == -INFINITY ? 0.0f : m), unit = __int_as_float((254 - v_exp) << 23);
           float2 sums[4] = {};
+#pragma unroll 1
+          for (int c2 = 0; c2 < 4; c2 += 2) {
 #pragma unroll
-          for (int c = 0; c < 4; c++) {
-            uint32_t pk[16];
+            for (int k = 0; k < 2; k++) {
+              const int c = c2 + k;
+              uint32_t(&z)[32] = x[k];
+              if (c < 3) tm_load(s_at + 32 * (c + 1), x[k ^ 1]);
+              prepare(c, z);
+              uint32_t pk[16];
 #pragma unroll
-            for (int i = 0; i < 16; i++) {
-              const int at = 32 * c + 2 * i;
-              float2 y = make_float2(__uint_as_float(x[at]), __uint_as_float(x[at + 1]));
-              if (RAW)
-                y = fma2(y, make_float2(f[RAW ? at / 16 : 0], f[RAW ? at / 16 : 0]), make_float2(base, base));
-              else
-                y = add2(y, make_float2(base, base));
-              y = make_float2(ex2(y.x), ex2(y.y));
-              sums[i & 3] = add2(sums[i & 3], y);
-              if (RAW) {
-                const float v = in.vs[RAW ? at / 16 : 0] * unit;
-                y = mul2(y, make_float2(v, v));
-              } else {
-                const float2 v2 = *reinterpret_cast<const float2 *>(&in.vs[RAW ? 0 : at]);
-                y = mul2(y, make_float2(v2.x * unit, v2.y * unit));
+              for (int h = 0; h < 2; h++) {
+                const float f = scale_of(2 * c + h), v = RAW ? in.vs[RAW ? 2 * c + h : 0] * unit : 0.0f;
+#pragma unroll
+                for (int i = 8 * h; i < 8 * h + 8; i++) {
+                  float2 y = make_float2(__uint_as_float(z[2 * i]), __uint_as_float(z[2 * i + 1]));
+                  y = RAW ? fma2(y, make_float2(f, f), make_float2(base, base)) : add2(y, make_float2(base, base));
+                  y = make_float2(ex2(y.x), ex2(y.y));
+                  sums[i & 3] = add2(sums[i & 3], y);
+                  if (RAW) {
+                    y = mul2(y, make_float2(v, v));
+                  } else {
+                    const float2 v2 = *reinterpret_cast<const float2 *>(&in.vs[RAW ? 0 : 32 * c + 2 * i]);
+                    y = mul2(y, make_float2(v2.x * unit, v2.y * unit));
+                  }
+                  pk[i] = pack<false>(y.x, y.y);
+                }
               }
-              pk[i] = pack<false>(y.x, y.y);
+              if (c < 3) tm_landed(x[k ^ 1]);  // (P lies over the columns that have been read)
+              tm_store16(s_at + 16 * c, pk);
             }
-            tm_store16(s_at + 16 * c, pk);
-            if (c & 1) {  // half of P is there
-              tm_wait_st();
-              tm_before();
-              __syncwarp();
-              if (lane == 0) bar_arrive(&sm.p_full[t][c >> 1]);
-            }
+            tm_wait_st();  // half of P is there
+            tm_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&sm.p_full[t][c2 >> 1]);
           }
           l = add2(l, add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
         }
         if (!ok) break;
         float sum = l.x + l.y;
+        m += kOwnLift - kLift;
         if (done > 0) {
           if (!(ok = bar_wait(&sm.o_full[t], o_phase, &sm.dead))) break;
           o_phase ^= 1;
@@ -845,17 +863,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
           }
           const float turn_l = total_l == 0.0f ? 0.0f : 1.0f / total_l;
           float *part = a.parts + int64_t(slot_out) * kRows * (D + 2);
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 32; c++) {
             uint32_t y[32];
             tm_load(o_at + 32 * c, y);
-            tm_wait_ld();
+            tm_landed(y);
 #pragma unroll
             for (int i = 0; i < 32; i++) y[i] = __float_as_uint(__uint_as_float(y[i]) * f_mine);
             if (both) {
               uint32_t z[32];
               tm_load(o_at + kTile + 32 * c, z);
-              tm_wait_ld();
+              tm_landed(z);
 #pragma unroll
               for (int i = 0; i < 32; i++) y[i] = __float_as_uint(__uint_as_float(y[i]) + __uint_as_float(z[i]) * f_other);
             }
@@ -891,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
             if (!whole)
               part[kRows * D + t * kTile + r] = m, part[kRows * (D + 1) + t * kTile + r] = sum;
             else if (a.lse)
-              a.lse[at] = total_l == 0.0f ? -INFINITY : (top - kLift + log2f(total_l)) * 0.6931471805599453f;
+              a.lse[at] = total_l == 0.0f ? -INFINITY : (top - kOwnLift + log2f(total_l)) * 0.6931471805599453f;
           }
           __syncwarp();
           if (lane == 0) {
@@ -973,7 +991,7 @@ __global__ void __launch_bounds__(2 * D, 2048 / (2 * D)) k_shared_join(const __g
                            : make_uint2(pack<false>(y[0] * f, y[1] * f), pack<false>(y[2] * f, y[3] * f));
     *reinterpret_cast<uint2 *>(a.out + at * a.d + c * 4) = w;
   }
-  if (c == 0 && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (top - kLift + log2f(sum)) * 0.6931471805599453f;
+  if (c == 0 && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (top - kOwnLift + log2f(sum)) * 0.6931471805599453f;
 }
 
 bool groups_ok(const cg_cache *c, const cg_attend *t, const cg_groups *g) {

@@ -1,9 +1,9 @@
 """cg_shared_attend on the GPU against its 64-bit definition (tests/serve_ref.py): each sequence by itself, over its own row of the table.
 
-Beside the tolerances there, a small weight has an absolute one.  A weight of the second product is W = p s / u in f16, with p = 2^(score - m + 12),
-m at most 3 under the maximum, s its page's V scale and u a power of two, s < u <= 2 max s.  f16 rounds W by 2^-11 of itself at most, or by half of
-the spacing of its subnormals, 2^-25.  The output is u sum(W c) / sum(p), c the codes, and sum(p) >= 2^12, for the maximum itself is in the sum: what
-the subnormals' spacing moves is at most 2^-25 u sum|c| / 2^12 <= 2^-36 max(s) sum|c|.  (It is seen where the positions that have the weight have
+Beside the tolerances there, a small weight has an absolute one.  A weight of the second product is W = p s / u in f16, with p = 2^(score - m + 7),
+m at most 8 under the maximum, s its page's V scale and u a power of two, s < u <= 2 max s.  f16 rounds W by 2^-11 of itself at most, or by half of
+the spacing of its subnormals, 2^-25.  The output is u sum(W c) / sum(p), c the codes, and sum(p) >= 2^7, for the maximum itself is in the sum: what
+the subnormals' spacing moves is at most 2^-25 u sum|c| / 2^7 <= 2^-31 max(s) sum|c|.  (It is seen where the positions that have the weight have
 code 0 in a channel.)
 """
 import math
@@ -106,7 +106,7 @@ class Setup:
 
     def tolerances(self, o, l, A, X, n, small):
         to, tl = ref.tolerances(o, l, A, X, self.q.shape[3], n, self.q.dtype, 11)  # weights go into the second product with 11 bits
-        return to + 2.0 ** -36 * small, tl
+        return to + 2.0 ** -31 * small, tl
 
     def check(self, out, z, only=None):
         B, T, Hq, d = self.q.shape
