@@ -36,8 +36,8 @@ namespace cg {
 namespace {
 
 constexpr int kThreads = 512;
-// Registers a thread: 512 are launched with 128 each (2 * 176 + 88 + 72 = 4 * 128).
-constexpr int kSoftRegs = 176, kConvRegs = 88, kOtherRegs = 72;
+// Registers a thread: 512 are launched with 128 each (2 * 192 + 72 + 56 = 4 * 128).
+constexpr int kSoftRegs = 192, kConvRegs = 72, kOtherRegs = 56;
 constexpr int kTile = 128;  // rows of a tile, positions of a tile
 constexpr int kRows = 2 * kTile;
 constexpr int kGrid = kSMs;
@@ -261,6 +261,15 @@ __device__ inline void tm_landed(uint32_t (&x)[32]) {
 #define CG_W8(i) "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3]), "+r"(x[i + 4]), "+r"(x[i + 5]), "+r"(x[i + 6]), "+r"(x[i + 7])
   asm volatile("tcgen05.wait::ld.sync.aligned;" : CG_W8(0), CG_W8(8), CG_W8(16), CG_W8(24) : : "memory");
 #undef CG_W8
+}
+
+// 16 columns of this thread's lane, waited for.
+__device__ inline void tm_load16(uint32_t addr, uint32_t (&x)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+               "tcgen05.wait::ld.sync.aligned;"
+               : CG_R8(x, 0), CG_R8(x, 8)
+               : "r"(addr)
+               : "memory");
 }
 
 // Copies `bytes`, a multiple of 16, to shared memory.
@@ -710,49 +719,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
           if (!(ok = bar_wait(&sm.s_full[t], s_phase, &sm.dead))) break;
           s_phase ^= 1;
           tm_after();
-          // The scores are read twice, for the maximum and for the exponentials, 32
-          // columns ahead of the arithmetic each time.
-          uint32_t x[2][32];
           const int whole = in.whole;
+          if (!RAW || !whole) {  // in the way of the loops below: scales of single positions (K's), and positions that are not there
+#pragma unroll 1
+            for (int c = 0; c < 4; c++) {
+              uint32_t y[32];
+              tm_load(s_at + 32 * c, y);
+              tm_landed(y);
+              const uint32_t valid = in.valid[c];
+#pragma unroll
+              for (int i = 0; i < 32; i++) {
+                if (!RAW) y[i] = __float_as_uint(__uint_as_float(y[i]) * (in.ks[RAW ? 0 : 32 * c + i] * sc));
+                if (!(valid >> i & 1)) y[i] = 0xff800000u;
+              }
+              tm_store32(s_at + 32 * c, y);
+            }
+            tm_wait_st();
+          }
           // What turns a product into a score: a page's scale times the row's.  It is
           // not 0, so that what is masked stays at -inf (a page's codes are 0 where its scale is).
           auto scale_of = [&](int i) { return RAW ? fmaxf(in.ks[RAW ? i : 0] * sc, 0x1p-126f) : 1.0f; };
-          auto prepare = [&](int c, uint32_t (&y)[32]) {  // columns 32 c ...
-            if (!RAW) {
+          uint32_t x[4][32];
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 k2 = *reinterpret_cast<const float2 *>(&in.ks[RAW ? 0 : 32 * c + i]);
-                const float2 z = mul2(make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), make_float2(k2.x * sc, k2.y * sc));
-                y[i] = __float_as_uint(z.x), y[i + 1] = __float_as_uint(z.y);
-              }
-            }
-            if (!whole) {
-              const uint32_t valid = in.valid[c];
+          for (int c = 0; c < 4; c++) tm_load(s_at + 32 * c, x[c]);
 #pragma unroll
-              for (int i = 0; i < 32; i++)
-                if (!(valid >> i & 1)) y[i] = 0xff800000u;
-            }
-          };
-          tm_load(s_at, x[0]);
-          tm_landed(x[0]);
+          for (int c = 0; c < 4; c++) tm_landed(x[c]);
           float now = -INFINITY;
-#pragma unroll 1
-          for (int c2 = 0; c2 < 4; c2 += 2)
 #pragma unroll
-            for (int k = 0; k < 2; k++) {
-              const int c = c2 + k;
-              uint32_t(&y)[32] = x[k];
-              tm_load(s_at + 32 * (c + 1 & 3), x[k ^ 1]);  // the last one is the first of the next pass
-              prepare(c, y);
+          for (int c = 0; c < 4; c++)
 #pragma unroll
-              for (int h = 0; h < 2; h++) {
-                auto at = [&](int i) { return __uint_as_float(y[16 * h + i]); };
-                float top[2] = {fmaxf(at(0), at(1)), fmaxf(at(2), at(3))};
+            for (int h = 0; h < 2; h++) {
+              auto at = [&](int i) { return __uint_as_float(x[c][16 * h + i]); };
+              float top[2] = {fmaxf(at(0), at(1)), fmaxf(at(2), at(3))};
 #pragma unroll
-                for (int i = 4; i < 16; i += 4) top[0] = max3(top[0], at(i), at(i + 1)), top[1] = max3(top[1], at(i + 2), at(i + 3));
-                now = fmaxf(now, fmaxf(top[0], top[1]) * scale_of(2 * c + h));
-              }
-              tm_landed(x[k ^ 1]);
+              for (int i = 4; i < 16; i += 4) top[0] = max3(top[0], at(i), at(i + 1)), top[1] = max3(top[1], at(i + 2), at(i + 3));
+              now = fmaxf(now, fmaxf(top[0], top[1]) * scale_of(2 * c + h));
             }
           const bool moved = now > m + kLag;
           const float keep = moved ? ex2(m - now) : 1.0f;
@@ -766,52 +767,45 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
           if (done > 0 && __any_sync(0xffffffffu, scale_o != 1.0f)) {
             l = mul2(l, make_float2(keep, keep));
 #pragma unroll 1
-            for (int c = 0; c < D / 32; c++) {
-              uint32_t y[32];
-              tm_load(o_at + 32 * c, y);
-              tm_landed(y);
+            for (int c = 0; c < D / 16; c++) {
+              uint32_t y[16];
+              tm_load16(o_at + 16 * c, y);
 #pragma unroll
-              for (int i = 0; i < 32; i++) y[i] = __float_as_uint(__uint_as_float(y[i]) * scale_o);
-              tm_store32(o_at + 32 * c, y);
+              for (int i = 0; i < 16; i++) y[i] = __float_as_uint(__uint_as_float(y[i]) * scale_o);
+              tm_store16(o_at + 16 * c, y);
             }
           }
           done++;
           const float base = kLift - (m == -INFINITY ? 0.0f : m), unit = __int_as_float((254 - v_exp) << 23);
           float2 sums[4] = {};
-#pragma unroll 1
-          for (int c2 = 0; c2 < 4; c2 += 2) {
 #pragma unroll
-            for (int k = 0; k < 2; k++) {
-              const int c = c2 + k;
-              uint32_t(&z)[32] = x[k];
-              if (c < 3) tm_load(s_at + 32 * (c + 1), x[k ^ 1]);
-              prepare(c, z);
-              uint32_t pk[16];
+          for (int c = 0; c < 4; c++) {
+            uint32_t pk[16];
 #pragma unroll
-              for (int h = 0; h < 2; h++) {
-                const float f = scale_of(2 * c + h), v = RAW ? in.vs[RAW ? 2 * c + h : 0] * unit : 0.0f;
+            for (int h = 0; h < 2; h++) {
+              const float f = scale_of(2 * c + h), v = RAW ? in.vs[RAW ? 2 * c + h : 0] * unit : 0.0f;
 #pragma unroll
-                for (int i = 8 * h; i < 8 * h + 8; i++) {
-                  float2 y = make_float2(__uint_as_float(z[2 * i]), __uint_as_float(z[2 * i + 1]));
-                  y = RAW ? fma2(y, make_float2(f, f), make_float2(base, base)) : add2(y, make_float2(base, base));
-                  y = make_float2(ex2(y.x), ex2(y.y));
-                  sums[i & 3] = add2(sums[i & 3], y);
-                  if (RAW) {
-                    y = mul2(y, make_float2(v, v));
-                  } else {
-                    const float2 v2 = *reinterpret_cast<const float2 *>(&in.vs[RAW ? 0 : 32 * c + 2 * i]);
-                    y = mul2(y, make_float2(v2.x * unit, v2.y * unit));
-                  }
-                  pk[i] = pack<false>(y.x, y.y);
+              for (int i = 8 * h; i < 8 * h + 8; i++) {
+                float2 y = make_float2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1]));
+                y = RAW ? fma2(y, make_float2(f, f), make_float2(base, base)) : add2(y, make_float2(base, base));
+                y = make_float2(ex2(y.x), ex2(y.y));
+                sums[i & 3] = add2(sums[i & 3], y);
+                if (RAW) {
+                  y = mul2(y, make_float2(v, v));
+                } else {
+                  const float2 v2 = *reinterpret_cast<const float2 *>(&in.vs[RAW ? 0 : 32 * c + 2 * i]);
+                  y = mul2(y, make_float2(v2.x * unit, v2.y * unit));
                 }
+                pk[i] = pack<false>(y.x, y.y);
               }
-              if (c < 3) tm_landed(x[k ^ 1]);  // (P lies over the columns that have been read)
-              tm_store16(s_at + 16 * c, pk);
             }
-            tm_wait_st();  // half of P is there
-            tm_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(&sm.p_full[t][c2 >> 1]);
+            tm_store16(s_at + 16 * c, pk);
+            if (c & 1) {  // half of P is there
+              tm_wait_st();
+              tm_before();
+              __syncwarp();
+              if (lane == 0) bar_arrive(&sm.p_full[t][c >> 1]);
+            }
           }
           l = add2(l, add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
         }
