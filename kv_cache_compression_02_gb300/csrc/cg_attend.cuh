@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(kThreads, Shape<NB>::kPerSM) k_attend(const __
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
   asm volatile("griddepcontrol.launch_dependents;");
+  if (OWN) status_cleared();  // launched early, behind the plan that makes a.first
   if (threadIdx.x == 0) {
     sm.errors = sm.dead = 0;
     a.notes[blockIdx.x].parts = 0;
@@ -1036,7 +1037,12 @@ cudaError_t launch_kernels(const AttendArgs &a, unsigned grid, cudaStream_t st) 
   constexpr int kSmem = int(sizeof(Smem<D, NB>));
   const cudaError_t e = cudaFuncSetAttribute(k_attend<FMT, D, NB, BF16, PLAIN, OWN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  k_attend<FMT, D, NB, BF16, PLAIN, OWN><<<grid, kThreads, kSmem, st>>>(a);
+  if (OWN) {
+    const cudaError_t e1 = launch_early(k_attend<FMT, D, NB, BF16, PLAIN, OWN>, dim3(grid), dim3(kThreads), kSmem, st, a);
+    if (e1 != cudaSuccess) return e1;
+  } else {
+    k_attend<FMT, D, NB, BF16, PLAIN, OWN><<<grid, kThreads, kSmem, st>>>(a);
+  }
   const cudaError_t e2 = launch_early(k_join<D, NB, BF16, OWN>, dim3(grid, unsigned((min(8 * NB, a.rows) + 3) / 4)), dim3(128), 0, st, a);
   return e2 != cudaSuccess ? e2 : cudaGetLastError();
 }

@@ -57,7 +57,7 @@ struct Note {
   uint32_t errors;
   int32_t parts;   // of the item that this CTA has the first but not the last part of, or 0
   int32_t second;  // the first part is in this CTA's second slot
-  int32_t g, h, q;
+  int32_t e0, row0, rows, head;  // as in Todo
 };
 
 struct SharedArgs {
@@ -71,7 +71,7 @@ struct SharedArgs {
   uint32_t *status, *bad;
   int32_t *owner, *first;  // of a sequence: its entry in the groups, and the pages that it shares
   int32_t *seq;            // of an entry: its sequence, or -1
-  int32_t *keys, *lead;    // of a group: its positions (0: nothing to do), and an entry whose row of the table has them
+  int32_t *keys, *lead;    // of a group: its positions (0: nothing to do), and a sequence whose row of the table has them
   float *own, *own_ml;
   Note *notes;
   float *parts;  // [2 * kGrid][kRows][D + 2]
@@ -120,12 +120,17 @@ struct Smem {
 // new token of the sequence sees the whole prefix; the others read their
 // positions by themselves.
 __global__ void __launch_bounds__(kPlan) k_shared_plan(const SharedArgs a) {
-  for (int b = threadIdx.x; b < a.B; b += kPlan) a.owner[b] = 0x7fffffff, a.first[b] = 0;
+  asm volatile("griddepcontrol.launch_dependents;");
+  constexpr int kKept = 8192;  // sequences whose entries are kept here (64 of them: 4.6 us, in global memory 5.0)
+  __shared__ int s_owner[kKept];
+  int *const owner = a.B <= kKept ? s_owner : a.owner;
+  for (int b = threadIdx.x; b < a.B; b += kPlan) owner[b] = 0x7fffffff, a.first[b] = 0;
   bool bad = false, fall = false;
   for (int g = threadIdx.x; g < a.n_groups; g += kPlan) {
+    const int e0 = a.cu[g], e1 = a.cu[g + 1], pages = a.shared[g];
     a.keys[g] = 0, a.lead[g] = 0x7fffffff;
-    fall |= a.cu[g] < 0 || a.cu[g + 1] < a.cu[g] || a.cu[g + 1] > a.n_members;
-    bad |= a.shared[g] < 0 || a.shared[g] > a.stride;
+    fall |= e0 < 0 || e1 < e0 || e1 > a.n_members;
+    bad |= pages < 0 || pages > a.stride;
   }
   fall = __syncthreads_or(fall);
   if (!fall) {
@@ -133,7 +138,7 @@ __global__ void __launch_bounds__(kPlan) k_shared_plan(const SharedArgs a) {
     for (int e = e0 + threadIdx.x; e < e1; e += kPlan) {
       const int b = a.member[e];
       if (uint32_t(b) < uint32_t(a.B))
-        atomicMin(&a.owner[b], e);
+        atomicMin(&owner[b], e);
       else
         bad = true;
     }
@@ -142,9 +147,10 @@ __global__ void __launch_bounds__(kPlan) k_shared_plan(const SharedArgs a) {
       const int b = a.member[e];
       int takes = -1;
       if (uint32_t(b) < uint32_t(a.B)) {
-        if (__ldcg(&a.owner[b]) != e) {
+        if (*static_cast<volatile int *>(&owner[b]) != e) {
           bad = true;
         } else {
+          const int64_t len = max(int64_t(0), min(int64_t(a.len[b]), int64_t(a.stride) * a.bt));
           int g = 0, hi = a.n_groups;  // the last group that begins at or before e
           while (hi - g > 1) {
             const int mid = g + (hi - g) / 2;
@@ -154,12 +160,12 @@ __global__ void __launch_bounds__(kPlan) k_shared_plan(const SharedArgs a) {
               hi = mid;
           }
           const int pages = a.shared[g];
-          const int64_t keys = int64_t(pages) * a.bt, len = max(int64_t(0), min(int64_t(a.len[b]), int64_t(a.stride) * a.bt));
+          const int64_t keys = int64_t(pages) * a.bt;
           if (pages > 0 && pages <= a.stride && len - a.T + 1 >= keys) {
             takes = b;
             a.first[b] = pages;
             a.keys[g] = int(keys);
-            atomicMin(&a.lead[g], e);
+            atomicMin(&a.lead[g], b);
           }
         }
       }
@@ -390,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
                 todo.slot = c0 == c1 ? -1 : 2 * int(blockIdx.x) + (seg > 0);  // slot 1: the run's last part
                 if (c0 != c1 && int64_t(blockIdx.x) == c0) {
                   Note &note = a.notes[blockIdx.x];
-                  note.parts = int(c1 - c0 + 1), note.second = seg > 0, note.g = p.g, note.h = p.h, note.q = p.q;
+                  note.parts = int(c1 - c0 + 1), note.second = seg > 0, note.e0 = todo.e0, note.row0 = todo.row0, note.rows = todo.rows, note.head = p.h;
                 }
               }
               bar_arrive(&sm.todo_full[turn]);
@@ -402,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
           }
           if (!more) break;
           const int keys = a.keys[p.g];
-          const int32_t *row = a.table + int64_t(a.seq[a.lead[p.g]]) * a.stride;
+          const int32_t *row = a.table + int64_t(a.lead[p.g]) * a.stride;
           constexpr int kEach = Info<RAW>::kEach, kCount = Info<RAW>::kCount, kMine = (kCount + 31) / 32;
           int page[kMine], at[kMine];  // of the warp's next tile
           auto look = [&](int j) {
@@ -607,15 +613,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
           const Info<RAW> &in = sm.info[is_v ? v_slot : k_slot];
           if (!(ok = bar_wait(&sm.info_full[is_v ? v_slot : k_slot], is_v ? v_phase : k_phase, &sm.dead))) break;
           if (RAW && !(ok = bar_wait(&sm.raw_full[at], raw_phase, &sm.dead))) break;
-          if (!(ok = bar_wait(&sm.kv_empty[stage], kv_phase, &sm.dead))) break;
           const uint8_t *pool = is_v ? a.vp : a.kp, *from = sm.raw[RAW ? at : 0] + r0 * D + u * 8;
           const bool there = u * 8 < a.d, whole = in.whole;
           uint8_t *to = sm.kv[stage][u >> 3] + r0 * 128 + (((u & 7) ^ (r0 & 7)) << 4);  // (kStep is a multiple of 8)
+          constexpr int kBatch = RAW ? kUnits : 8;  // (codes from shared memory: all of them before the wait; from global memory: 8)
 #pragma unroll 1
-          for (int h = 0; h < kUnits; h += 8) {
-            uint2 w[8];
+          for (int h = 0; h < kUnits; h += kBatch) {
+            uint2 w[kBatch];
 #pragma unroll
-            for (int k = 0; k < 8; k++) {
+            for (int k = 0; k < kBatch; k++) {
               const int r = (h + k) * kStep;
               if (RAW) {
                 w[k] = *reinterpret_cast<const uint2 *>(from + r * D);
@@ -624,22 +630,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
                 w[k] = there && begin >= 0 ? *reinterpret_cast<const uint2 *>(pool + begin + u * 8) : make_uint2(0, 0);
               }
             }
-            if (RAW && !whole) {  // nothing was copied there
+            if (RAW) {
+              if (!whole) {  // nothing was copied there
 #pragma unroll
-              for (int k = 0; k < 8; k++) {
-                const int r = r0 + (h + k) * kStep;
-                if (!(in.valid[r / 32] >> (r & 31) & 1)) w[k] = make_uint2(0, 0);
+                for (int k = 0; k < kBatch; k++) {
+                  const int r = r0 + (h + k) * kStep;
+                  if (!(in.valid[r / 32] >> (r & 31) & 1)) w[k] = make_uint2(0, 0);
+                }
               }
+              __syncwarp();
+              if (lane == 0) bar_arrive(&sm.raw_empty[at]);
             }
+            if (h == 0 && !(ok = bar_wait(&sm.kv_empty[stage], kv_phase, &sm.dead))) break;
 #pragma unroll
-            for (int k = 0; k < 8; k++) *reinterpret_cast<uint4 *>(to + (h + k) * kStep * 128) = operands_of<FMT>(w[k]);
+            for (int k = 0; k < kBatch; k++) *reinterpret_cast<uint4 *>(to + (h + k) * kStep * 128) = operands_of<FMT>(w[k]);
           }
+          if (!ok) break;
           fence_async();
           __syncwarp();
-          if (lane == 0) {
-            bar_arrive(&sm.kv_full[stage]);
-            if (RAW) bar_arrive(&sm.raw_empty[at]);
-          }
+          if (lane == 0) bar_arrive(&sm.kv_full[stage]);
           if (++stage == kStages) stage = 0, kv_phase ^= 1;
           if (++at == kRaw) at = 0, raw_phase ^= 1;
           if (is_v) {
@@ -928,9 +937,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
 }
 
 // Joins the parts of items that several CTAs had, with what each sequence has
-// to itself: eight rows a CTA, four channels a thread.
+// to itself: eight rows a CTA, four channels a thread.  First the rows' maxima
+// and sums, then the outputs, eight parts' loads in flight.
 template <int D>
-__global__ void __launch_bounds__(2 * D, 2048 / (2 * D)) k_shared_join(const __grid_constant__ SharedArgs a) {
+__global__ void __launch_bounds__(2 * D) k_shared_join(const __grid_constant__ SharedArgs a) {
   status_cleared();
   if (blockIdx.x == 0 && blockIdx.y == 0) {  // the status of the call, with that of the kernels before
     __shared__ uint32_t s_errors;
@@ -943,46 +953,43 @@ __global__ void __launch_bounds__(2 * D, 2048 / (2 * D)) k_shared_join(const __g
     if (threadIdx.x == 0 && s_errors) atomicOr(a.status, s_errors);
   }
   const Note note = a.notes[blockIdx.x];
-  if (note.parts == 0) return;
-  const int r = blockIdx.y * 8 + threadIdx.x % 8, c = threadIdx.x / 8, e0 = a.cu[note.g], row = note.q * kRows + r;
-  if (row >= (a.cu[note.g + 1] - e0) * a.TG) return;
-  const int b = a.seq[e0 + row / a.TG];
-  if (b < 0) return;
-  const int64_t at = (int64_t(b) * a.T + row % a.TG / a.G) * a.Hq + note.h * a.G + row % a.G;
+  if (note.parts == 0 || note.row0 + int(blockIdx.y) * 8 >= note.rows) return;
+  const int rr = threadIdx.x % 8, r = blockIdx.y * 8 + rr, c = threadIdx.x / 8, row = note.row0 + r;
+  const int b = row < note.rows ? a.seq[note.e0 + row / a.TG] : -1;
   auto part = [&](int i) { return a.parts + (2 * (int64_t(blockIdx.x) + i) + (i == 0 ? note.second : 0)) * kRows * (D + 2); };
-  float top = __ldcg(&a.own_ml[2 * at]), sum = __ldcg(&a.own_ml[2 * at + 1]), y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (top != -INFINITY && c * 4 < a.d) {
-    const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.own + at * a.d + c * 4));
-    y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
+  __shared__ float s_m[kGrid][8], s_l[kGrid][8];  // of each part
+  for (int i = c; i < note.parts; i += D / 4) {
+    const float *p = part(i);
+    s_m[i][rr] = __ldcg(p + kRows * D + r), s_l[i][rr] = __ldcg(p + kRows * (D + 1) + r);
   }
-  for (int base = 0; base < note.parts; base += 2) {
-    float m[2], l[2], now = top;
-    float4 v[2];
+  const int64_t at = b >= 0 ? (int64_t(b) * a.T + row % a.TG / a.G) * a.Hq + note.head * a.G + row % a.G : 0;
+  const float own_m = b >= 0 ? __ldcg(&a.own_ml[2 * at]) : -INFINITY, own_l = b >= 0 ? __ldcg(&a.own_ml[2 * at + 1]) : 0.0f;
+  float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (own_m != -INFINITY && c * 4 < a.d) y = __ldcg(reinterpret_cast<const float4 *>(a.own + at * a.d + c * 4));
+  __syncthreads();
+  float top = own_m;
+  for (int i = 0; i < note.parts; i++) top = fmaxf(top, s_m[i][rr]);
+  const float own_w = own_m == -INFINITY ? 0.0f : ex2(own_m - top);
+  float sum = own_l * own_w;
+  for (int i = 0; i < note.parts; i++) sum += s_l[i][rr] * (s_m[i][rr] == -INFINITY ? 0.0f : ex2(s_m[i][rr] - top));
+  if (b < 0) return;
+  y.x *= own_w, y.y *= own_w, y.z *= own_w, y.w *= own_w;
+  for (int base = 0; base < note.parts; base += 8) {
+    float4 v[8];
 #pragma unroll
-    for (int i = 0; i < 2; i++)
+    for (int i = 0; i < 8; i++)
+      if (base + i < note.parts) v[i] = __ldcg(reinterpret_cast<const float4 *>(part(base + i)) + c * kRows + r);
+#pragma unroll
+    for (int i = 0; i < 8; i++)
       if (base + i < note.parts) {
-        const float *p = part(base + i);
-        m[i] = __ldcg(p + kRows * D + r), l[i] = __ldcg(p + kRows * (D + 1) + r);
-        v[i] = __ldcg(reinterpret_cast<const float4 *>(p) + c * kRows + r);
-        now = fmaxf(now, m[i]);
-      }
-    const float keep = top == -INFINITY ? 0.0f : ex2(top - now);
-    top = now;
-    sum *= keep;
-#pragma unroll
-    for (int k = 0; k < 4; k++) y[k] *= keep;
-#pragma unroll
-    for (int i = 0; i < 2; i++)
-      if (base + i < note.parts) {
-        const float w = m[i] == -INFINITY ? 0.0f : ex2(m[i] - now);
-        sum += w * l[i];
-        y[0] += w * v[i].x, y[1] += w * v[i].y, y[2] += w * v[i].z, y[3] += w * v[i].w;
+        const float m = s_m[base + i][rr], w = m == -INFINITY ? 0.0f : ex2(m - top);
+        y.x += w * v[i].x, y.y += w * v[i].y, y.z += w * v[i].z, y.w += w * v[i].w;
       }
   }
   const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
   if (c * 4 < a.d) {
-    const uint2 w = a.bf16 ? make_uint2(pack<true>(y[0] * f, y[1] * f), pack<true>(y[2] * f, y[3] * f))
-                           : make_uint2(pack<false>(y[0] * f, y[1] * f), pack<false>(y[2] * f, y[3] * f));
+    const uint2 w = a.bf16 ? make_uint2(pack<true>(y.x * f, y.y * f), pack<true>(y.z * f, y.w * f))
+                           : make_uint2(pack<false>(y.x * f, y.y * f), pack<false>(y.z * f, y.w * f));
     *reinterpret_cast<uint2 *>(a.out + at * a.d + c * 4) = w;
   }
   if (c == 0 && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (top - kOwnLift + log2f(sum)) * 0.6931471805599453f;
