@@ -15,8 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libcachegen.so")
 SOURCES = ["cg_api.cu", "cg_fit.cu", "cg_encode.cu", "cg_decode.cu", "cg_noalloc.cu", "cg_plan.cu", "cg_assemble.cu",
-           "cg_cache_write.cu", "cg_cache_attend.cu", "cg_prompt.cu", "cg_pages.cu", "cg_shared.cu", "cg_shared_own.cu"]
-HEADERS = ["cg_layout.cuh", "cg_kernels.cuh", "cg_args.h", "cg_cache.cuh", "cg_tma.cuh", "cg_tc.cuh", "cg_attend.cuh", "cg_shared.cuh"]
+           "cg_cache_write.cu", "cg_cache_attend.cu", "cg_prompt.cu", "cg_pages.cu", "cg_shared.cu", "cg_shared_own.cu", "cg_cross_few.cu"]
+HEADERS = ["cg_layout.cuh", "cg_kernels.cuh", "cg_args.h", "cg_cache.cuh", "cg_tma.cuh", "cg_tc.cuh", "cg_attend.cuh", "cg_shared.cuh", "cg_cross_few.cuh"]
 ABI = ["cachegen.h", "cachegen_cache.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -43,6 +43,7 @@
 // keys: 82 us.  Rows of up to 64 channels have operands of 64 (8192 tokens, d =
 // 64: 278 us; padded to 128 they take 360).
 #include "cg_cache.cuh"
+#include "cg_cross_few.cuh"
 #include "cg_tc.cuh"
 #include "cg_tma.cuh"
 
@@ -841,20 +842,6 @@ int padded(int d) { return d <= 64 ? 64 : 128; }
 // the status word, then the notes
 constexpr uint64_t kNotes = 256 + ((sizeof(Note) * kGrid + 255) & ~uint64_t(255));
 
-// A map of rows of d elements with two strides, in boxes of 64 x n1 x n2.
-bool make_map(CUtensorMap *map, const void *base, int d, int64_t size1, int64_t stride1, int n1, int64_t size2, int64_t stride2, int n2) {
-  const EncodeTiled encode = encode_tiled();
-  if (!encode) return false;
-  // an extent of one needs no stride, but the map wants a positive one
-  if (size1 == 1) stride1 = d;
-  if (size2 == 1) stride2 = d;
-  const cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(size1), cuuint64_t(size2)};
-  const cuuint64_t strides[2] = {cuuint64_t(2 * stride1), cuuint64_t(2 * stride2)};
-  const cuuint32_t box[3] = {64, cuuint32_t(n1), cuuint32_t(n2)}, ones[3] = {1, 1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D, bool BF16, bool CROSS>
 cudaError_t launch(const PromptArgs &a, unsigned grid, cudaStream_t st) {
   constexpr int kSmem = int(sizeof(Smem<D>));
@@ -866,7 +853,10 @@ cudaError_t launch(const PromptArgs &a, unsigned grid, cudaStream_t st) {
   return e2 != cudaSuccess ? e2 : cudaGetLastError();
 }
 
-size_t workspace_bytes(const cg_prompt &p) { return size_t(kNotes + 4 * uint64_t(2 * kGrid) * kRows * (padded(p.d) + 2)); }
+size_t workspace_bytes(const cg_prompt &p) {
+  const uint64_t bytes = kNotes + 4 * uint64_t(2 * kGrid) * kRows * (padded(p.d) + 2);
+  return size_t(bytes > few_bytes(p) ? bytes : few_bytes(p));
+}
 
 // Both calls: k_first is cu_k, or (CROSS) where each sequence's keys begin.
 template <bool CROSS>
@@ -906,6 +896,8 @@ cg_status attend(const cg_prompt *prompt, const void *q_dev, const void *k_dev, 
   }
   if (!ok) return CG_ERR_INVALID_ARG;  // strides that a tensor map cannot have
   const bool bf16 = p.dtype == CG_BF16;
+  if (CROSS && int64_t(p.max_q) * a.G <= kFewRows)
+    return cross_few(p, q_dev, k_dev, v_dev, cu_q_dev, k_first_dev, k_len_dev, out_dev, lse_dev, ws, st);
   const cudaError_t e = p.d <= 64 ? (bf16 ? launch<64, true, CROSS>(a, kGrid, st) : launch<64, false, CROSS>(a, kGrid, st))
                                   : (bf16 ? launch<128, true, CROSS>(a, kGrid, st) : launch<128, false, CROSS>(a, kGrid, st));
   return e == cudaSuccess ? CG_OK : CG_ERR_CUDA;

@@ -611,8 +611,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
         for (int i = 0; i < 2 * n; i++) {
           const bool is_v = i == 2 * n - 1 || (i > 0 && i % 2 == 0);
           const Info<RAW> &in = sm.info[is_v ? v_slot : k_slot];
-          if (!(ok = bar_wait(&sm.info_full[is_v ? v_slot : k_slot], is_v ? v_phase : k_phase, &sm.dead))) break;
-          if (RAW && !(ok = bar_wait(&sm.raw_full[at], raw_phase, &sm.dead))) break;
+          if (RAW) {  // (who had the codes copied has seen the tile's pages)
+            if (!(ok = bar_wait(&sm.raw_full[at], raw_phase, &sm.dead))) break;
+          } else {
+            if (!(ok = bar_wait(&sm.info_full[is_v ? v_slot : k_slot], is_v ? v_phase : k_phase, &sm.dead))) break;
+          }
           const uint8_t *pool = is_v ? a.vp : a.kp, *from = sm.raw[RAW ? at : 0] + r0 * D + u * 8;
           const bool there = u * 8 < a.d, whole = in.whole;
           uint8_t *to = sm.kv[stage][u >> 3] + r0 * 128 + (((u & 7) ^ (r0 & 7)) << 4);  // (kStep is a multiple of 8)

@@ -28,6 +28,20 @@ inline EncodeTiled encode_tiled() {
   return fn;
 }
 
+// A map of rows of d elements with two strides, in boxes of 64 x n1 x n2.
+inline bool make_map(CUtensorMap *map, const void *base, int d, int64_t size1, int64_t stride1, int n1, int64_t size2, int64_t stride2, int n2) {
+  const EncodeTiled encode = encode_tiled();
+  if (!encode) return false;
+  // an extent of one needs no stride, but the map wants a positive one
+  if (size1 == 1) stride1 = d;
+  if (size2 == 1) stride2 = d;
+  const cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(size1), cuuint64_t(size2)};
+  const cuuint64_t strides[2] = {cuuint64_t(2 * stride1), cuuint64_t(2 * stride2)};
+  const cuuint32_t box[3] = {64, cuuint32_t(n1), cuuint32_t(n2)}, ones[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 __device__ inline uint32_t smem_of(const void *p) { return uint32_t(__cvta_generic_to_shared(p)); }
 
 __device__ inline void bar_init(uint64_t *bar, int count) {

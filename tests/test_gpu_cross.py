@@ -76,6 +76,22 @@ CASES = {
     "long_states": (F16, 2, 1, 128, [40], [3], [6000]),
     "many_sequences": (BF16, 2, 1, 16, [(5 * i) % 7 for i in range(900)], [i for i in range(900)], [(3 * i) % 11 for i in range(900)]),
     "whole_tiles": (BF16, 4, 2, 64, [64, 130], [128, 0], [256, 384]),
+    # up to 16 rows of a KV head: another kernel
+    "few_one_key": (F16, 1, 1, 128, [1], [5], [1]),
+    "few_one_tile": (BF16, 2, 2, 128, [1, 2], [0, 32], [32, 32]),
+    "few_8_rows": (F16, 16, 2, 128, [1, 1, 1], [0, 40, 3], [333, 31, 1000]),
+    "few_9_rows": (BF16, 9, 1, 128, [1], [7], [700]),
+    "few_16_rows": (F16, 8, 2, 128, [4, 1, 0, 3], [0, 100, 5, 2], [901, 33, 600, 0]),
+    "few_d64_5_beams": (BF16, 6, 2, 64, [5, 4, 5, 1, 0], [0, 0, 0, 77, 77], [500, 500, 500, 64, 65]),
+    "few_d8": (F16, 3, 3, 8, [2, 1], [1, 0], [70, 33]),
+    "few_d16": (BF16, 8, 1, 16, [2, 1], [1, 0], [70, 33]),
+    "few_d40": (F16, 4, 2, 40, [3, 1, 2], [0, 9, 100], [257, 0, 31]),
+    "few_d72": (BF16, 5, 5, 72, [7], [0], [300]),
+    "few_d120": (BF16, 12, 4, 120, [3, 5], [4, 0], [260, 95]),
+    "few_long": (F16, 8, 1, 128, [2], [1], [30000]),
+    "few_long_d64": (BF16, 4, 2, 64, [1], [0], [40001]),
+    "few_many": (F16, 4, 4, 64, [1 + i % 3 for i in range(1500)], [3 * i for i in range(1500)], [(7 * i) % 100 for i in range(1500)]),
+    "few_without_keys": (F16, 4, 2, 64, [1, 2, 1], [0, 0, 4], [0, 0, 0]),
 }
 
 
@@ -92,12 +108,14 @@ def test_cross(name):
     assert torch.isfinite(out).all() and not torch.isnan(z).any()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cu", [[0, 3, 5, 70, 71, 200], [0, 3, 5, 6, 13, 20]])
 @pytest.mark.parametrize("dt", [F16, BF16])
-def test_what_a_sequence_does_not_see_does_not_matter(dt):
+def test_what_a_sequence_does_not_see_does_not_matter(dt, cu, d):
     """NaN and infinities behind a sequence's last key, of padded and of other sequences' keys."""
-    H, d, width, count = 2, 64, 200, [130, 0, 200, 1, 128]
-    begin, cu = [width * i for i in range(5)], [0, 3, 5, 70, 71, 200]
-    q, k, v = rows(200, 4, d, dt, 4), rows(5 * width, H, d, dt, 5, True), rows(5 * width, H, d, dt, 6)
+    H, width, count = 2, 200, [130, 0, 200, 1, 128]
+    begin = [width * i for i in range(5)]
+    q, k, v = rows(cu[-1], 4, d, dt, 4), rows(5 * width, H, d, dt, 5, True), rows(5 * width, H, d, dt, 6)
     for b, n in enumerate(count):
         for x, bad in ((k, math.nan), (v, math.inf)):
             x[begin[b] + n:begin[b] + width] = bad
@@ -107,48 +125,52 @@ def test_what_a_sequence_does_not_see_does_not_matter(dt):
     check(out, z, q, k, v, cu, begin, count, 0.2)
 
 
-def test_values_that_are_seen_count():
+@pytest.mark.parametrize("n", [2, 40])
+def test_values_that_are_seen_count(n):
     """An Inf or NaN among the keys' values that a row does see reaches the row, in its channel."""
-    q, k, v = rows(3, 2, 64, F16, 7), rows(150, 1, 64, F16, 8), rows(150, 1, 64, F16, 9)
+    q, k, v = rows(n + 1, 2, 64, F16, 7), rows(150, 1, 64, F16, 8), rows(150, 1, 64, F16, 9)
     v[140, 0, 5], v[3, 0, 9], v[149, 0, 11] = math.inf, math.nan, -math.inf
-    out, _, st = run(q.cuda(), k.cuda(), v.cuda(), [0, 2, 3], [0, 0], [150, 140], 0.1)
+    out, _, st = run(q.cuda(), k.cuda(), v.cuda(), [0, n, n + 1], [0, 0], [150, 140], 0.1)
     out = out.cpu()
     assert st == cg.CG_OK
-    assert (out[:2, :, 5] == math.inf).all() and (out[:2, :, 11] == -math.inf).all() and torch.isnan(out[:, :, 9]).all()
-    assert torch.isfinite(out[2, :, 5]).all() and torch.isfinite(out[2, :, 11]).all()
+    assert (out[:n, :, 5] == math.inf).all() and (out[:n, :, 11] == -math.inf).all() and torch.isnan(out[:, :, 9]).all()
+    assert torch.isfinite(out[n, :, 5]).all() and torch.isfinite(out[n, :, 11]).all()
 
 
-def test_strided_rows_no_lse_and_rows_of_no_sequence():
+@pytest.mark.parametrize("cu", [[2, 9, 17], [2, 9, 40]])
+def test_strided_rows_no_lse_and_rows_of_no_sequence(cu):
     """The codec's layout [H][S][d], queries between other heads, queries before and behind those of the sequences."""
-    H, d, n = 2, 64, 333
+    H, d, n, last = 2, 64, 333, cu[-1]
     kv = torch.randn(2, H, n, d, generator=torch.Generator().manual_seed(1)).half()
     k, v = kv[0].transpose(0, 1), kv[1].transpose(0, 1)
-    wide = torch.full((20, 7, d), math.nan, dtype=F16)
-    wide[:, 1:5] = rows(20, 4, d, F16, 2)
+    wide = torch.full((50, 7, d), math.nan, dtype=F16)
+    wide[:, 1:5] = rows(50, 4, d, F16, 2)
     w, kvd = wide.cuda(), kv.cuda()
-    out, _, st = run(w[:, 1:5], kvd[0].transpose(0, 1), kvd[1].transpose(0, 1), [2, 9, 17], [5, 0], [300, 333], 0.1, lse=False)
-    assert st == cg.CG_OK and torch.isnan(out[:2]).all() and torch.isnan(out[17:]).all()
-    want, z, _ = run(wide[:, 1:5].contiguous().cuda(), k.contiguous().cuda(), v.contiguous().cuda(), [2, 9, 17], [5, 0], [300, 333], 0.1)
-    assert torch.equal(out[2:17], want[2:17])
-    check(want, z, wide[:, 1:5], k, v, [2, 9, 17], [5, 0], [300, 333], 0.1)
+    out, _, st = run(w[:, 1:5], kvd[0].transpose(0, 1), kvd[1].transpose(0, 1), cu, [5, 0], [300, 333], 0.1, lse=False)
+    assert st == cg.CG_OK and torch.isnan(out[:2]).all() and torch.isnan(out[last:]).all()
+    want, z, _ = run(wide[:, 1:5].contiguous().cuda(), k.contiguous().cuda(), v.contiguous().cuda(), cu, [5, 0], [300, 333], 0.1)
+    assert torch.equal(out[2:last], want[2:last])
+    check(want, z, wide[:, 1:5], k, v, cu, [5, 0], [300, 333], 0.1)
 
 
-def test_bad_sequences_are_left_out():
+@pytest.mark.parametrize("most", [None, 12])
+def test_bad_sequences_are_left_out(most):
+    """(more than 16 rows of a KV head might come where `most` says so)"""
     q, k, v = rows(12, 2, 64, F16, 1), rows(100, 1, 64, F16, 2), rows(100, 1, 64, F16, 3)
     d = (q.cuda(), k.cuda(), v.cuda())
     cu = [0, 2, 4, 6, 8, 10, 12]
     big = 2 ** 31 - 1
     for begin, count, bad in (([0, -1, 0, 0, 0, 50], [100, 5, -1, 101, 90, 51], [1, 2, 3, 5]), ([0, big, 0, 99, 100, 5], [1, 1, big, 1, 0, big], [1, 2, 5])):
-        out, z, st = run(*d, cu, begin, count, 0.1, max_k=100)
+        out, z, st = run(*d, cu, begin, count, 0.1, max_q=most, max_k=100)
         assert st == cg.CG_ERR_INVALID_ARG
         for b in range(6):
             if b in bad:
                 assert torch.isnan(out[2 * b:2 * b + 2]).all() and torch.isnan(z[2 * b:2 * b + 2]).all()
         check(out, z, q, k, v, cu, begin, count, 0.1, [b for b in range(6) if b not in bad])
-    out, z, st = run(*d, cu, [0] * 6, [10, 20, 30, 31, 30, 1], 0.1, max_k=30)
+    out, z, st = run(*d, cu, [0] * 6, [10, 20, 30, 31, 30, 1], 0.1, max_q=most, max_k=30)
     assert st == cg.CG_ERR_INVALID_ARG and torch.isnan(out[6:8]).all()
     for bad_cu in ([0, 2, 1, 6, 8, 10, 12], [0, 2, 4, 6, 8, 10, 13], [-1, 2, 4, 6, 8, 10, 12]):
-        assert run(*d, bad_cu, [0] * 6, [9] * 6, 0.1, max_q=20)[2] == cg.CG_ERR_INVALID_ARG
+        assert run(*d, bad_cu, [0] * 6, [9] * 6, 0.1, max_q=20 if most else 8)[2] == cg.CG_ERR_INVALID_ARG
     assert run(*d, [0, 5, 5, 5, 5, 5, 12], [0] * 6, [9] * 6, 0.1, max_q=6)[2] == cg.CG_ERR_INVALID_ARG
 
 
@@ -166,14 +188,16 @@ def test_no_queries_and_no_keys():
     assert cg.cg_read_status(ws) == cg.CG_OK and (out == 0).all() and (z == -math.inf).all()
 
 
-def test_repeats_other_stream_graph_and_two_calls_at_once():
-    q, k, v = (x.cuda() for x in (rows(90, 8, 128, BF16, 1), rows(3000, 2, 128, BF16, 2, True), rows(3000, 2, 128, BF16, 3)))
-    args = ([0, 77, 90], [0, 100], [3000, 2000], 0.1)
+@pytest.mark.parametrize("nq", [[77, 13], [3, 4]])
+def test_repeats_other_stream_graph_and_two_calls_at_once(nq):
+    n = sum(nq)
+    q, k, v = (x.cuda() for x in (rows(n, 8, 128, BF16, 1), rows(3000, 2, 128, BF16, 2, True), rows(3000, 2, 128, BF16, 3)))
+    args = ([0, nq[0], n], [0, 100], [3000, 2000], 0.1)
     want, zw, _ = run(q, k, v, *args)
     side = torch.cuda.Stream()
     got, z, st = run(q, k, v, *args, stream=side)
     assert st == cg.CG_OK and torch.equal(got, want) and torch.equal(z, zw)
-    p = cg.Prompt(2, 8, 2, 128, cg.CG_BF16, 90, 3000, 77, 3000, 0.1, q.stride()[:2], k.stride()[:2], v.stride()[:2])
+    p = cg.Prompt(2, 8, 2, 128, cg.CG_BF16, n, 3000, max(nq), 3000, 0.1, q.stride()[:2], k.stride()[:2], v.stride()[:2])
     ws = [cg.empty_u8(cg.cg_prompt_workspace_bytes(p)) for _ in range(2)]
     outs = [torch.zeros_like(q) for _ in range(2)]
     cu, begin, count = i32(args[0]), i32(args[1]), i32(args[2])
