@@ -421,13 +421,13 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_few(const __grid_cons
 }
 
 // Joins the parts of items that several warps had: a CTA per warp that has the
-// first part of such an item; a warp per row, four channels a lane, eight parts'
-// loads in flight.  It is launched with the first kernel and waits for its end here.
+// first part of such an item, and four rows; a warp per row, four channels a
+// lane, eight parts' loads in flight.  It is launched with the first kernel and waits for its end here.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(128) k_few_join(const __grid_constant__ FewArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (blockIdx.x == 0) {  // the status of the call
+  if (blockIdx.x == 0 && blockIdx.y == 0) {  // the status of the call
     uint32_t e = 0;
     for (int i = threadIdx.x; i < int(kSMs); i += 128) e |= __ldcg(&a.errors[i]);
     __shared__ uint32_t s_errors;
@@ -441,45 +441,45 @@ __global__ void __launch_bounds__(128) k_few_join(const __grid_constant__ FewArg
   if (note.parts == 0) return;
   const int q0 = a.cu_q[note.b], rows = (a.cu_q[note.b + 1] - q0) * a.G;
   auto part = [&](int i) { return a.parts + (2 * (int64_t(blockIdx.x) + i) + (i == 0 ? note.second : 0)) * kFewRows * (D + 2); };
-  for (int r = warp; r < rows; r += 4) {
-    float top = -INFINITY, sum = 0.0f, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int base = 0; base < note.parts; base += 32) {
-      const int n = min(32, note.parts - base);
-      float m = -INFINITY, l = 0.0f;  // lane i: of part base + i
-      if (lane < n) m = __ldcg(part(base + lane) + kFewRows * D + r), l = __ldcg(part(base + lane) + kFewRows * (D + 1) + r);
-      float now = m;
+  const int r = blockIdx.y * 4 + warp;
+  if (r >= rows) return;
+  float top = -INFINITY, sum = 0.0f, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int base = 0; base < note.parts; base += 32) {
+    const int n = min(32, note.parts - base);
+    float m = -INFINITY, l = 0.0f;  // lane i: of part base + i
+    if (lane < n) m = __ldcg(part(base + lane) + kFewRows * D + r), l = __ldcg(part(base + lane) + kFewRows * (D + 1) + r);
+    float now = m;
 #pragma unroll
-      for (int o = 16; o; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
-      now = fmaxf(now, top);
-      const float keep = top == -INFINITY ? 0.0f : ex2(top - now);
-      const float w = m == -INFINITY ? 0.0f : ex2(m - now);
-      top = now;
-      sum *= keep;
+    for (int o = 16; o; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
+    now = fmaxf(now, top);
+    const float keep = top == -INFINITY ? 0.0f : ex2(top - now);
+    const float w = m == -INFINITY ? 0.0f : ex2(m - now);
+    top = now;
+    sum *= keep;
 #pragma unroll
-      for (int k = 0; k < 4; k++) y[k] *= keep;
-      float lw = l * w;
+    for (int k = 0; k < 4; k++) y[k] *= keep;
+    float lw = l * w;
 #pragma unroll
-      for (int o = 16; o; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
-      sum += lw;
-      for (int i0 = 0; i0 < n; i0 += 8) {
-        float4 v[8];
+    for (int o = 16; o; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+    sum += lw;
+    for (int i0 = 0; i0 < n; i0 += 8) {
+      float4 v[8];
 #pragma unroll
-        for (int i = 0; i < 8; i++)
-          if (i0 + i < n && lane * 4 < D) v[i] = __ldcg(reinterpret_cast<const float4 *>(part(base + i0 + i) + r * D) + lane);
+      for (int i = 0; i < 8; i++)
+        if (i0 + i < n && lane * 4 < D) v[i] = __ldcg(reinterpret_cast<const float4 *>(part(base + i0 + i) + r * D) + lane);
 #pragma unroll
-        for (int i = 0; i < 8; i++)
-          if (i0 + i < n) {
-            const float f = __shfl_sync(0xffffffffu, w, i0 + i);
-            if (lane * 4 < D) y[0] += f * v[i].x, y[1] += f * v[i].y, y[2] += f * v[i].z, y[3] += f * v[i].w;
-          }
-      }
+      for (int i = 0; i < 8; i++)
+        if (i0 + i < n) {
+          const float f = __shfl_sync(0xffffffffu, w, i0 + i);
+          if (lane * 4 < D) y[0] += f * v[i].x, y[1] += f * v[i].y, y[2] += f * v[i].z, y[3] += f * v[i].w;
+        }
     }
-    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int64_t at = (int64_t(q0) + r / a.G) * a.Hq + note.h * a.G + r % a.G;
-    if (lane * 4 < a.d)
-      *reinterpret_cast<uint2 *>(a.out + at * a.d + lane * 4) = make_uint2(pack<BF16>(y[0] * f, y[1] * f), pack<BF16>(y[2] * f, y[3] * f));
-    if (lane == 0 && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (top - kLift + log2f(sum)) * 0.6931471805599453f;
   }
+  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int64_t at = (int64_t(q0) + r / a.G) * a.Hq + note.h * a.G + r % a.G;
+  if (lane * 4 < a.d)
+    *reinterpret_cast<uint2 *>(a.out + at * a.d + lane * 4) = make_uint2(pack<BF16>(y[0] * f, y[1] * f), pack<BF16>(y[2] * f, y[3] * f));
+  if (lane == 0 && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (top - kLift + log2f(sum)) * 0.6931471805599453f;
 }
 
 int padded(int d) { return d <= 64 ? 64 : 128; }
@@ -494,7 +494,7 @@ cudaError_t launch(const FewArgs &a, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(k_few<D, NB, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   k_few<D, NB, BF16><<<kSMs, Shape<D>::kThreads, kSmem, st>>>(a);
-  const cudaError_t e2 = launch_early(k_few_join<D, BF16>, dim3(Shape<D>::kRuns), dim3(128), 0, st, a);
+  const cudaError_t e2 = launch_early(k_few_join<D, BF16>, dim3(Shape<D>::kRuns, unsigned((a.max_q * a.G + 3) / 4)), dim3(128), 0, st, a);
   return e2 != cudaSuccess ? e2 : cudaGetLastError();
 }
 

@@ -508,7 +508,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
         const uint32_t q_lo = operand_lo(sm.q[0], 16), k_lo = operand_lo(sm.kv[0], 16), v_lo = operand_lo(sm.kv[0], kTile * 128);
         int stage = 0, turn = 0, slot = 0;
         uint32_t kv_phase = 0, q_phase = 0, todo_phase = 0, p_phase[2] = {0, 0};
-        bool ok = true;
+        // A wait that runs out is seen between parts only (the others end at once, and what
+        // is issued meanwhile stays within the CTA's own memory): without a way out of the
+        // loops the compiler sees that the warp stays together, and what the products take
+        // comes from uniform registers.
         auto s_product = [&](int t, int q, int st) {  // S_t = Q_q K^T
           const uint32_t a0 = q_lo + q * kStage, b0 = k_lo + st * kStage;
           if (elected()) {
@@ -520,23 +523,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
         };
         auto take = [&]() {  // the next operand tile
           const int st = stage;
-          ok = bar_wait(&sm.kv_full[st], kv_phase, &sm.dead);
+          bar_wait(&sm.kv_full[st], kv_phase, &sm.dead);
           if (++stage == kStages) stage = 0, kv_phase ^= 1;
           return st;
         };
         for (;;) {
-          if (!(ok = bar_wait(&sm.todo_full[turn], todo_phase, &sm.dead))) break;
-          const int n = sm.todo[turn].n, split = sm.todo[turn].split;
+          const bool there = bar_wait(&sm.todo_full[turn], todo_phase, &sm.dead);
+          if (!__all_sync(0xffffffffu, there)) break;
+          const int n = __shfl_sync(0xffffffffu, sm.todo[turn].n, 0), split = __shfl_sync(0xffffffffu, sm.todo[turn].split, 0);
           __syncwarp();
           if (lane == 0) bar_arrive(&sm.todo_empty[turn]);
           turn ^= 1;
           if (turn == 0) todo_phase ^= 1;
           if (n < 0) break;
-          if (!(ok = bar_wait(&sm.q_full, q_phase, &sm.dead))) break;
+          bar_wait(&sm.q_full, q_phase, &sm.dead);
           q_phase ^= 1;
           {
             const int ks = take();
-            if (!ok) break;
             tm_after();
             s_product(0, 0, ks);
             if (!split) s_product(1, 1, ks);
@@ -545,40 +548,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
               if (n == 1) mma_commit(&sm.q_empty);
             }
           }
-          for (int j = 0; j < n && ok; j++) {
+          for (int j = 0; j < n; j++) {
             const bool more = j + 1 < n;
             int ks = 0;
             if (more) {
               ks = take();
-              if (!ok) break;
               if (split) {  // the other tile's: P(j-1), which it overwrites, is behind PV(j-1)
                 tm_after();
                 s_product(j + 1 & 1, 0, ks);
               }
             }
             const int vs = take();
-            if (!ok) break;
 #pragma unroll
             for (int t = 0; t < 2; t++) {
               if (split && t != (j & 1)) continue;
               const uint32_t b0 = v_lo + vs * kStage;
 #pragma unroll
               for (int half = 0; half < 2; half++) {  // O_t += P_t V
-                if (!(ok = bar_wait(&sm.p_full[t][half], p_phase[t], &sm.dead))) break;
+                bar_wait(&sm.p_full[t][half], p_phase[t], &sm.dead);
                 tm_after();
                 if (elected())
 #pragma unroll
                   for (int k = half * 4; k < half * 4 + 4; k++)
                     mma_ts(tmem + 2 * kTile + t * kTile, tmem + t * kTile + k * 8, b0 + k * (2048 >> 4), kO, j > split || k > 0);
               }
-              if (!ok) break;
               p_phase[t] ^= 1;
               if (more && !split)
                 s_product(t, t, ks);
               else if ((!more || (split && j + 2 == n)) && elected())
                 mma_commit(&sm.o_full[t]);
             }
-            if (!ok) break;
             if (elected()) {
               mma_commit(&sm.kv_empty[vs]);
               mma_commit(&sm.info_empty[slot]);
@@ -587,7 +586,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
             }
             if (++slot == kInfo) slot = 0;
           }
-          if (!ok) break;
         }
       }
     } else if (warp >= 8) {
