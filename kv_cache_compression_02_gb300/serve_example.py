@@ -3,8 +3,10 @@
 A context's KV (synthetic, from :mod:`.synth`) is fitted, encoded and decoded by the codec into a buffer with room for
 a question.  Each layer of the decoded context goes into 8-bit pages (cg_pages_extend, cg_cache_write); a question is
 run against the decoded fp16 keys (cg_prompt_attend) and its own keys join the pages; three readers branch off it
-(cg_pages_fork) and generate a few tokens each (cg_pages_extend, cg_cache_write, cg_cache_attend); two of them are
-dropped (cg_pages_free) and the cache is compacted (cg_pages_compact).  Queries, keys and values of the new tokens are
+(cg_pages_fork) and generate a few tokens each (cg_pages_extend, cg_pages_slots, cg_cache_write, cg_pages_groups,
+cg_shared_attend: the context that they share is read once for all of them); another look at the context alone is taken
+by rows that are no part of it (cg_cross_attend); two readers are dropped (cg_pages_free), the cache is compacted
+(cg_pages_compact) and the last one attends by itself (cg_cache_attend).  Queries, keys and values of the new tokens are
 random rows: there is no model here, only what a server does around one.
 """
 from __future__ import annotations
@@ -72,35 +74,44 @@ def run(L=2, H=2, G=4, S=1500, question=37, steps=5, block_tokens=16, fmt=None, 
     last = context[L - 1]
     done(cg.cg_prompt_attend(prompt, q, last[0], last[1], i32([0, question]), i32([0, n_tok]), answer, None, wsp), "prompt", wsp)
 
+    # what the context alone says to the question, without the question's own keys: one pass over it for two sequences of rows
+    look, look_lse = torch.empty_like(q), torch.empty(question, Hq, **dev)
+    half = question // 2
+    cross = cg.Prompt(2, Hq, H, d, cg.CG_F16, question, n_tok, question - half, S, 1.0 / math.sqrt(d), (Hq * d, d), (d, n_tok * d), (d, n_tok * d))
+    wsp = cg.empty_u8(cg.cg_prompt_workspace_bytes(cross))
+    done(cg.cg_cross_attend(cross, q, last[0], last[1], i32([0, half, question]), i32([0, 0]), i32([S, S]), look, look_lse, wsp), "cross", wsp)
+
     # three readers branch off and generate: one batched call of each kind a step (the last layer here)
     ids = i32([1, 2, 3])
     done(cg.cg_pages_fork(cache, pages, addr[0], addr[1], i32([0] * readers), ids, ws), "fork", ws)
     att = cg.Attend(n_seqs, 1, Hq, cg.CG_F16, per, 1.0 / math.sqrt(d))
-    wsa = cg.empty_u8(cg.cg_cache_workspace_bytes(cache, att))
     one = cg.Rows(n_seqs, readers, 1, cg.CG_F16, per, H * d, d)
     new_q, new_k, new_v = rows(steps, n_seqs, 1, Hq, d), rows(steps, readers, H, d), rows(steps, readers, H, d)
     outs, lse = torch.empty(steps, n_seqs, 1, Hq, d, dtype=torch.float16, **dev), torch.empty(steps, n_seqs, 1, Hq, **dev)
+    new, cu, start, wsr = i32([0, 1, 1, 1]), i32([0] * (n_seqs + 1)), i32([0] * n_seqs), cg.empty_u8(256)
+    groups = cg.Groups(i32([0] * (n_seqs // 2 + 1)), i32([0] * n_seqs), i32([0] * (n_seqs // 2)))
+    wsg = cg.empty_u8(cg.cg_pages_workspace_bytes(cache, pages, n_seqs))
+    wsa = cg.empty_u8(cg.cg_shared_workspace_bytes(cache, att, groups))
+    k_pool, v_pool, k_scale, v_scale = pools[L - 1, 0], pools[L - 1, 1], scales[L - 1, 0], scales[L - 1, 1]
     for s in range(steps):
-        start = lens.clone()
-        done(cg.cg_pages_extend(cache, pages, ids, start[1:] + 1, ws), "extend", ws)
-        done(cg.cg_cache_write(cache, one, new_k[s], new_v[s], i32([0, 0, 1, 2, 3]), start, table, pools[L - 1, 0], pools[L - 1, 1], scales[L - 1, 0],
-                               scales[L - 1, 1], wsw), "write", wsw)
-        done(cg.cg_cache_attend(cache, att, new_q[s], pools[L - 1, 0], pools[L - 1, 1], scales[L - 1, 0], scales[L - 1, 1], table, lens, outs[s],
-                                lse[s], wsa), "attend", wsa)
+        done(cg.cg_pages_extend(cache, pages, ids, lens[1:] + 1, ws), "extend", ws)
+        done(cg.cg_pages_slots(cache, pages, readers, new, cu, start, None, None, None, wsr), "slots", wsr)
+        done(cg.cg_cache_write(cache, one, new_k[s], new_v[s], cu, start, table, k_pool, v_pool, k_scale, v_scale, wsw), "write", wsw)
+        done(cg.cg_pages_groups(cache, pages, max(1, S // block_tokens // 2), *groups.tensors, wsg), "groups", wsg)
+        done(cg.cg_shared_attend(cache, att, groups, new_q[s], k_pool, v_pool, k_scale, v_scale, table, lens, outs[s], lse[s], wsa), "attend", wsa)
 
     # two readers leave; the pages that are left move to the front
     used = int((refs > 0).sum())
     done(cg.cg_pages_free(cache, pages, ids[:2], ws), "free", ws)
     n_live = i32([0])
     done(cg.cg_pages_compact(cache, pages, addr[0], addr[1], refs, table, n_live, ws), "compact", ws)
-    again, z = torch.empty_like(outs[0]), torch.empty_like(lse[0])
-    done(cg.cg_cache_attend(cache, att, new_q[-1], pools[L - 1, 0], pools[L - 1, 1], scales[L - 1, 0], scales[L - 1, 1], table, lens, again, z, wsa),
-         "attend", wsa)
+    again, z, wsa = torch.empty_like(outs[0]), torch.empty_like(lse[0]), cg.empty_u8(cg.cg_cache_workspace_bytes(cache, att))
+    done(cg.cg_cache_attend(cache, att, new_q[-1], k_pool, v_pool, k_scale, v_scale, table, lens, again, z, wsa), "attend", wsa)
     if verbose:
         fp16 = context.numel() * 2
         print(f"context of {S} tokens: {int(nbytes.item())} bytes on the wire; {n_tok} tokens in {int(n_live.item())} of {n_blocks} pages after "
               f"compaction ({used} with three readers), {pools.element_size() * 8}-bit codes of {fp16} bytes of fp16")
-    return dict(context=context, q=q, answer=answer, new_q=new_q, new_k=new_k, new_v=new_v, outs=outs, lse=lse, again=again, used=used,
+    return dict(context=context, q=q, answer=answer, look=look, look_lse=look_lse, groups=groups, new_q=new_q, new_k=new_k, new_v=new_v, outs=outs, lse=lse, again=again, used=used,
                 n_live=int(n_live.item()), refs=refs, table=table, lens=lens, pools=pools, scales=scales)
 
 
