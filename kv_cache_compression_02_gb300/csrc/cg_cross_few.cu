@@ -4,7 +4,9 @@
 // For one KV head of one sequence the up to 16 rows (queries x Hq / H) are one
 // matrix.  Both products are taken transposed on mma.sync m16n8k16, S^T = K Q^T
 // and O^T = V^T P^T, so that positions and channels fill the side of 16 and
-// eight rows waste nothing.  P is rounded to the type of the rows.
+// eight rows waste nothing.  P goes into the second product as two values of the
+// rows' type, so that a weight is off by at most 2^-16 (bf16) or 2^-21 (f16) of
+// itself, or by f16's least step: 2^-31 of the largest.
 //
 // What bounds it is the read of the keys and values.  A warp works by itself: it
 // has tiles of 32 positions copied (TMA) two tiles ahead, a running maximum, sum
@@ -327,7 +329,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_few(const __grid_cons
           for (int j = 0; j < kJ; j++) o[j][n][0] *= keep[n].x, o[j][n][1] *= keep[n].y, o[j][n][2] *= keep[n].x, o[j][n][3] *= keep[n].y;
         }
       }
-      uint32_t p[2][NB][2];  // P^T as an operand
+      // P^T as an operand, and what it leaves over: the tensor cores have the time.  It
+      // is taken a little less than it is, so that the rest is above 0 where P is, too,
+      // and an infinite value of V stays what it is.
+      uint32_t p[2][NB][2], rest[2][NB][2];
+      const float2 less = BF16 ? make_float2(1.0f - 0x1p-8f, 1.0f - 0x1p-8f) : make_float2(1.0f - 0x1p-10f, 1.0f - 0x1p-10f);
       const float2 sl = make_float2(a.scale_log2, a.scale_log2);
 #pragma unroll
       for (int n = 0; n < NB; n++) {
@@ -339,7 +345,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_few(const __grid_cons
             float2 y = fma2(make_float2(x[tt][n][2 * half], x[tt][n][2 * half + 1]), sl, base);
             y = make_float2(ex2(y.x), ex2(y.y));
             sum[n] = add2(sum[n], y);
-            p[tt][n][half] = transposed(pack<BF16>(y.x, y.y));
+            const float2 z = mul2(y, less);
+            const uint32_t w = pack<BF16>(z.x, z.y);
+            p[tt][n][half] = transposed(w);
+            rest[tt][n][half] = transposed(pack<BF16>(y.x - elem<BF16>(uint16_t(w)), y.y - elem<BF16>(uint16_t(w >> 16))));
           }
       }
       // O^T += V^T P^T
@@ -351,7 +360,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_few(const __grid_cons
           uint32_t f[4];
           load_matrices<true>(f, v_at + (c >> 3) * (kTok * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 #pragma unroll
-          for (int n = 0; n < NB; n++) mma<BF16>(o[j][n], f, p[tt][n][0], p[tt][n][1]);
+          for (int n = 0; n < NB; n++) {
+            mma<BF16>(o[j][n], f, p[tt][n][0], p[tt][n][1]);
+            mma<BF16>(o[j][n], f, rest[tt][n][0], rest[tt][n][1]);
+          }
         }
       __syncwarp();
       if (issued < tiles) issue(s);

@@ -285,10 +285,10 @@ __device__ inline void copy_bulk(uint32_t dst, const void *src, uint32_t bytes, 
                : "memory");
 }
 
-// RAW: pages are a multiple of 16 tokens, so that 16 positions have one scale,
-// and rows have D channels: codes are copied, `chunk` positions (a power of two
-// up to 128 that divides a page) at a time.  Other shapes load them a position
-// and eight channels at a time.
+// RAW: pages are a multiple of 16 tokens, so that 16 positions have one scale
+// and lie together: their codes are copied, `chunk` positions (a power of two up
+// to 128 that divides a page) at a time.  Other shapes load them a position and
+// eight channels at a time (pages of 24, not 32: PAGE24).
 template <int FMT, int D, bool RAW>
 __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ SharedArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
         uint32_t todo_phase = 0, k_phase = 0, v_phase = 0, raw_phase = 1;
         bool ok = true;
         const int chunk = a.chunk;  // lane l has the l-th
-        const uint32_t bytes = uint32_t(chunk) * D;
+        const uint32_t bytes = uint32_t(chunk) * a.d;
         auto copy = [&](const uint8_t *pool, int slot, uint32_t phase) {
           if (!(ok = bar_wait(&sm.info_full[slot], phase, &sm.dead))) return;
           if (!(ok = bar_wait(&sm.raw_empty[at], raw_phase, &sm.dead))) return;
@@ -614,21 +614,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
           } else {
             if (!(ok = bar_wait(&sm.info_full[is_v ? v_slot : k_slot], is_v ? v_phase : k_phase, &sm.dead))) break;
           }
-          const uint8_t *pool = is_v ? a.vp : a.kp, *from = sm.raw[RAW ? at : 0] + r0 * D + u * 8;
+          const uint8_t *pool = is_v ? a.vp : a.kp, *from = sm.raw[RAW ? at : 0] + r0 * a.d + u * 8;
           const bool there = u * 8 < a.d, whole = in.whole;
           uint8_t *to = sm.kv[stage][u >> 3] + r0 * 128 + (((u & 7) ^ (r0 & 7)) << 4);  // (kStep is a multiple of 8)
           constexpr int kBatch = RAW ? kUnits : 8;  // (codes from shared memory: all of them before the wait; from global memory: 8)
 #pragma unroll 1
           for (int h = 0; h < kUnits; h += kBatch) {
             uint2 w[kBatch];
+            if (RAW && a.d == D) {
 #pragma unroll
-            for (int k = 0; k < kBatch; k++) {
-              const int r = (h + k) * kStep;
-              if (RAW) {
-                w[k] = *reinterpret_cast<const uint2 *>(from + r * D);
-              } else {
-                const int64_t begin = in.row[RAW ? 0 : r0 + r];
-                w[k] = there && begin >= 0 ? *reinterpret_cast<const uint2 *>(pool + begin + u * 8) : make_uint2(0, 0);
+              for (int k = 0; k < kBatch; k++) w[k] = *reinterpret_cast<const uint2 *>(from + (h + k) * kStep * D);
+            } else {
+#pragma unroll
+              for (int k = 0; k < kBatch; k++) {
+                const int r = (h + k) * kStep;
+                if (RAW) {
+                  w[k] = there ? *reinterpret_cast<const uint2 *>(from + r * a.d) : make_uint2(0, 0);
+                } else {
+                  const int64_t begin = in.row[RAW ? 0 : r0 + r];
+                  w[k] = there && begin >= 0 ? *reinterpret_cast<const uint2 *>(pool + begin + u * 8) : make_uint2(0, 0);
+                }
               }
             }
             if (RAW) {
@@ -1039,7 +1044,7 @@ cudaError_t launch(const SharedArgs &a, cudaStream_t st) {
 
 template <int FMT>
 cudaError_t launch_format(const SharedArgs &a, cudaStream_t st) {
-  const bool raw = a.bt % 16 == 0 && (a.d == 64 || a.d == 128);
+  const bool raw = a.bt % 16 == 0;
   if (a.d <= 64) return raw ? launch<FMT, 64, true>(a, st) : launch<FMT, 64, false>(a, st);
   return raw ? launch<FMT, 128, true>(a, st) : launch<FMT, 128, false>(a, st);
 }
