@@ -203,9 +203,12 @@ __device__ inline int clamped_length(const AttendArgs &a, int b) {
   return int(max(int64_t(0), min(int64_t(a.len[b]), int64_t(a.stride) * a.bt)));
 }
 
+// (The plan has ended when the kernel begins, but is not the one that it waits for: the read goes past the L1 cache.)
+__device__ inline int first_of(const AttendArgs &a, int b) { return __ldcg(a.first + b); }
+
 template <bool OWN>
 __device__ inline int length(const AttendArgs &a, const int *kept, int b) {
-  return a.B <= kLens ? kept[b] : clamped_length(a, b) - (OWN ? a.first[b] * a.bt : 0);
+  return a.B <= kLens ? kept[b] : clamped_length(a, b) - (OWN ? first_of(a, b) * a.bt : 0);
 }
 
 __device__ inline int tiles_of(int len) { return int((uint32_t(len) + kUnit - 1) / kUnit); }
@@ -213,7 +216,7 @@ __device__ inline int tiles_of(int len) { return int((uint32_t(len) + kUnit - 1)
 template <bool OWN>
 __device__ inline void set_seq(const AttendArgs &a, const int *kept, Walk &w) {
   w.len = length<OWN>(a, kept, w.b);
-  if (OWN) w.first = a.first[w.b];
+  if (OWN) w.first = first_of(a, w.b);
   w.tiles = tiles_of(w.len);
 }
 
@@ -238,7 +241,7 @@ __device__ inline void write_row(const AttendArgs &a, int b, int h, int r, const
                                  float l, bool lead) {
   const int t = r / a.G;
   const int64_t row = (int64_t(b) * a.T + t) * a.Hq + h * a.G + r % a.G;
-  if (OWN && a.first[b] > 0) {
+  if (OWN && first_of(a, b) > 0) {
 #pragma unroll
     for (int i = 0; i < N; i += 4)
       if (c0 + i < a.d) *reinterpret_cast<float4 *>(a.own + row * a.d + c0 + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
@@ -275,7 +278,6 @@ __global__ void __launch_bounds__(kThreads, Shape<NB>::kPerSM) k_attend(const __
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
   asm volatile("griddepcontrol.launch_dependents;");
-  if (OWN) status_cleared();  // launched early, behind the plan that makes a.first
   if (threadIdx.x == 0) {
     sm.errors = sm.dead = 0;
     a.notes[blockIdx.x].parts = 0;
@@ -287,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, Shape<NB>::kPerSM) k_attend(const __
   int most = 0;
   bool bad_len = false;
   for (int b = b0; b < b1; b++) {
-    const int n = a.len[b], whole = clamped_length(a, b), fit = OWN ? whole - a.first[b] * a.bt : whole, tiles = tiles_of(fit);
+    const int n = a.len[b], whole = clamped_length(a, b), fit = OWN ? whole - first_of(a, b) * a.bt : whole, tiles = tiles_of(fit);
     bad_len |= n != whole;
     if (a.B <= kLens) sm.len[b] = fit;
     cost += tiles ? tiles + kIn : 0;
@@ -326,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, Shape<NB>::kPerSM) k_attend(const __
   for (int b = blockIdx.x; b < a.B; b += gridDim.x)  // sequences with nothing in them
     if (length<OWN>(a, sm.len, b) == 0) {
       const int64_t rows = int64_t(a.T) * a.Hq, at = b * rows;
-      if (OWN && a.first[b] > 0) {
+      if (OWN && first_of(a, b) > 0) {
         for (int64_t i = threadIdx.x; i < rows; i += kThreads) a.own_ml[2 * (at + i)] = -INFINITY, a.own_ml[2 * (at + i) + 1] = 0.0f;
         continue;
       }
@@ -339,6 +341,7 @@ __global__ void __launch_bounds__(kThreads, Shape<NB>::kPerSM) k_attend(const __
   if (blockIdx.x >= ctas) {
     __syncthreads();
     if (threadIdx.x == 0) a.notes[blockIdx.x].errors = sm.errors;
+    if (OWN) status_cleared();
     return;
   }
   const int64_t lo = total * blockIdx.x / ctas, hi = total * (blockIdx.x + 1) / ctas;
@@ -936,6 +939,8 @@ __global__ void __launch_bounds__(kThreads, Shape<NB>::kPerSM) k_attend(const __
   if (sm.dead)  // what is in flight gets a moment to land
     for (int i = 0; i < 1000; i++) __nanosleep(1000);
   if (threadIdx.x == 0) a.notes[blockIdx.x].errors = sm.errors;
+  // OWN: launched early, beside the kernel for the prefixes; what waits for this one waits for that one, too
+  if (OWN) status_cleared();
 }
 
 // Joins the parts of items that several CTAs had: one CTA per CTA that has the
@@ -996,7 +1001,7 @@ __global__ void __launch_bounds__(128) k_join(const __grid_constant__ AttendArgs
   }
   const int t = row / a.G;
   const int64_t at = (int64_t(note.b) * a.T + t) * a.Hq + note.h * a.G + row % a.G;
-  if (OWN && a.first[note.b] > 0) {
+  if (OWN && first_of(a, note.b) > 0) {
     if (lane * 4 < a.d) *reinterpret_cast<float4 *>(a.own + at * a.d + lane * 4) = make_float4(y[0], y[1], y[2], y[3]);
     if (lane == 0) a.own_ml[2 * at] = top, a.own_ml[2 * at + 1] = sum;
     return;

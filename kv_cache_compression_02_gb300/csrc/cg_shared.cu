@@ -53,11 +53,12 @@ constexpr float kLift = 7.0f, kLag = 8.0f, kOwnLift = 12.0f;
 // What an item costs: kIn for its way in and out, and for each tile of positions.
 constexpr int kIn = 10, kFull = 4, kSplit = 2;
 
-struct Note {
+struct alignas(16) Note {
   uint32_t errors;
   int32_t parts;   // of the item that this CTA has the first but not the last part of, or 0
   int32_t second;  // the first part is in this CTA's second slot
   int32_t e0, row0, rows, head;  // as in Todo
+  int32_t reserved;
 };
 
 struct SharedArgs {
@@ -69,10 +70,12 @@ struct SharedArgs {
   float *lse;
   const int32_t *cu, *member, *shared;  // the caller's groups
   uint32_t *status, *bad;
+  int32_t *any;  // whether some group counts
   int32_t *owner, *first;  // of a sequence: its entry in the groups, and the pages that it shares
   int32_t *seq;            // of an entry: its sequence, or -1
   int32_t *keys, *lead;    // of a group: its positions (0: nothing to do), and a sequence whose row of the table has them
-  float *own, *own_ml;
+  float *own, *own_ml;     // of each row [B][T][Hq]: what its sequence has to itself, not normalised, with maximum and sum
+  float *pre, *pre_ml;     // the same of the prefix where one CTA had all of it; else the sum is -1 and the parts have it
   Note *notes;
   float *parts;  // [2 * kGrid][kRows][D + 2]
   int64_t q_seq, q_tok, q_head;
@@ -125,7 +128,7 @@ __global__ void __launch_bounds__(kPlan) k_shared_plan(const SharedArgs a) {
   __shared__ int s_owner[kKept];
   int *const owner = a.B <= kKept ? s_owner : a.owner;
   for (int b = threadIdx.x; b < a.B; b += kPlan) owner[b] = 0x7fffffff, a.first[b] = 0;
-  bool bad = false, fall = false;
+  bool bad = false, fall = false, any = false;
   for (int g = threadIdx.x; g < a.n_groups; g += kPlan) {
     const int e0 = a.cu[g], e1 = a.cu[g + 1], pages = a.shared[g];
     a.keys[g] = 0, a.lead[g] = 0x7fffffff;
@@ -163,6 +166,7 @@ __global__ void __launch_bounds__(kPlan) k_shared_plan(const SharedArgs a) {
           const int64_t keys = int64_t(pages) * a.bt;
           if (pages > 0 && pages <= a.stride && len - a.T + 1 >= keys) {
             takes = b;
+            any = true;
             a.first[b] = pages;
             a.keys[g] = int(keys);
             atomicMin(&a.lead[g], b);
@@ -173,7 +177,8 @@ __global__ void __launch_bounds__(kPlan) k_shared_plan(const SharedArgs a) {
     }
   }
   bad = __syncthreads_or(bad || fall);
-  if (threadIdx.x == 0) *a.bad = bad ? kStBadArg : 0;
+  any = __syncthreads_or(any);
+  if (threadIdx.x == 0) *a.bad = bad ? kStBadArg : 0, *a.any = any;
 }
 
 // ---- items --------------------------------------------------------------------------
@@ -297,6 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
   constexpr uint32_t kTileBytes = kChunks * kTile * 128;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  status_cleared();  // the plan is there
   asm volatile("griddepcontrol.launch_dependents;");
   if (threadIdx.x == 0) {
     sm.errors = sm.dead = 0;
@@ -858,19 +864,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
             m = top;
           }
           const int64_t at = (int64_t(b) * a.T + tok) * a.Hq + head;
-          float f_own = 0.0f, total_l = sum, top = m;
-          if (whole) {  // with what the sequence has to itself
-            status_cleared();
-            if (b >= 0) {
-              const float mo = __ldcg(&a.own_ml[2 * at]), lo_ = __ldcg(&a.own_ml[2 * at + 1]);
-              top = fmaxf(m, mo);
-              const float kp = m == -INFINITY ? 0.0f : ex2(m - top);
-              f_own = mo == -INFINITY ? 0.0f : ex2(mo - top);
-              f_mine *= kp, f_other *= kp;
-              total_l = sum * kp + lo_ * f_own;
-            }
-          }
-          const float turn_l = total_l == 0.0f ? 0.0f : 1.0f / total_l;
           float *part = a.parts + int64_t(slot_out) * kRows * (D + 2);
 #pragma unroll 1
           for (int c = 0; c < D / 32; c++) {
@@ -887,26 +880,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
               for (int i = 0; i < 32; i++) y[i] = __float_as_uint(__uint_as_float(y[i]) + __uint_as_float(z[i]) * f_other);
             }
             if (whole) {
-              if (b >= 0) {
+              if (b >= 0)
 #pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                  if (32 * c + i >= a.d) continue;
-                  float o[8];
-#pragma unroll
-                  for (int k = 0; k < 8; k++) o[k] = __uint_as_float(y[i + k]);
-                  if (f_own != 0.0f) {
-                    const float4 u0 = __ldcg(reinterpret_cast<const float4 *>(a.own + at * a.d + 32 * c + i));
-                    const float4 u1 = __ldcg(reinterpret_cast<const float4 *>(a.own + at * a.d + 32 * c + i + 4));
-                    o[0] += f_own * u0.x, o[1] += f_own * u0.y, o[2] += f_own * u0.z, o[3] += f_own * u0.w;
-                    o[4] += f_own * u1.x, o[5] += f_own * u1.y, o[6] += f_own * u1.z, o[7] += f_own * u1.w;
-                  }
-                  uint32_t w4[4];
-#pragma unroll
-                  for (int k = 0; k < 4; k++)
-                    w4[k] = a.bf16 ? pack<true>(o[2 * k] * turn_l, o[2 * k + 1] * turn_l) : pack<false>(o[2 * k] * turn_l, o[2 * k + 1] * turn_l);
-                  *reinterpret_cast<uint4 *>(a.out + at * a.d + 32 * c + i) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-                }
-              }
+                for (int i = 0; i < 32; i += 4)
+                  if (32 * c + i < a.d) *reinterpret_cast<uint4 *>(a.pre + at * a.d + 32 * c + i) = make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
             } else if (b >= 0) {  // four channels of 32 rows lie together
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
@@ -915,10 +892,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
           }
           tm_before();
           if (b >= 0) {
-            if (!whole)
-              part[kRows * D + t * kTile + r] = m, part[kRows * (D + 1) + t * kTile + r] = sum;
-            else if (a.lse)
-              a.lse[at] = total_l == 0.0f ? -INFINITY : (top - kOwnLift + log2f(total_l)) * 0.6931471805599453f;
+            if (!whole) part[kRows * D + t * kTile + r] = m, part[kRows * (D + 1) + t * kTile + r] = sum;
+            a.pre_ml[2 * at] = m, a.pre_ml[2 * at + 1] = whole ? sum : -1.0f;
           }
           __syncwarp();
           if (lane == 0) {
@@ -939,18 +914,60 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
     for (int i = 0; i < 1000; i++) __nanosleep(1000);
   if (warp == 15) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   if (threadIdx.x == 0) a.notes[blockIdx.x].errors = sm.errors | (sm.dead ? kStTimeout : 0);
-  status_cleared();  // the join that waits for this kernel reads what the ones before it have written
+}
+
+// A finished row's channels 4 c ...
+__device__ inline void write_row(const SharedArgs &a, int64_t at, int c, float4 y, float top, float sum) {
+  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+  if (c * 4 < a.d) {
+    const uint2 w = a.bf16 ? make_uint2(pack<true>(y.x * f, y.y * f), pack<true>(y.z * f, y.w * f))
+                           : make_uint2(pack<false>(y.x * f, y.y * f), pack<false>(y.z * f, y.w * f));
+    *reinterpret_cast<uint2 *>(a.out + at * a.d + c * 4) = w;
+  }
+  if (c == 0 && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (top - kOwnLift + log2f(sum)) * 0.6931471805599453f;
+}
+
+// Rows whose prefix one CTA had: a warp per row, by the whole grid.
+template <int D>
+__device__ void join_whole(const SharedArgs &a, int64_t first, int64_t step) {
+  const int lane = threadIdx.x & 31;
+  const int64_t rows = int64_t(a.n_members) * a.T * a.Hq, of_one = int64_t(a.T) * a.Hq;
+  const int e0 = a.cu[0], e1 = a.cu[a.n_groups];
+  for (int64_t r = first; r < rows; r += step) {
+    const int64_t e = r / of_one;
+    if (e < e0 || e >= e1) continue;
+    const int b = __ldcg(&a.seq[e]);
+    if (b < 0) continue;
+    const int64_t at = b * of_one + r % of_one;
+    const float pl = __ldcg(&a.pre_ml[2 * at + 1]);
+    if (pl < 0.0f) continue;
+    const float pm = __ldcg(&a.pre_ml[2 * at]), om = __ldcg(&a.own_ml[2 * at]), ol = __ldcg(&a.own_ml[2 * at + 1]), top = fmaxf(pm, om);
+    const float wp = pm == -INFINITY ? 0.0f : ex2(pm - top), wo = om == -INFINITY ? 0.0f : ex2(om - top);
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (lane * 4 < a.d) {
+      const float4 p = __ldcg(reinterpret_cast<const float4 *>(a.pre + at * a.d) + lane);
+      y = make_float4(p.x * wp, p.y * wp, p.z * wp, p.w * wp);
+      if (om != -INFINITY) {
+        const float4 o = __ldcg(reinterpret_cast<const float4 *>(a.own + at * a.d) + lane);
+        y.x += o.x * wo, y.y += o.y * wo, y.z += o.z * wo, y.w += o.w * wo;
+      }
+    }
+    write_row(a, at, lane, y, top, pl * wp + ol * wo);
+  }
 }
 
 // Joins the parts of items that several CTAs had, with what each sequence has
 // to itself: eight rows a CTA, four channels a thread.  First the rows' maxima
-// and sums, then the outputs, eight parts' loads in flight.
+// and sums, then the outputs, eight parts' loads in flight.  The last kWholeY
+// CTAs of each column look after the other rows.
+constexpr int kWholeY = 4;
+
 template <int D>
 __global__ void __launch_bounds__(2 * D) k_shared_join(const __grid_constant__ SharedArgs a) {
   status_cleared();
   if (blockIdx.x == 0 && blockIdx.y == 0) {  // the status of the call, with that of the kernels before
     __shared__ uint32_t s_errors;
-    if (threadIdx.x == 0) s_errors = *a.bad;
+    if (threadIdx.x == 0) s_errors = __ldcg(a.bad);
     __syncthreads();
     uint32_t e = 0;
     for (int i = threadIdx.x; i < int(gridDim.x); i += 2 * D) e |= __ldcg(&a.notes[i].errors);
@@ -958,10 +975,22 @@ __global__ void __launch_bounds__(2 * D) k_shared_join(const __grid_constant__ S
     __syncthreads();
     if (threadIdx.x == 0 && s_errors) atomicOr(a.status, s_errors);
   }
-  const Note note = a.notes[blockIdx.x];
+  if (blockIdx.y >= kRows / 8) {
+    constexpr int kWarps = 2 * D / 32;
+    if (__ldcg(a.any))
+      join_whole<D>(a, (int64_t(blockIdx.y - kRows / 8) * gridDim.x + blockIdx.x) * kWarps + threadIdx.x / 32, int64_t(kWholeY) * gridDim.x * kWarps);
+    return;
+  }
+  // what the kernels before the last one have written is read past the L1 cache
+  union {
+    int4 words[2];
+    Note note;
+  } u;
+  u.words[0] = __ldcg(reinterpret_cast<const int4 *>(a.notes + blockIdx.x)), u.words[1] = __ldcg(reinterpret_cast<const int4 *>(a.notes + blockIdx.x) + 1);
+  const Note &note = u.note;
   if (note.parts == 0 || note.row0 + int(blockIdx.y) * 8 >= note.rows) return;
   const int rr = threadIdx.x % 8, r = blockIdx.y * 8 + rr, c = threadIdx.x / 8, row = note.row0 + r;
-  const int b = row < note.rows ? a.seq[note.e0 + row / a.TG] : -1;
+  const int b = row < note.rows ? __ldcg(&a.seq[note.e0 + row / a.TG]) : -1;
   auto part = [&](int i) { return a.parts + (2 * (int64_t(blockIdx.x) + i) + (i == 0 ? note.second : 0)) * kRows * (D + 2); };
   __shared__ float s_m[kGrid][8], s_l[kGrid][8];  // of each part
   for (int i = c; i < note.parts; i += D / 4) {
@@ -992,13 +1021,7 @@ __global__ void __launch_bounds__(2 * D) k_shared_join(const __grid_constant__ S
         y.x += w * v[i].x, y.y += w * v[i].y, y.z += w * v[i].z, y.w += w * v[i].w;
       }
   }
-  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-  if (c * 4 < a.d) {
-    const uint2 w = a.bf16 ? make_uint2(pack<true>(y.x * f, y.y * f), pack<true>(y.z * f, y.w * f))
-                           : make_uint2(pack<false>(y.x * f, y.y * f), pack<false>(y.z * f, y.w * f));
-    *reinterpret_cast<uint2 *>(a.out + at * a.d + c * 4) = w;
-  }
-  if (c == 0 && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (top - kOwnLift + log2f(sum)) * 0.6931471805599453f;
+  write_row(a, at, c, y, top, sum);
 }
 
 bool groups_ok(const cg_cache *c, const cg_attend *t, const cg_groups *g) {
@@ -1009,7 +1032,7 @@ bool groups_ok(const cg_cache *c, const cg_attend *t, const cg_groups *g) {
 int padded(int d) { return d <= 64 ? 64 : 128; }
 
 struct Places {
-  uint64_t bad, owner, first, seq, keys, lead, own, own_ml, notes, parts, bytes;
+  uint64_t bad, owner, first, seq, keys, lead, own, own_ml, pre, pre_ml, notes, parts, bytes;
 };
 
 Places places(const cg_cache *c, const cg_attend *t, const cg_groups *g) {
@@ -1024,7 +1047,9 @@ Places places(const cg_cache *c, const cg_attend *t, const cg_groups *g) {
   w.lead = w.keys + pad256(4 * uint64_t(g->n_groups));
   w.own = w.lead + pad256(4 * uint64_t(g->n_groups));
   w.own_ml = w.own + pad256(4 * rows * c->d);
-  w.notes = w.own_ml + pad256(8 * rows);
+  w.pre = w.own_ml + pad256(8 * rows);
+  w.pre_ml = w.pre + pad256(4 * rows * c->d);
+  w.notes = w.pre_ml + pad256(8 * rows);
   w.parts = w.notes + pad256(sizeof(Note) * kGrid);
   w.bytes = w.parts + 4 * uint64_t(2 * kGrid) * kRows * (padded(c->d) + 2);
   return w;
@@ -1036,10 +1061,7 @@ cudaError_t launch(const SharedArgs &a, cudaStream_t st) {
   static_assert(kSmem <= 227 * 1024, "fits in an SM");
   const cudaError_t e = cudaFuncSetAttribute(k_shared<FMT, D, RAW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  const cudaError_t e2 = launch_early(k_shared<FMT, D, RAW>, dim3(kGrid), dim3(kThreads), kSmem, st, a);
-  if (e2 != cudaSuccess) return e2;
-  const cudaError_t e3 = launch_early(k_shared_join<D>, dim3(kGrid, kRows / 8), dim3(2 * D), 0, st, a);
-  return e3 != cudaSuccess ? e3 : cudaGetLastError();
+  return launch_early(k_shared<FMT, D, RAW>, dim3(kGrid), dim3(kThreads), kSmem, st, a);
 }
 
 template <int FMT>
@@ -1085,6 +1107,8 @@ extern "C" cg_status cg_shared_attend(const cg_cache *cache, const cg_attend *at
   a.out = static_cast<uint16_t *>(out_dev), a.lse = lse_dev;
   a.cu = groups->cu_group_dev, a.member = groups->member_dev, a.shared = groups->shared_dev;
   a.status = reinterpret_cast<uint32_t *>(ws), a.bad = reinterpret_cast<uint32_t *>(ws + w.bad);
+  a.any = reinterpret_cast<int32_t *>(ws + w.bad + 4);
+  a.pre = reinterpret_cast<float *>(ws + w.pre), a.pre_ml = reinterpret_cast<float *>(ws + w.pre_ml);
   a.owner = reinterpret_cast<int32_t *>(ws + w.owner), a.first = reinterpret_cast<int32_t *>(ws + w.first);
   a.seq = reinterpret_cast<int32_t *>(ws + w.seq), a.keys = reinterpret_cast<int32_t *>(ws + w.keys);
   a.lead = reinterpret_cast<int32_t *>(ws + w.lead);
@@ -1099,9 +1123,12 @@ extern "C" cg_status cg_shared_attend(const cg_cache *cache, const cg_attend *at
   a.chunk = kTile;
   while (a.bt % a.chunk) a.chunk /= 2;
   k_shared_plan<<<1, kPlan, 0, st>>>(a);
+  cudaError_t e = cache->format == CG_CACHE_E4M3 ? launch_format<CG_CACHE_E4M3>(a, st) : launch_format<CG_CACHE_INT8>(a, st);
+  if (e != cudaSuccess) return CG_ERR_CUDA;
   const cg_status rc = attend_own(cache, attend, a.first, a.own, a.own_ml, q_dev, k_pool, v_pool, k_scale, v_scale, table_dev, len_dev, out_dev,
                                   lse_dev, ws, st);
   if (rc != CG_OK) return rc;
-  const cudaError_t e = cache->format == CG_CACHE_E4M3 ? launch_format<CG_CACHE_E4M3>(a, st) : launch_format<CG_CACHE_INT8>(a, st);
-  return e == cudaSuccess ? CG_OK : CG_ERR_CUDA;
+  e = a.d <= 64 ? launch_early(k_shared_join<64>, dim3(kGrid, kRows / 8 + kWholeY), dim3(2 * 64), 0, st, a)
+                : launch_early(k_shared_join<128>, dim3(kGrid, kRows / 8 + kWholeY), dim3(2 * 128), 0, st, a);
+  return e == cudaSuccess ? launched() : CG_ERR_CUDA;
 }
