@@ -355,3 +355,15 @@ def test_groups_as_the_table_gives_them():
         assert (outs[0].double() - outs[1].double()).abs().max() <= 2.0 ** -7 * top
         assert (z[0] - z[1]).abs().max() <= 1e-4
     assert groups.tensors[0].tolist() == [0, 1 + readers, 1 + readers, 1 + readers] and groups.tensors[2].tolist() == [n // bt, 0, 0]
+
+
+def test_heads_and_tokens_in_reverse():
+    """Strides may be negative: query heads and tokens from the last to the first."""
+    s = Setup("int8", BF16, 3, 8, 2, 64, 16, [(12, [5, 9, 3])], [20], seed=8)
+    B, T, Hq, d = s.q.shape
+    want, zw, _ = s.run()
+    args = s.on_gpu()
+    back = s.q.flip(1, 2).contiguous().cuda()
+    args[0] = back[:, -1:, -1:]  # the address of what is first now
+    got, z, st = s.run(args=args, q_stride=(T * Hq * d, -Hq * d, -d))
+    assert st == cg.CG_OK and torch.equal(got, want) and torch.equal(z, zw)
