@@ -146,6 +146,10 @@ CASES = {
     "page_longer_than_a_tile": ("int8", F16, 1, 8, 8, 64, 512, [(2, [50, 1])], []),
     "many_groups": ("e4m3", F16, 1, 4, 2, 64, 16, [(1 + i % 9, [1 + i % 4, 2]) for i in range(120)], [3] * 10),
     "groups_of_one": ("int8", F16, 1, 4, 2, 128, 16, [(12, [4]), (1, [1])], []),
+    "more_sequences_than_are_kept": ("int8", BF16, 1, 2, 1, 16, 16, [(2 + i % 3, [(i * k) % 5 for k in range(14)]) for i in range(50)], [3, 0]),
+    "more_groups_than_threads": ("e4m3", F16, 1, 1, 1, 8, 16, [(1 + i % 2, [1, 2]) for i in range(1100)], []),
+    "more_sequences_than_the_plan_keeps": ("int8", F16, 1, 1, 1, 8, 4, [(3, [i % 3 for i in range(4200)]), (9, [1] * 4000)], [1, 2]),
+    "rows_of_one_reader_in_many_blocks": ("e4m3", BF16, 40, 16, 1, 64, 16, [(20, [40, 55])], []),
 }
 
 
