@@ -37,7 +37,7 @@
 // which comes before the read of the codes.  64 readers of 32768 tokens, 64 heads
 // on 8, d = 128, 20 to 2000 tokens of their own, e4m3: 109 us, of which the
 // prefix takes 71 (0.97 PFLOP/s; 27 tiles of 256 rows a CTA at 2.1 us, 10 us of
-// set-up); each reader by itself 2.0 ms.  16 readers of 131072 tokens, int8: 103
+// set-up); without sharing 698 us.  16 readers of 131072 tokens, int8: 103
 // us (2.6 TB/s of distinct codes).  The roles of a scheduler's four warps differ,
 // so that their code has to fit its instruction cache together: loops that were
 // unrolled whole took 147 and 192 us.
@@ -1008,6 +1008,13 @@ __global__ void __launch_bounds__(2 * D) k_shared_join(const __grid_constant__ S
   const int rr = threadIdx.x % 8, r = blockIdx.y * 8 + rr, c = threadIdx.x / 8, row = note.row0 + r;
   const int b = row < note.rows ? __ldcg(&a.seq[note.e0 + row / a.TG]) : -1;
   auto part = [&](int i) { return a.parts + (2 * (int64_t(blockIdx.x) + i) + (i == 0 ? note.second : 0)) * kRows * (D + 2); };
+  float4 v[8];  // the first parts' outputs are on their way before their weights are known
+  auto load = [&](int base) {
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+      if (base + i < note.parts) v[i] = __ldcg(reinterpret_cast<const float4 *>(part(base + i)) + c * kRows + r);
+  };
+  load(0);
   __shared__ float s_m[kGrid][8], s_l[kGrid][8];  // of each part
   for (int i = c; i < note.parts; i += D / 4) {
     const float *p = part(i);
@@ -1026,10 +1033,7 @@ __global__ void __launch_bounds__(2 * D) k_shared_join(const __grid_constant__ S
   if (b < 0) return;
   y.x *= own_w, y.y *= own_w, y.z *= own_w, y.w *= own_w;
   for (int base = 0; base < note.parts; base += 8) {
-    float4 v[8];
-#pragma unroll
-    for (int i = 0; i < 8; i++)
-      if (base + i < note.parts) v[i] = __ldcg(reinterpret_cast<const float4 *>(part(base + i)) + c * kRows + r);
+    if (base > 0) load(base);
 #pragma unroll
     for (int i = 0; i < 8; i++)
       if (base + i < note.parts) {
