@@ -25,7 +25,7 @@
  *     written through it.
  *   - 8 <= d <= 128, d a multiple of 8.  Pools and the first rows of q, k, v
  *     and out are 16-byte aligned, and their strides are multiples of 8
- *     elements (positive ones at cg_prompt_attend).  A sequence of an
+ *     elements (positive ones at cg_prompt_attend and cg_cross_attend).  A sequence of an
  *     attention call has at most 2^30 positions.
  *   - Lengths, offsets and ids are int32 on the device; every byte offset is
  *     computed in 64 bits.  Every call takes H * block_tokens up to 2^30 and
@@ -211,7 +211,7 @@ cg_status cg_prompt_attend(const cg_prompt *prompt, const void *q_dev, const voi
  * that go on from it (out and lse of such a part can be joined with another
  * part's).  Sequences may share keys.  prompt as at cg_prompt_attend (n_k: rows
  * that k and v have; max_k: no k_len is more), with its workspace, its formulas
- * and its rounding of the probabilities; a row without keys gives out 0, lse
+ * and its rounding of the probabilities, or a finer one; a row without keys gives out 0, lse
  * -inf.  Keys that a sequence does not see do not matter, whatever they hold.
  *   cu_q_dev:               int32 [n_seq + 1], as at cg_prompt_attend;
  *   k_begin_dev, k_len_dev: int32 [n_seq];

@@ -58,7 +58,6 @@ constexpr int kRows = 2 * kTile;
 constexpr int kGrid = kSMs;
 constexpr int kStages = 3;   // operand tiles of K or V
 constexpr int kRaw = 4;      // tiles of codes
-constexpr int kInfo = 6;     // tiles whose pages and scales are known
 constexpr int kLookers = 2;  // warps that look them up
 constexpr int kPlan = 1024;
 // p = 2^(s - m + kLift) < 2^15, m at most kLag under the maximum.  The parts that
@@ -99,10 +98,10 @@ struct SharedArgs {
   bool bf16;
 };
 
-// Pages and scales of a tile of positions, for each 16 of them (RAW) or each one.
-template <bool RAW>
+// Pages and scales of a tile of positions, for each EACH of them.
+template <int EACH>
 struct Info {
-  static constexpr int kEach = RAW ? 16 : 1, kCount = kTile / kEach;
+  static constexpr int kCount = kTile / EACH;
   int64_t row[kCount];  // where a position's codes begin, or -1
   float ks[kCount], vs[kCount];
   uint32_t valid[4];
@@ -116,13 +115,15 @@ struct Todo {
   int head, slot;    // KV head; slot of the workspace, or -1: the item is whole
 };
 
-template <int D, bool RAW>
+template <int D, int EACH>
 struct Smem {
+  static constexpr bool RAW = EACH > 1;
+  static constexpr int kInfo = EACH == 8 ? 4 : 6;  // tiles whose pages and scales are known (as there is room)
   static constexpr int kChunks = D / 64;  // of 64 channels: 128 bytes, a swizzled row
   uint8_t q[2][kChunks][kTile * 128];
   uint8_t kv[kStages][kChunks][kTile * 128];
   uint8_t raw[RAW ? kRaw : 1][RAW ? kTile * D : 16];
-  Info<RAW> info[kInfo];
+  Info<EACH> info[kInfo];
   float ml[kTile][2];  // split: b's maximum and sum, for a
   int ml_exp;
   uint64_t todo_full[2], todo_empty[2], info_full[kInfo], info_empty[kInfo], q_full, q_empty, kv_full[kStages], kv_empty[kStages], raw_full[kRaw], raw_empty[kRaw], s_full[2],
@@ -305,16 +306,19 @@ __device__ inline void copy_bulk(uint32_t dst, const void *src, uint32_t bytes, 
                : "memory");
 }
 
-// RAW: pages are a multiple of 16 tokens, so that 16 positions have one scale
-// and lie together: their codes are copied, `chunk` positions (a power of two up
-// to 128 that divides a page) at a time.  Other shapes load them a position and
-// eight channels at a time (a context of 32768 tokens and 16
-// readers in pages of 32: 45 us, of 24: 60 us).
-template <int FMT, int D, bool RAW>
+// EACH positions have one scale and lie together: 16 or 8 where pages are multiples
+// of that, else 1.  With 16 and 8 (RAW) codes are copied, `chunk` positions (a power
+// of two up to 128 that divides a page) at a time; with 1 they are loaded a position
+// and eight channels at a time, and scales are applied on a way of their own (a
+// context of 32768 tokens and 16 readers in pages of 32: 45 us, of 24: 54, of 7: 61).
+template <int FMT, int D, int EACH>
 __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ SharedArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  Smem<D, RAW> &sm = *reinterpret_cast<Smem<D, RAW> *>(smem_raw);
-  constexpr int kChunks = Smem<D, RAW>::kChunks;
+  constexpr bool RAW = EACH > 1;
+  constexpr int kWith = RAW ? EACH : 16;  // positions that the softmax takes together
+  constexpr int kInfo = Smem<D, EACH>::kInfo;
+  Smem<D, EACH> &sm = *reinterpret_cast<Smem<D, EACH> *>(smem_raw);
+  constexpr int kChunks = Smem<D, EACH>::kChunks;
   constexpr uint32_t kTileBytes = kChunks * kTile * 128;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -431,12 +435,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
           if (!more) break;
           const int keys = a.keys[p.g];
           const int32_t *row = a.table + int64_t(a.lead[p.g]) * a.stride;
-          constexpr int kEach = Info<RAW>::kEach, kCount = Info<RAW>::kCount, kMine = (kCount + 31) / 32;
+          constexpr int kCount = Info<EACH>::kCount, kMine = (kCount + 31) / 32;
           int page[kMine], at[kMine];  // of the warp's next tile
           auto look = [&](int j) {
 #pragma unroll
             for (int k = 0; k < kMine; k++) {
-              const int i = 32 * k + lane, tok = (p.j0 + j) * kTile + i * kEach, blk = tok / a.bt;
+              const int i = 32 * k + lane, tok = (p.j0 + j) * kTile + i * EACH, blk = tok / a.bt;
               const bool there = i < kCount && tok < keys;
               at[k] = there ? tok - blk * a.bt : -1;
               page[k] = there ? row[blk] : -1;
@@ -461,17 +465,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
               mine += kLookers;
               if (mine < p.n) look(mine);
               if (!(ok = bar_wait(&sm.info_empty[slot], phase, &sm.dead))) break;
-              Info<RAW> &in = sm.info[slot];
+              Info<EACH> &in = sm.info[slot];
               int whole = 1;
 #pragma unroll
               for (int k = 0; k < kMine; k++) {
                 const int i = 32 * k + lane;
                 const uint32_t valid = __ballot_sync(0xffffffffu, good[k]);
-                whole &= valid == (RAW ? 0xffu : 0xffffffffu);
+                whole &= valid == (kCount < 32 ? (1u << kCount % 32) - 1 : 0xffffffffu);
                 if (i < kCount) in.row[i] = begin[k], in.ks[i] = ks[k], in.vs[i] = vs[k];
                 top = fmaxf(top, fabsf(vs[k]));
                 if (RAW) {
-                  if (lane < 4) in.valid[lane] = (valid >> (2 * lane) & 1 ? 0xffffu : 0) | (valid >> (2 * lane + 1) & 1 ? 0xffff0000u : 0);
+                  constexpr int kBits = 32 / EACH;  // of `valid`, for a word of positions
+                  uint32_t word = 0;
+#pragma unroll
+                  for (int b = 0; b < kBits; b++) word |= (valid >> (kBits * (lane & 3) + b) & 1 ? (1u << EACH % 32) - 1 : 0) << b * EACH;
+                  if (lane < 4) in.valid[lane] = word;
                 } else if (lane == 0) {
                   in.valid[k] = valid;
                 }
@@ -495,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
         auto copy = [&](const uint8_t *pool, int slot, uint32_t phase) {
           if (!(ok = bar_wait(&sm.info_full[slot], phase, &sm.dead))) return;
           if (!(ok = bar_wait(&sm.raw_empty[at], raw_phase, &sm.dead))) return;
-          const int64_t begin = lane < kTile / chunk ? sm.info[slot].row[RAW ? lane * (chunk / 16) : 0] : -1;
+          const int64_t begin = lane < kTile / chunk ? sm.info[slot].row[RAW ? lane * (chunk / EACH) : 0] : -1;
           const uint32_t there = __ballot_sync(0xffffffffu, begin >= 0);
           if (lane == 0) bar_expect(&sm.raw_full[at], __popc(there) * bytes);
           __syncwarp();
@@ -630,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
 #pragma unroll 1
         for (int i = 0; i < 2 * n; i++) {
           const bool is_v = i == 2 * n - 1 || (i > 0 && i % 2 == 0);
-          const Info<RAW> &in = sm.info[is_v ? v_slot : k_slot];
+          const Info<EACH> &in = sm.info[is_v ? v_slot : k_slot];
           if (RAW) {  // (who had the codes copied has seen the tile's pages)
             if (!(ok = bar_wait(&sm.raw_full[at], raw_phase, &sm.dead))) break;
           } else {
@@ -747,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
         int v_exp = 1;  // O is in units of 2^(v_exp - 127), the largest V scale so far
         int done = 0;   // tiles of this thread's
         for (int j = 0; j < n; j++) {
-          const Info<RAW> &in = sm.info[slot];
+          const Info<EACH> &in = sm.info[slot];
           const uint32_t full = info_phase;
           uint64_t *const info_full = &sm.info_full[slot];
           if (++slot == kInfo) slot = 0, info_phase ^= 1;
@@ -785,12 +793,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
 #pragma unroll
           for (int c = 0; c < 4; c++)
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-              auto at = [&](int i) { return __uint_as_float(x[c][16 * h + i]); };
+            for (int h = 0; h < 32 / kWith; h++) {
+              auto at = [&](int i) { return __uint_as_float(x[c][kWith * h + i]); };
               float top[2] = {fmaxf(at(0), at(1)), fmaxf(at(2), at(3))};
 #pragma unroll
-              for (int i = 4; i < 16; i += 4) top[0] = max3(top[0], at(i), at(i + 1)), top[1] = max3(top[1], at(i + 2), at(i + 3));
-              now = fmaxf(now, fmaxf(top[0], top[1]) * scale_of(2 * c + h));
+              for (int i = 4; i < kWith; i += 4) top[0] = max3(top[0], at(i), at(i + 1)), top[1] = max3(top[1], at(i + 2), at(i + 3));
+              now = fmaxf(now, fmaxf(top[0], top[1]) * scale_of(32 / kWith * c + h));
             }
           const bool moved = now > m + kLag;
           const float keep = moved ? ex2(m - now) : 1.0f;
@@ -819,10 +827,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
           for (int c = 0; c < 4; c++) {
             uint32_t pk[16];
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-              const float f = scale_of(2 * c + h), v = RAW ? in.vs[RAW ? 2 * c + h : 0] * unit : 0.0f;
+            for (int h = 0; h < 32 / kWith; h++) {
+              const int group = 32 / kWith * c + h;
+              const float f = scale_of(group), v = RAW ? in.vs[RAW ? group : 0] * unit : 0.0f;
 #pragma unroll
-              for (int i = 8 * h; i < 8 * h + 8; i++) {
+              for (int i = kWith / 2 * h; i < kWith / 2 * (h + 1); i++) {
                 float2 y = make_float2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1]));
                 y = RAW ? fma2(y, make_float2(f, f), make_float2(base, base)) : add2(y, make_float2(base, base));
                 y = make_float2(ex2(y.x), ex2(y.y));
@@ -1075,20 +1084,20 @@ Places places(const cg_cache *c, const cg_attend *t, const cg_groups *g) {
   return w;
 }
 
-template <int FMT, int D, bool RAW>
+template <int FMT, int D, int EACH>
 cudaError_t launch(const SharedArgs &a, cudaStream_t st) {
-  constexpr int kSmem = int(sizeof(Smem<D, RAW>));
+  constexpr int kSmem = int(sizeof(Smem<D, EACH>));
   static_assert(kSmem <= 227 * 1024, "fits in an SM");
-  const cudaError_t e = cudaFuncSetAttribute(k_shared<FMT, D, RAW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const cudaError_t e = cudaFuncSetAttribute(k_shared<FMT, D, EACH>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  return launch_early(k_shared<FMT, D, RAW>, dim3(kGrid), dim3(kThreads), kSmem, st, a);
+  return launch_early(k_shared<FMT, D, EACH>, dim3(kGrid), dim3(kThreads), kSmem, st, a);
 }
 
 template <int FMT>
 cudaError_t launch_format(const SharedArgs &a, cudaStream_t st) {
-  const bool raw = a.bt % 16 == 0;
-  if (a.d <= 64) return raw ? launch<FMT, 64, true>(a, st) : launch<FMT, 64, false>(a, st);
-  return raw ? launch<FMT, 128, true>(a, st) : launch<FMT, 128, false>(a, st);
+  const int each = a.bt % 16 == 0 ? 16 : a.bt % 8 == 0 ? 8 : 1;
+  if (a.d <= 64) return each == 16 ? launch<FMT, 64, 16>(a, st) : each == 8 ? launch<FMT, 64, 8>(a, st) : launch<FMT, 64, 1>(a, st);
+  return each == 16 ? launch<FMT, 128, 16>(a, st) : each == 8 ? launch<FMT, 128, 8>(a, st) : launch<FMT, 128, 1>(a, st);
 }
 
 }  // namespace

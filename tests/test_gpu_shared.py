@@ -140,6 +140,10 @@ CASES = {
     "d40": ("int8", F16, 3, 6, 3, 40, 24, [(12, [3, 49, 3])], [2]),
     "d64": ("e4m3", F16, 1, 16, 2, 64, 32, [(10, [700, 3])], [64]),
     "d72_page_16": ("e4m3", F16, 1, 8, 1, 72, 16, [(33, [3, 4])], []),
+    "page_8": ("e4m3", BF16, 1, 16, 2, 128, 8, [(37, [3, 4, 9])], [17]),
+    "page_24_rows_over_128": ("int8", F16, 1, 32, 1, 128, 24, [(31, [1, 2, 3, 4, 70, 6, 7])], []),
+    "page_40_d64": ("e4m3", F16, 2, 8, 2, 64, 40, [(23, [2, 50, 3]), (3, [2, 9])], [5]),
+    "page_8_d40": ("int8", BF16, 1, 4, 2, 40, 8, [(150, [1, 2])], []),
     "d96": ("e4m3", F16, 1, 40, 2, 96, 16, [(33, [3, 4, 5])], [20]),
     "d120_page_128": ("int8", BF16, 8, 16, 2, 120, 128, [(3, [13, 8, 30])], []),
     "group_7": ("e4m3", F16, 3, 35, 5, 128, 16, [(25, [30, 3])], [61]),
