@@ -211,8 +211,9 @@ cg_status cg_prompt_attend(const cg_prompt *prompt, const void *q_dev, const voi
  * that go on from it (out and lse of such a part can be joined with another
  * part's).  Sequences may share keys.  prompt as at cg_prompt_attend (n_k: rows
  * that k and v have; max_k: no k_len is more), with its workspace, its formulas
- * and its rounding of the probabilities, or a finer one; a row without keys gives out 0, lse
- * -inf.  Keys that a sequence does not see do not matter, whatever they hold.
+ * and its rounding of the probabilities, or a finer one; a row without keys
+ * gives out 0, lse -inf.  Keys that a sequence does not see do not matter,
+ * whatever they hold.
  *   cu_q_dev:               int32 [n_seq + 1], as at cg_prompt_attend;
  *   k_begin_dev, k_len_dev: int32 [n_seq];
  *   out_dev, lse_dev:       as at cg_prompt_attend.
