@@ -369,8 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
   const int skip = most <= 1 && n_items <= gridDim.x ? 0 : 1;  // 0: a CTA per item
   if (!skip) total = n_items, cost = items, cost_to = items_to;
   const int64_t before = cost_to - cost;
-  // no run is shorter than a tile: each has one of every item that goes through it
-  const int64_t ctas = min(int64_t(gridDim.x), skip ? (total + kFull - 1) / kFull : total);
+  // No run is shorter than a tile, so that each has one of every item that goes through
+  // it: the join takes a part from every CTA between those of the first and last tile.
+  const int64_t ctas = min(int64_t(gridDim.x), skip ? total / kFull : total);
   const int64_t lo = ctas ? total * blockIdx.x / ctas : 0, hi = ctas ? total * (blockIdx.x + 1) / ctas : 0;
   const bool busy = int64_t(blockIdx.x) < ctas;
   if (busy && lo >= before && lo < before + cost) {  // one thread's groups hold the first cost

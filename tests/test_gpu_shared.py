@@ -85,11 +85,11 @@ class Setup:
         """What a call takes behind its descriptions: q, pools, scales, table, lengths."""
         return [self.q.cuda(), *(t.cuda() for t in self.pools), *(t.cuda() for t in self.scales), self.table.cuda(), i32(self.lens)]
 
-    def run(self, groups=None, args=None, stream=None, lse=True, q_stride=None):
+    def run(self, groups=None, args=None, stream=None, lse=True, q_stride=None, fill=0xA5):
         cache, att = self.shapes(q_stride)
         groups = self.groups() if groups is None else groups
         ws = cg.empty_u8(cg.cg_shared_workspace_bytes(cache, att, groups))
-        ws.fill_(0xA5)  # a workspace may hold anything
+        ws.fill_(fill)  # a workspace may hold anything
         out = torch.full(self.q.shape, math.nan, dtype=self.q.dtype, device="cuda")
         z = torch.full(self.q.shape[:3], math.nan, device="cuda") if lse else None
         args = self.on_gpu() if args is None else args
@@ -166,6 +166,27 @@ def test_shared(name):
     n = len(s.lens)
     s.check(out, z, range(0, n, 9) if n > 60 else None)
     assert torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("name", list(CASES))
+def test_what_the_workspace_held_does_not_matter(name):
+    """0xff bytes are NaN as floats: a part that nothing has written shows in the results."""
+    fmt, dt, T, Hq, H, d, bt, groups, loose = CASES[name]
+    s = Setup(fmt, dt, T, Hq, H, d, bt, groups, loose, seed=len(name))
+    args = s.on_gpu()
+    (out, z, st), (want, zw, _) = s.run(None, args, fill=0xFF), s.run(None, args)
+    assert st == cg.CG_OK and torch.equal(out, want) and torch.equal(z, zw)
+
+
+@pytest.mark.parametrize("pages", [3, 4, 5, 6, 17, 18, 30, 31, 32, 33, 34])
+@pytest.mark.parametrize("readers,H", [(17, 1), (20, 3), (33, 1), (48, 1)])
+def test_little_work_in_runs_of_odd_lengths(pages, readers, H):
+    """Blocks of 256 rows and of up to 128 behind one another, less work than every CTA could have: 8 rows a reader and KV head, a tile a page."""
+    s = Setup("int8", BF16, 1, 8 * H, H, 40, 128, [(pages, [i % 3 for i in range(readers)])], seed=pages)
+    out, z, st = s.run(fill=0xFF)
+    assert st == cg.CG_OK
+    s.check(out, z, range(0, readers, 11))
+    assert torch.isfinite(out).all() and torch.isfinite(z).all()
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
