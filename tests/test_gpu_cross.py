@@ -29,7 +29,7 @@ def run(q, k, v, cu_q, begin, count, scale, max_q=None, max_k=None, lse=True, st
     p = cg.Prompt(len(cu_q) - 1, Hq, H, d, DT[q.dtype], n_q, n_k, max([b - a for a, b in zip(cu_q, cu_q[1:])]) if max_q is None else max_q,
                   max(count) if max_k is None else max_k, scale, q.stride()[:2], k.stride()[:2], v.stride()[:2])
     ws = cg.empty_u8(cg.cg_prompt_workspace_bytes(p))
-    ws.fill_(0xA5)  # a workspace may hold anything
+    ws.fill_(0xFF)  # a workspace may hold anything, NaN among it
     out = torch.full((n_q, Hq, d), math.nan, dtype=q.dtype, device="cuda")
     z = torch.full((n_q, Hq), math.nan, device="cuda") if lse else None
     args = i32(cu_q), i32(begin), i32(count)

@@ -23,7 +23,7 @@ def book(table, lens, n_blocks, bt):
     cache = cg.Cache(1, 2, 16, bt, n_blocks, cg.CG_CACHE_INT8)
     pages = cg.Pages(torch.zeros(n_blocks, dtype=torch.int32, device="cuda"), i32(table), i32(lens))
     ws = cg.empty_u8(cg.cg_pages_workspace_bytes(cache, pages, len(lens)))
-    ws.fill_(0xA5)
+    ws.fill_(0xFF)
     return cache, pages, ws
 
 
