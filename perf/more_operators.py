@@ -408,10 +408,10 @@ def _make_pages(cg, s, c):
     cache = cg.Cache(1, c["kv_heads"], c["d"], c["page"], s["n_blocks"], cg.CG_CACHE_E4M3)
     pages = cg.Pages(s["refs"], s["table"], s["lens"])
     n = s["table"].shape[0]
-    sizes = (n // 2 + 1, n, n // 2) if c["op"] == "groups" else (n + 1, n, s["n_rows"], s["n_rows"])
-    got = [torch.empty(k, dtype=torch.int32, device="cuda") for k in sizes]
-    if c["op"] == "slots":
-        got.append(torch.empty(s["n_rows"], dtype=torch.int64, device="cuda"))
+    if c["op"] == "groups":
+        got = [_ints([0] * k) for k in (n // 2 + 1, n, n // 2)]
+    else:
+        got = [_ints([0] * k) for k in (n + 1, n, s["n_rows"], s["n_rows"])] + [torch.zeros(s["n_rows"], dtype=torch.int64, device="cuda")]
     return cg, cache, pages, got, cg.empty_u8(cg.cg_pages_workspace_bytes(cache, pages, n))
 
 
