@@ -33,8 +33,8 @@
  *     and H up to 32767.
  *   - Scales of pages are not negative; that of a page whose rows
  *     cg_cache_write adds to is 0 or at least 2^-100, as it writes them.
- *     In the attention calls a value of V times the number of positions stays
- *     under 2^112: sums of weights up to 2^15 are taken in fp32.
+ *     In the attention calls a finite value of V times the number of positions
+ *     stays under 2^112: sums of weights up to 2^15 are taken in fp32.
  *   - An array without entries (rows, ids of a call for none) may be NULL.
  *   - The attention calls' waits for their own copies and products are
  *     bounded (about two seconds); a wait that runs out reports
@@ -194,8 +194,11 @@ size_t cg_prompt_workspace_bytes(const cg_prompt *prompt);
  * see nothing and give out 0, lse -inf).  Formulas as at cg_cache_attend.
  * Rows of other sequences, and keys that a row does not see, do not matter,
  * whatever they hold.  Probabilities are rounded to the type of the rows for
- * the second product.  A call on the same inputs gives the same bits every
- * time; the bits of a sequence may depend on the lengths of the others.
+ * the second product.  An infinite value of v that a row sees makes its output
+ * infinite (NaN beside one of the other sign) as long as its weight is at least
+ * 2^-30 (f16) or 2^-110 (bf16) of the row's largest; under that it may be NaN.
+ * A call on the same inputs gives the same bits every time; the bits of a
+ * sequence may depend on the lengths of the others.
  *   out_dev: [n_q][Hq][d], contiguous;  lse_dev: fp32 [n_q][Hq], or NULL;
  *   rows of q outside every sequence get no output.
  * Device errors: CG_ERR_INVALID_ARG (offsets that fall, pass n_q or n_k, or

@@ -5,8 +5,8 @@
 // matrix.  Both products are taken transposed on mma.sync m16n8k16, S^T = K Q^T
 // and O^T = V^T P^T, so that positions and channels fill the side of 16 and
 // eight rows waste nothing.  P goes into the second product as two values of the
-// rows' type, so that a weight is off by at most 2^-16 (bf16) or 2^-21 (f16) of
-// itself, or by f16's least step: 2^-31 of the largest.
+// rows' type, so that a weight is off by at most 2^-16 (bf16) or 2^-20 (f16) of
+// itself, or by half of f16's least step: 2^-32 of the largest.
 //
 // What bounds it is the read of the keys and values.  A warp works by itself: it
 // has tiles of 32 positions copied (TMA) two tiles ahead, a running maximum, sum
@@ -331,9 +331,15 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_few(const __grid_cons
       }
       // P^T as an operand, and what it leaves over: the tensor cores have the time.  It
       // is taken a little less than it is, so that the rest is above 0 where P is, too,
-      // and an infinite value of V stays what it is.
+      // and an infinite value of V stays what it is.  In f16 a P under kHalved is
+      // subnormal, or nearly: a little less may round to P itself, and it is taken in
+      // halves (off by 2^-25 either way; both are above 0 where P is above 2^-23).
       uint32_t p[2][NB][2], rest[2][NB][2];
-      const float2 less = BF16 ? make_float2(1.0f - 0x1p-8f, 1.0f - 0x1p-8f) : make_float2(1.0f - 0x1p-10f, 1.0f - 0x1p-10f);
+      constexpr float kLess = BF16 ? 1.0f - 0x1p-8f : 1.0f - 0x1p-10f, kHalved = 0x1p-13f;
+      auto less = [&](float2 y) {
+        const float2 f = make_float2(!BF16 && y.x < kHalved ? 0.5f : kLess, !BF16 && y.y < kHalved ? 0.5f : kLess);
+        return mul2(y, f);
+      };
       const float2 sl = make_float2(a.scale_log2, a.scale_log2);
 #pragma unroll
       for (int n = 0; n < NB; n++) {
@@ -345,7 +351,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_few(const __grid_cons
             float2 y = fma2(make_float2(x[tt][n][2 * half], x[tt][n][2 * half + 1]), sl, base);
             y = make_float2(ex2(y.x), ex2(y.y));
             sum[n] = add2(sum[n], y);
-            const float2 z = mul2(y, less);
+            const float2 z = less(y);
             const uint32_t w = pack<BF16>(z.x, z.y);
             p[tt][n][half] = transposed(w);
             rest[tt][n][half] = transposed(pack<BF16>(y.x - elem<BF16>(uint16_t(w)), y.y - elem<BF16>(uint16_t(w >> 16))));
