@@ -299,6 +299,13 @@ __device__ inline void tm_load16(uint32_t addr, uint32_t (&x)[16]) {
                : "memory");
 }
 
+// The larger of two values, or NaN where one of them is.
+__device__ inline float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 // Copies `bytes`, a multiple of 16, to shared memory.
 __device__ inline void copy_bulk(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
   asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
@@ -783,8 +790,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
             tm_wait_st();
           }
           // What turns a product into a score: a page's scale times the row's.  It is
-          // not 0, so that what is masked stays at -inf (a page's codes are 0 where its scale is).
-          auto scale_of = [&](int i) { return RAW ? fmaxf(in.ks[RAW ? i : 0] * sc, 0x1p-126f) : 1.0f; };
+          // not 0, so that what is masked stays at -inf (a page's codes are 0 where its scale is);
+          // a NaN stays one.
+          auto scale_of = [&](int i) { return RAW ? max_nan(in.ks[RAW ? i : 0] * sc, 0x1p-126f) : 1.0f; };
           uint32_t x[4][32];
 #pragma unroll
           for (int c = 0; c < 4; c++) tm_load(s_at + 32 * c, x[c]);

@@ -8,6 +8,7 @@ from kv_cache_compression_02_gb300 import cachegen as cg
 from tests import gpu_util as gu
 from tests import test_gpu_cross as cross
 from tests import test_gpu_prompt as prompt
+from tests import test_gpu_shared as shared
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +58,19 @@ def test_infinite_values_under_small_weights_of_a_prompt(dt, n, d):
     out, z, st = prompt.run(q.cuda(), k.cuda(), v.cuda(), [0, n], [0, 2 * d + n], 1.0)
     assert st == cg.CG_OK and torch.isfinite(z).all()
     assert torch.equal(out.float().cpu(), sign.expand(n, 2, d))
+
+
+@pytest.mark.parametrize("bt", [16, 64, 8, 7])
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_a_scale_that_is_nan_reaches_the_readers_of_its_page(fmt, which, bt):
+    """K's scale (0) makes outputs and lse of its head NaN, V's (1) the outputs, for those who read the page and for no others, whatever the page size."""
+    s = shared.Setup(fmt, BF16, 1, 16, 2, 128, bt, [(300 // bt, [5, 20, 3]), (160 // bt, [1, 2])], [30], seed=11 + bt)
+    s.scales[which][s.table[s.members[0][0], 1].long(), 1] = math.nan
+    out, z, st = s.run(fill=0xFF)
+    assert st == cg.CG_OK
+    hit = torch.zeros(len(s.lens), dtype=torch.bool)
+    hit[s.members[0]] = True
+    assert torch.isnan(out[hit.cuda(), :, 8:]).all() and torch.isfinite(out[hit.cuda(), :, :8]).all() and torch.isfinite(out[~hit.cuda()]).all()
+    assert torch.equal(torch.isnan(z).cpu(), (hit[:, None, None] & (torch.arange(16) >= 8)) if which == 0 else torch.zeros(z.shape, dtype=torch.bool))
+    s.check(out, z)
