@@ -3,11 +3,11 @@
 A context's KV (synthetic, from :mod:`.synth`) is fitted, encoded and decoded by the codec into a buffer with room for
 a question.  Each layer of the decoded context goes into 8-bit pages (cg_pages_extend, cg_cache_write); a question is
 run against the decoded fp16 keys (cg_prompt_attend) and its own keys join the pages; three readers branch off it
-(cg_pages_fork) and generate a few tokens each (cg_pages_extend, cg_pages_slots, cg_cache_write, cg_pages_groups,
-cg_shared_attend: the context that they share is read once for all of them); another look at the context alone is taken
-by rows that are no part of it (cg_cross_attend); two readers are dropped (cg_pages_free), the cache is compacted
-(cg_pages_compact) and the last one attends by itself (cg_cache_attend).  Queries, keys and values of the new tokens are
-random rows: there is no model here, only what a server does around one.
+(cg_pages_fork, cg_pages_groups) and generate a few tokens each (cg_pages_extend, cg_pages_slots, cg_cache_write and, where
+the context that they share is long enough, cg_shared_attend, which reads it once for all of them, else cg_cache_attend);
+another look at the context alone is taken by rows that are no part of it (cg_cross_attend); two readers are dropped
+(cg_pages_free), the cache is compacted (cg_pages_compact) and the last one attends by itself (cg_cache_attend).  Queries,
+keys and values of the new tokens are random rows: there is no model here, only what a server does around one.
 """
 from __future__ import annotations
 
@@ -16,8 +16,12 @@ import math
 import numpy as np
 
 
-def run(L=2, H=2, G=4, S=1500, question=37, steps=5, block_tokens=16, fmt=None, seed=0, verbose=True):
-    """-> a dict with what the calls produced, for a caller that wants to check it."""
+SHARING_PAYS = 500_000  # positions of KV heads that are not read again, from which cg_shared_attend is faster than cg_cache_attend
+
+
+def run(L=2, H=2, G=4, S=1500, question=37, steps=5, block_tokens=16, fmt=None, seed=0, share=None, verbose=True):
+    """-> a dict with what the calls produced, for a caller that wants to check it.  share: whether the readers attend by
+    cg_shared_attend (None: where it pays)."""
     import torch
 
     from . import cachegen as cg, synth
@@ -91,14 +95,19 @@ def run(L=2, H=2, G=4, S=1500, question=37, steps=5, block_tokens=16, fmt=None, 
     new, cu, start, wsr = i32([0, 1, 1, 1]), i32([0] * (n_seqs + 1)), i32([0] * n_seqs), cg.empty_u8(256)
     groups = cg.Groups(i32([0] * (n_seqs // 2 + 1)), i32([0] * n_seqs), i32([0] * (n_seqs // 2)))
     wsg = cg.empty_u8(cg.cg_pages_workspace_bytes(cache, pages, n_seqs))
-    wsa = cg.empty_u8(cg.cg_shared_workspace_bytes(cache, att, groups))
+    # who shares what stays as it is while they generate: it is found once and looked at once, to see whether sharing pays
+    done(cg.cg_pages_groups(cache, pages, max(1, S // block_tokens // 2), *groups.tensors, wsg), "groups", wsg)
+    cu_group, _, shared = (t.tolist() for t in groups.tensors)
+    saved = sum((b - a - 1) * n for a, b, n in zip(cu_group, cu_group[1:], shared)) * block_tokens * H
+    share = saved >= SHARING_PAYS if share is None else share
+    wsa = cg.empty_u8(cg.cg_shared_workspace_bytes(cache, att, groups) if share else cg.cg_cache_workspace_bytes(cache, att))
     k_pool, v_pool, k_scale, v_scale = pools[L - 1, 0], pools[L - 1, 1], scales[L - 1, 0], scales[L - 1, 1]
     for s in range(steps):
         done(cg.cg_pages_extend(cache, pages, ids, lens[1:] + 1, ws), "extend", ws)
         done(cg.cg_pages_slots(cache, pages, readers, new, cu, start, None, None, None, wsr), "slots", wsr)
         done(cg.cg_cache_write(cache, one, new_k[s], new_v[s], cu, start, table, k_pool, v_pool, k_scale, v_scale, wsw), "write", wsw)
-        done(cg.cg_pages_groups(cache, pages, max(1, S // block_tokens // 2), *groups.tensors, wsg), "groups", wsg)
-        done(cg.cg_shared_attend(cache, att, groups, new_q[s], k_pool, v_pool, k_scale, v_scale, table, lens, outs[s], lse[s], wsa), "attend", wsa)
+        what = (new_q[s], k_pool, v_pool, k_scale, v_scale, table, lens, outs[s], lse[s], wsa)
+        done(cg.cg_shared_attend(cache, att, groups, *what) if share else cg.cg_cache_attend(cache, att, *what), "attend", wsa)
 
     # two readers leave; the pages that are left move to the front
     used = int((refs > 0).sum())
@@ -111,8 +120,8 @@ def run(L=2, H=2, G=4, S=1500, question=37, steps=5, block_tokens=16, fmt=None, 
         fp16 = context.numel() * 2
         print(f"context of {S} tokens: {int(nbytes.item())} bytes on the wire; {n_tok} tokens in {int(n_live.item())} of {n_blocks} pages after "
               f"compaction ({used} with three readers), {pools.element_size() * 8}-bit codes of {fp16} bytes of fp16")
-    return dict(context=context, q=q, answer=answer, look=look, look_lse=look_lse, groups=groups, new_q=new_q, new_k=new_k, new_v=new_v, outs=outs, lse=lse, again=again, used=used,
-                n_live=int(n_live.item()), refs=refs, table=table, lens=lens, pools=pools, scales=scales)
+    return dict(context=context, q=q, answer=answer, look=look, look_lse=look_lse, groups=groups, share=share, new_q=new_q, new_k=new_k, new_v=new_v, outs=outs,
+                lse=lse, again=again, used=used, n_live=int(n_live.item()), refs=refs, table=table, lens=lens, pools=pools, scales=scales)
 
 
 if __name__ == "__main__":
