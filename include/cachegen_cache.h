@@ -221,7 +221,9 @@ cg_status cg_prompt_attend(const cg_prompt *prompt, const void *q_dev, const voi
  * that k and v have; max_k: no k_len is more), with its workspace, its formulas
  * and its rounding of the probabilities, or a finer one; a row without keys
  * gives out 0, lse -inf.  Keys that a sequence does not see do not matter,
- * whatever they hold.
+ * whatever they hold.  Where max_q * Hq / H is at most 16 the call goes to a kernel
+ * for few rows, with the finer rounding (64 sequences of one query: 28 us, else
+ * 66): a decoder's step should give the max_q that it has.
  *   cu_q_dev:               int32 [n_seq + 1], as at cg_prompt_attend;
  *   k_begin_dev, k_len_dev: int32 [n_seq];
  *   out_dev, lse_dev:       as at cg_prompt_attend.

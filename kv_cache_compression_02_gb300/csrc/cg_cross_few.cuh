@@ -9,8 +9,8 @@ namespace cg {
 
 // Up to this many rows (queries x Hq / H) the keys are what is to be moved, and
 // tiles of 128 rows would be nearly empty: 64 sequences of one query and 16
-// heads on 100 to 1500 keys take 27 us here, 68 us on those; 40 of up to 12 rows
-// on 333 to 901 keys 16 us and 27 us.
+// heads on 100 to 1500 keys take 28 us here, 66 us on those; 40 of up to 12 rows
+// on 333 to 901 keys 14.6 us and 25.7 us (ten calls in a graph).
 constexpr int kFewRows = 16;
 
 uint64_t few_bytes(const cg_prompt &p);  // of the workspace

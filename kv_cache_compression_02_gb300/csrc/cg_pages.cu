@@ -370,7 +370,7 @@ __device__ inline bool slot_row(const SlotArgs &a, const int32_t *cu, int total,
 }
 
 // Offsets and first positions, by one CTA.  ALL: the rows, too, as long as they
-// are few: 64 rows take 3.3 us in one kernel, 4.1 us in two.
+// are few: 64 rows take 3.2 us in one kernel, 4.7 us in two.
 constexpr int kFewRows = 4096, kFewSeqs = 2048;
 
 template <bool ALL>
@@ -492,8 +492,8 @@ __global__ void __launch_bounds__(kPlan) k_groups_plan(const GroupArgs a) {
 }
 
 // The same for up to kFew sequences: each looks through the others' pages in
-// shared memory (the call with 67 sequences 5.0 us, with the plan above 6.5 us;
-// with 265 of them 10.3 and 8.5 us).
+// shared memory (the call with 67 sequences 5.1 us, with the plan above 6.6 us;
+// with 265 of them 10.3 and 8.4 us).
 constexpr int kFew = 128;  // sequences
 
 __global__ void __launch_bounds__(kPlan) k_groups_few(const GroupArgs a) {

@@ -312,7 +312,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
   if (!skip) total = n_items, cost = items, cost_to = items_to;
   const int64_t before = cost_to - cost;
   if (blockIdx.x == 0 && bad) atomicOr(&sm.errors, kStBadArg);
-  // no run is shorter than a key tile: each has one of every item that goes through it
+  // No run but the first is shorter than a key tile, so that each has one of every item
+  // that goes through it: the join takes a part from every CTA between those of the first
+  // and last tile.  (Rounded up, an odd total leaves the first run one unit of cost; that
+  // lies in the first item's way in, where no tile begins.)
   int64_t ctas = min(int64_t(gridDim.x), skip ? (total + kTileCost - 1) / kTileCost : total);
   if (skip) ctas = aligned_runs(ctas, n_items, total, int64_t(most) * kTileCost + kIn);
   const int64_t lo = ctas ? total * blockIdx.x / ctas : 0, hi = ctas ? total * (blockIdx.x + 1) / ctas : 0;

@@ -14,7 +14,11 @@
 // of two above the largest scale so far (O is scaled when that grows).  P is
 // rounded to f16: a weight is off by at most 2^-11 of itself or 2^-31 of the
 // largest times the largest scale, whichever is more (the largest has at least
-// 2^7, and half of the spacing of f16's subnormals is 2^-25).
+// 2^7, and half of the spacing of f16's subnormals is 2^-25).  What the rounding
+// leaves would take a product of its own, as in cg_cache_attend: built so, in the
+// columns that S leaves free, the two calls below take 145 us each, not 109 and
+// 103.  Outputs against 64 bits, relative: f16 3.0e-4 (a 32-bit form rounded once
+// 2.1e-4), bf16 1.7e-3 as that form.
 //
 // A CTA has two tiles of rows, a and b, whose softmax warpgroups take turns with
 // the products; where an item has up to 128 rows, a and b are the same rows
@@ -39,8 +43,8 @@
 // prefix takes 71 (0.97 PFLOP/s; 27 tiles of 256 rows a CTA at 2.1 us, 10 us of
 // set-up); without sharing 698 us.  16 readers of 131072 tokens, int8: 103
 // us (2.6 TB/s of distinct codes).  The roles of a scheduler's four warps differ,
-// so that their code has to fit its instruction cache together: loops that were
-// unrolled whole took 147 and 192 us.
+// so that their code has to fit its instruction cache together: with loops unrolled
+// whole the two calls took 155 and 182 us where they then took 115 and 109.
 #include "cg_shared.cuh"
 
 #include "cg_cache.cuh"
@@ -61,8 +65,8 @@ constexpr int kRaw = 4;      // tiles of codes
 constexpr int kLookers = 2;  // warps that look them up
 constexpr int kPlan = 1024;
 // p = 2^(s - m + kLift) < 2^15, m at most kLag under the maximum.  The parts that
-// these are joined with have kOwnLift.  (With 12 and 3 here O is scaled so often
-// that 64 readers of 32768 tokens take 155 us, not 150.)
+// these are joined with have kOwnLift.  (With 12 and 3 here O is scaled more often:
+// 64 readers of 32768 tokens take 115.5 us, with 7 and 8 112, back to back.)
 constexpr float kLift = 7.0f, kLag = 8.0f, kOwnLift = 12.0f;
 // What an item costs: kIn for its way in and out, and for each tile of positions.
 constexpr int kIn = 10, kFull = 4, kSplit = 2;
