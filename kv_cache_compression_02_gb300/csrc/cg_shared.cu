@@ -16,9 +16,9 @@
 // largest times the largest scale, whichever is more (the largest has at least
 // 2^7, and half of the spacing of f16's subnormals is 2^-25).  What the rounding
 // leaves would take a product of its own, as in cg_cache_attend: built so, in the
-// columns that S leaves free, the two calls below take 145 us each, not 109 and
-// 103.  Outputs against 64 bits, relative: f16 3.0e-4 (a 32-bit form rounded once
-// 2.1e-4), bf16 1.7e-3 as that form.
+// columns that S leaves free, the two calls below take 145 us each back to back, not
+// 112 and 106.  Outputs against 64 bits, relative: f16 3.0e-4 (a 32-bit form
+// rounded once 2.1e-4), bf16 1.7e-3 as that form.
 //
 // A CTA has two tiles of rows, a and b, whose softmax warpgroups take turns with
 // the products; where an item has up to 128 rows, a and b are the same rows
