@@ -19,7 +19,7 @@ import numpy as np
 SHARING_PAYS = 500_000  # positions of KV heads that are not read again, from which cg_shared_attend is faster than cg_cache_attend
 
 
-def run(L=2, H=2, G=4, S=1500, question=37, steps=5, block_tokens=16, fmt=None, seed=0, share=None, verbose=True):
+def run(L=2, H=2, G=4, S=1500, question=37, steps=5, block_tokens=16, fmt=None, seed=0, verbose=True, share=None):
     """-> a dict with what the calls produced, for a caller that wants to check it.  share: whether the readers attend by
     cg_shared_attend (None: where it pays)."""
     import torch
